@@ -74,6 +74,21 @@ def lib():
         L.unpack_fp8.argtypes = [P, P, P, P, P, P]
         L.bfz_e4m3_encode.argtypes = [P, P, i64, P]
         L.bfz_transpose_pow2.argtypes = [P, P, P, P, P, P]
+        f64, f32 = C.c_double, C.c_float
+        L.bfz_adamw_fp8_step_clip.argtypes = [P, P, P, P, P, P, i64, A, O, P, P]
+        L.bfz_fold_adamw_fp8_step_clip.argtypes = [P, P, P, P, P, P, P, A, O, P, P]
+        L.bfz_fold_adamw_fp8_step_unpack_clip.argtypes = [P, P, P, P, P, P, P, P, P, A, O, P, P]
+        L.bfz_fold_adamw_fp8_step_unpack_t_clip.argtypes = [P, P, P, P, P, P, P, P, P, P, P, A, O, P, P]
+        L.bfz_norm_work_bytes.argtypes = []
+        L.bfz_norm_work_bytes.restype = i64
+        L.bfz_grad_norm.argtypes = [P, i32, f64, P, P, P, P, P]
+        L.bfz_shard_grad_norm.argtypes = [P, P, f64, P, P, P, P, P]
+        L.bfz_clip_coef.argtypes = [P, f64, P, P, P]
+        L.bfz_clip_grads.argtypes = [P, P, i32, P, P]
+        L.bfz_embed.argtypes = [P, i32, i64, P, i32, P, i64, i64, i64, f32, P, i32, i64, P]
+        L.bfz_embed_grad_work_bytes.argtypes = [i64, i64]
+        L.bfz_embed_grad_work_bytes.restype = i64
+        L.bfz_embed_grad.argtypes = [P, i32, i64, P, i32, i64, i64, i64, f32, i32, P, i32, i64, P, P]
         L.bfz_last_error.argtypes = []
         L.bfz_last_error.restype = C.c_char_p
         _lib = L
@@ -119,6 +134,23 @@ def _tile_array(t, q, name):
             raise ValueError(f"{name}: needs at least {q * TILE_ELEMS} elements, has {t.numel()}")
         return C.c_void_p(t.data_ptr()), TILE_ELEMS
     raise TypeError(f"{name}: need a contiguous tensor or a (tiles, 16384) view of unit inner stride")
+
+
+def _scalar(t, name, dtype=None):
+    """Pointer of a one-element device tensor (float32 unless dtype says)."""
+    import torch
+    p = _dev(t, dtype or torch.float32, name, 1)
+    if t.numel() != 1:
+        raise ValueError(f"{name}: needs one element, has {t.numel()}")
+    return p
+
+
+def _clip(name, grad_scale):
+    """A step's entry point and its extra argument: with a grad_scale the
+    bfz_..._clip form."""
+    if grad_scale is None:
+        return name, ()
+    return f"bfz_{name}_clip", (_scalar(grad_scale, "grad_scale"),)
 
 
 def _hparams(hp):
@@ -274,13 +306,15 @@ def pack_shard_strided(plan: Plan, srcs, dst, dst_stride, stream=None):
 
 
 def adamw_fp8_step(master, grad, m, v, codes, scale_inv, hp, n_tiles=None, scale_pow2=False,
-                   stream=None):
+                   stream=None, grad_scale=None):
     """Fused AdamW + per-tile E4M3 requant over n_tiles whole tiles (default:
     all of master).  hp: AdamW, or a dict of its fields.  master / m / v:
     contiguous, or (tiles, 16384) views with a common tile stride (the
     interleaved layout: state[:, 0], state[:, 1], state[:, 2] of a
     (q, 3, 16384) tensor).  Plain scales on three tile-major arrays call
-    adamw_fp8_step itself; anything else adamw_fp8_step_ex."""
+    adamw_fp8_step itself; anything else adamw_fp8_step_ex.
+    grad_scale: a float32 device scalar that the gradient is multiplied by as
+    it is read (grad_norm's coef; bfz_adamw_fp8_step_clip)."""
     import torch
     if n_tiles is None:
         if master.dim() == 2 and master.shape[1] == TILE_ELEMS:
@@ -294,16 +328,20 @@ def adamw_fp8_step(master, grad, m, v, codes, scale_inv, hp, n_tiles=None, scale
     args = [p, _dev(grad, torch.float32, "grad", n), mm, vv,
             _dev(codes, torch.uint8, "codes", n), _dev(scale_inv, torch.float32, "scale_inv", n_tiles)]
     hp = _hparams(hp)
-    if opts.scale_pow2 == 0 and opts.state_stride == 0:
+    if grad_scale is not None:
+        _check(lib().bfz_adamw_fp8_step_clip(*args, n_tiles, C.byref(hp), C.byref(opts),
+                                             _scalar(grad_scale, "grad_scale"), _stream(stream)))
+    elif opts.scale_pow2 == 0 and opts.state_stride == 0:
         _check(lib().adamw_fp8_step(*args, n_tiles, C.byref(hp), _stream(stream)))
     else:
         _check(lib().adamw_fp8_step_ex(*args, n_tiles, C.byref(hp), C.byref(opts), _stream(stream)))
 
 
 def fold_adamw_fp8_step(plan: Plan, grads, master, m, v, codes, scale_inv, hp, scale_pow2=False,
-                        stream=None):
+                        stream=None, grad_scale=None):
     """pack_shard of the row-major gradients grads[p] and adamw_fp8_step over
-    the whole shard in one pass (the folded gradient is never stored)."""
+    the whole shard in one pass (the folded gradient is never stored).
+    grad_scale: a float32 device scalar the gradient is multiplied by."""
     import torch
     arr = _ptr_array(grads, torch.float32, "grads", _weight_sizes(plan))
     q = plan.shard_tiles
@@ -311,14 +349,16 @@ def fold_adamw_fp8_step(plan: Plan, grads, master, m, v, codes, scale_inv, hp, s
     (p, mm, vv), opts = _state(master, m, v, q, scale_pow2)
     args = [p, mm, vv, _dev(codes, torch.uint8, "codes", n),
             _dev(scale_inv, torch.float32, "scale_inv", q)]
-    _check(lib().fold_adamw_fp8_step(plan.handle, C.cast(arr, C.c_void_p), *args,
-                                     C.byref(_hparams(hp)), C.byref(opts), _stream(stream)))
+    name, scale = _clip("fold_adamw_fp8_step", grad_scale)
+    _check(getattr(lib(), name)(plan.handle, C.cast(arr, C.c_void_p), *args,
+                                C.byref(_hparams(hp)), C.byref(opts), *scale, _stream(stream)))
 
 
 def fold_adamw_fp8_step_unpack(plan: Plan, grads, master, m, v, codes, scale_inv, dst_fp8,
-                               dst_scale, hp, scale_pow2=False, stream=None):
+                               dst_scale, hp, scale_pow2=False, stream=None, grad_scale=None):
     """fold_adamw_fp8_step and unpack_fp8 in one pass.  codes / scale_inv may
-    both be None (no tile-major copy of the codes)."""
+    both be None (no tile-major copy of the codes).  grad_scale: a float32
+    device scalar the gradient is multiplied by."""
     import torch
     if (codes is None) != (scale_inv is None):
         raise ValueError("codes and scale_inv: give both or neither")
@@ -329,17 +369,19 @@ def fold_adamw_fp8_step_unpack(plan: Plan, grads, master, m, v, codes, scale_inv
     c = None if codes is None else _dev(codes, torch.uint8, "codes", q * TILE_ELEMS)
     sc = None if scale_inv is None else _dev(scale_inv, torch.float32, "scale_inv", q)
     (p, mm, vv), opts = _state(master, m, v, q, scale_pow2)
-    _check(lib().fold_adamw_fp8_step_unpack(
+    name, scale = _clip("fold_adamw_fp8_step_unpack", grad_scale)
+    _check(getattr(lib(), name)(
         plan.handle, C.cast(g, C.c_void_p), p, mm, vv, c, sc, C.cast(a8, C.c_void_p),
-        C.cast(asc, C.c_void_p), C.byref(_hparams(hp)), C.byref(opts), _stream(stream)))
+        C.cast(asc, C.c_void_p), C.byref(_hparams(hp)), C.byref(opts), *scale, _stream(stream)))
 
 
 def fold_adamw_fp8_step_unpack_t(plan: Plan, grads, master, m, v, codes, scale_inv, dst_fp8,
-                                 dst_scale, dst_t, dst_t_scale, hp, stream=None):
+                                 dst_scale, dst_t, dst_t_scale, hp, stream=None, grad_scale=None):
     """fold_adamw_fp8_step_unpack with power-of-two scales plus the transposed
     copy (dst_t[p] uint8 (E, W, H), dst_t_scale[p] float32 (E, W, ceil(H/128)))
     in one pass (power-of-two scales are implied); codes / scale_inv may
-    both be None."""
+    both be None.  grad_scale: a float32 device scalar the gradient is
+    multiplied by."""
     import torch
     if (codes is None) != (scale_inv is None):
         raise ValueError("codes and scale_inv: give both or neither")
@@ -352,10 +394,11 @@ def fold_adamw_fp8_step_unpack_t(plan: Plan, grads, master, m, v, codes, scale_i
     c = None if codes is None else _dev(codes, torch.uint8, "codes", q * TILE_ELEMS)
     sc = None if scale_inv is None else _dev(scale_inv, torch.float32, "scale_inv", q)
     (p, mm, vv), opts = _state(master, m, v, q, True)
-    _check(lib().fold_adamw_fp8_step_unpack_t(
+    name, scale = _clip("fold_adamw_fp8_step_unpack_t", grad_scale)
+    _check(getattr(lib(), name)(
         plan.handle, C.cast(g, C.c_void_p), p, mm, vv, c, sc, C.cast(a8, C.c_void_p),
         C.cast(asc, C.c_void_p), C.cast(t8, C.c_void_p), C.cast(tsc, C.c_void_p),
-        C.byref(_hparams(hp)), C.byref(opts), _stream(stream)))
+        C.byref(_hparams(hp)), C.byref(opts), *scale, _stream(stream)))
 
 
 def unpack_fp8(plan: Plan, codes, scale_inv, dst_fp8, dst_scale, stream=None):
@@ -389,3 +432,7 @@ def e4m3_encode(x, out, stream=None):
     n = x.numel()
     _check(lib().bfz_e4m3_encode(_dev(x, torch.float32, "x"), _dev(out, torch.uint8, "out", n), n,
                                  _stream(stream)))
+
+
+from .norm import clip_coef, clip_grads, grad_norm, norm_workspace, shard_grad_norm  # noqa: E402
+from .embedding import embed, embed_grad, embed_grad_workspace  # noqa: E402

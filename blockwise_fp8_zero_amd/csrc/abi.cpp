@@ -23,6 +23,8 @@ int hip_fail(const char* where, int err) {
 // 32-bit number: at most this many tiles per launch.
 constexpr int64_t kMaxLaunchTiles = (int64_t(1) << 32) / 1024 - 1;
 
+}  // namespace
+
 // The plan's tile table lives on the device it was uploaded to: a call made
 // with another device current would hand that device a foreign pointer.
 int check_plan(const bfz_plan* plan, const char* where) {
@@ -51,8 +53,6 @@ int check_weights(const bfz_plan* plan, const void* const* ptrs, const char* whe
                             where, w);
     return BFZ_OK;
 }
-
-}  // namespace
 
 int fail(int code, const char* fmt, ...) {
     va_list ap;
@@ -175,6 +175,7 @@ int make_scalars(const bfz_adamw* hp, const bfz_step_options* opts, StepScalars*
     s->decay = float(lr * wd);
     s->has_decay = wd != 0.0;
     s->pow2 = opts->scale_pow2 != 0;
+    s->grad_scale = nullptr;
     return BFZ_OK;
 }
 
@@ -188,7 +189,8 @@ int check_state(float* master, float* m, float* v, uint8_t* codes, float* scale_
 
 int step_tiles(float* master, const float* grad, float* m, float* v, uint8_t* codes,
                float* scale_inv, int64_t n_tiles, const bfz_adamw* hp,
-               const bfz_step_options* opts, void* stream, const char* where) {
+               const bfz_step_options* opts, const float* grad_scale, void* stream,
+               const char* where) {
     if (!master || !grad || !m || !v || !codes || !scale_inv || !hp)
         return fail(BFZ_EINVAL, "%s: null pointer", where);
     if (n_tiles < 0 || n_tiles > kMaxLaunchTiles)
@@ -201,6 +203,7 @@ int step_tiles(float* master, const float* grad, float* m, float* v, uint8_t* co
     StepScalars s;
     rc = make_scalars(hp, opts, &s, where);
     if (rc) return rc;
+    s.grad_scale = grad_scale;
     int err = launch_step(master, grad, m, v, codes, scale_inv, n_tiles, s, stream);
     if (err != hipSuccess) return hip_fail(where, err);
     return BFZ_OK;
@@ -211,7 +214,7 @@ int step_tiles(float* master, const float* grad, float* m, float* v, uint8_t* co
 extern "C" int adamw_fp8_step(float* master, const float* grad, float* m, float* v,
                               uint8_t* codes, float* scale_inv, int64_t n_tiles,
                               const bfz_adamw* hp, void* stream) {
-    return step_tiles(master, grad, m, v, codes, scale_inv, n_tiles, hp, nullptr, stream,
+    return step_tiles(master, grad, m, v, codes, scale_inv, n_tiles, hp, nullptr, nullptr, stream,
                       "adamw_fp8_step");
 }
 
@@ -219,45 +222,66 @@ extern "C" int adamw_fp8_step_ex(float* master, const float* grad, float* m, flo
                                  uint8_t* codes, float* scale_inv, int64_t n_tiles,
                                  const bfz_adamw* hp, const bfz_step_options* opts,
                                  void* stream) {
-    return step_tiles(master, grad, m, v, codes, scale_inv, n_tiles, hp, opts, stream,
+    return step_tiles(master, grad, m, v, codes, scale_inv, n_tiles, hp, opts, nullptr, stream,
                       "adamw_fp8_step_ex");
 }
 
-extern "C" int fold_adamw_fp8_step(const bfz_plan* plan, const float* const* grad, float* master,
-                                   float* m, float* v, uint8_t* codes, float* scale_inv,
-                                   const bfz_adamw* hp, const bfz_step_options* opts,
-                                   void* stream) {
+namespace {
+
+int check_grad_scale(const float* grad_scale, const char* where) {
+    if (!grad_scale) return fail(BFZ_EINVAL, "%s: null pointer", where);
+    if (!aligned(grad_scale, 4)) return fail(BFZ_EALIGN, "%s: grad_scale must be 4-byte aligned", where);
+    return BFZ_OK;
+}
+
+}  // namespace
+
+extern "C" int bfz_adamw_fp8_step_clip(float* master, const float* grad, float* m, float* v,
+                                       uint8_t* codes, float* scale_inv, int64_t n_tiles,
+                                       const bfz_adamw* hp, const bfz_step_options* opts,
+                                       const float* grad_scale, void* stream) {
+    const char* where = "bfz_adamw_fp8_step_clip";
+    const int rc = check_grad_scale(grad_scale, where);
+    return rc ? rc
+              : step_tiles(master, grad, m, v, codes, scale_inv, n_tiles, hp, opts, grad_scale, stream,
+                           where);
+}
+
+namespace {
+
+int fold_step(const bfz_plan* plan, const float* const* grad, float* master, float* m, float* v,
+              uint8_t* codes, float* scale_inv, const bfz_adamw* hp, const bfz_step_options* opts,
+              const float* grad_scale, void* stream, const char* where) {
     if (!plan || !grad || !master || !m || !v || !codes || !scale_inv || !hp)
-        return fail(BFZ_EINVAL, "fold_adamw_fp8_step: null pointer");
-    int rc = check_plan(plan, "fold_adamw_fp8_step");
+        return fail(BFZ_EINVAL, "%s: null pointer", where);
+    int rc = check_plan(plan, where);
     if (rc) return rc;
-    rc = check_weights(plan, reinterpret_cast<const void* const*>(grad), "fold_adamw_fp8_step");
+    rc = check_weights(plan, reinterpret_cast<const void* const*>(grad), where);
     if (rc) return rc;
     for (int32_t w = 0; w < plan->n_weights; ++w)
         if (grad[w] && !aligned(grad[w], 4))
-            return fail(BFZ_EALIGN, "fold_adamw_fp8_step: gradient %d must be 4-byte aligned", w);
-    rc = check_state(master, m, v, codes, scale_inv, "fold_adamw_fp8_step");
+            return fail(BFZ_EALIGN, "%s: gradient %d must be 4-byte aligned", where, w);
+    rc = check_state(master, m, v, codes, scale_inv, where);
     if (rc) return rc;
     StepScalars s;
-    rc = make_scalars(hp, opts, &s, "fold_adamw_fp8_step");
+    rc = make_scalars(hp, opts, &s, where);
     if (rc) return rc;
+    s.grad_scale = grad_scale;
     for (const Segment& seg : plan->segments) {
         PackArgs args{};
         for (int32_t k = 0; k < seg.n_weights; ++k) args.src[k] = grad[seg.weight0 + k];
         const int64_t off = seg.slot0 * kTileElems, soff = seg.slot0 * s.state_stride;
         int err = launch_fold_step(plan->d_entries + seg.slot0, seg.n_slots, args, master + soff,
                                    m + soff, v + soff, codes + off, scale_inv + seg.slot0, s, stream);
-        if (err != hipSuccess) return hip_fail("fold_adamw_fp8_step", err);
+        if (err != hipSuccess) return hip_fail(where, err);
     }
     return BFZ_OK;
 }
 
-extern "C" int fold_adamw_fp8_step_unpack(const bfz_plan* plan, const float* const* grad,
-                                          float* master, float* m, float* v, uint8_t* codes,
-                                          float* scale_inv, uint8_t* const* dst_fp8,
-                                          float* const* dst_scale, const bfz_adamw* hp,
-                                          const bfz_step_options* opts, void* stream) {
-    const char* where = "fold_adamw_fp8_step_unpack";
+int fold_step_unpack(const bfz_plan* plan, const float* const* grad, float* master, float* m,
+                     float* v, uint8_t* codes, float* scale_inv, uint8_t* const* dst_fp8,
+                     float* const* dst_scale, const bfz_adamw* hp, const bfz_step_options* opts,
+                     const float* grad_scale, void* stream, const char* where) {
     if (!plan || !grad || !master || !m || !v || !dst_fp8 || !dst_scale || !hp)
         return fail(BFZ_EINVAL, "%s: null pointer", where);
     if (!codes != !scale_inv)
@@ -281,6 +305,7 @@ extern "C" int fold_adamw_fp8_step_unpack(const bfz_plan* plan, const float* con
     StepScalars s;
     rc = make_scalars(hp, opts, &s, where);
     if (rc) return rc;
+    s.grad_scale = grad_scale;
     for (const Segment& seg : plan->segments) {
         PackArgs in{};
         UnpackArgs out{};
@@ -299,13 +324,11 @@ extern "C" int fold_adamw_fp8_step_unpack(const bfz_plan* plan, const float* con
     return BFZ_OK;
 }
 
-extern "C" int fold_adamw_fp8_step_unpack_t(const bfz_plan* plan, const float* const* grad,
-                                            float* master, float* m, float* v, uint8_t* codes,
-                                            float* scale_inv, uint8_t* const* dst_fp8,
-                                            float* const* dst_scale, uint8_t* const* dst_t,
-                                            float* const* dst_t_scale, const bfz_adamw* hp,
-                                            const bfz_step_options* opts, void* stream) {
-    const char* where = "fold_adamw_fp8_step_unpack_t";
+int fold_step_unpack_t(const bfz_plan* plan, const float* const* grad, float* master, float* m,
+                       float* v, uint8_t* codes, float* scale_inv, uint8_t* const* dst_fp8,
+                       float* const* dst_scale, uint8_t* const* dst_t, float* const* dst_t_scale,
+                       const bfz_adamw* hp, const bfz_step_options* opts, const float* grad_scale,
+                       void* stream, const char* where) {
     if (!plan || !grad || !master || !m || !v || !dst_fp8 || !dst_scale || !dst_t || !dst_t_scale ||
         !hp)
         return fail(BFZ_EINVAL, "%s: null pointer", where);
@@ -337,6 +360,7 @@ extern "C" int fold_adamw_fp8_step_unpack_t(const bfz_plan* plan, const float* c
     StepScalars s;
     rc = make_scalars(hp, opts, &s, where);
     if (rc) return rc;
+    s.grad_scale = grad_scale;
     for (const Segment& seg : plan->segments) {
         PackArgs in{};
         UnpackArgs out{};
@@ -357,6 +381,71 @@ extern "C" int fold_adamw_fp8_step_unpack_t(const bfz_plan* plan, const float* c
         if (err != hipSuccess) return hip_fail(where, err);
     }
     return BFZ_OK;
+}
+
+}  // namespace
+
+extern "C" int fold_adamw_fp8_step(const bfz_plan* plan, const float* const* grad, float* master,
+                                   float* m, float* v, uint8_t* codes, float* scale_inv,
+                                   const bfz_adamw* hp, const bfz_step_options* opts,
+                                   void* stream) {
+    return fold_step(plan, grad, master, m, v, codes, scale_inv, hp, opts, nullptr, stream,
+                     "fold_adamw_fp8_step");
+}
+
+extern "C" int bfz_fold_adamw_fp8_step_clip(const bfz_plan* plan, const float* const* grad,
+                                            float* master, float* m, float* v, uint8_t* codes,
+                                            float* scale_inv, const bfz_adamw* hp,
+                                            const bfz_step_options* opts, const float* grad_scale,
+                                            void* stream) {
+    const char* where = "bfz_fold_adamw_fp8_step_clip";
+    const int rc = check_grad_scale(grad_scale, where);
+    return rc ? rc
+              : fold_step(plan, grad, master, m, v, codes, scale_inv, hp, opts, grad_scale, stream,
+                          where);
+}
+
+extern "C" int fold_adamw_fp8_step_unpack(const bfz_plan* plan, const float* const* grad,
+                                          float* master, float* m, float* v, uint8_t* codes,
+                                          float* scale_inv, uint8_t* const* dst_fp8,
+                                          float* const* dst_scale, const bfz_adamw* hp,
+                                          const bfz_step_options* opts, void* stream) {
+    return fold_step_unpack(plan, grad, master, m, v, codes, scale_inv, dst_fp8, dst_scale, hp,
+                            opts, nullptr, stream, "fold_adamw_fp8_step_unpack");
+}
+
+extern "C" int bfz_fold_adamw_fp8_step_unpack_clip(
+    const bfz_plan* plan, const float* const* grad, float* master, float* m, float* v,
+    uint8_t* codes, float* scale_inv, uint8_t* const* dst_fp8, float* const* dst_scale,
+    const bfz_adamw* hp, const bfz_step_options* opts, const float* grad_scale, void* stream) {
+    const char* where = "bfz_fold_adamw_fp8_step_unpack_clip";
+    const int rc = check_grad_scale(grad_scale, where);
+    return rc ? rc
+              : fold_step_unpack(plan, grad, master, m, v, codes, scale_inv, dst_fp8, dst_scale,
+                                 hp, opts, grad_scale, stream, where);
+}
+
+extern "C" int fold_adamw_fp8_step_unpack_t(const bfz_plan* plan, const float* const* grad,
+                                            float* master, float* m, float* v, uint8_t* codes,
+                                            float* scale_inv, uint8_t* const* dst_fp8,
+                                            float* const* dst_scale, uint8_t* const* dst_t,
+                                            float* const* dst_t_scale, const bfz_adamw* hp,
+                                            const bfz_step_options* opts, void* stream) {
+    return fold_step_unpack_t(plan, grad, master, m, v, codes, scale_inv, dst_fp8, dst_scale,
+                              dst_t, dst_t_scale, hp, opts, nullptr, stream,
+                              "fold_adamw_fp8_step_unpack_t");
+}
+
+extern "C" int bfz_fold_adamw_fp8_step_unpack_t_clip(
+    const bfz_plan* plan, const float* const* grad, float* master, float* m, float* v,
+    uint8_t* codes, float* scale_inv, uint8_t* const* dst_fp8, float* const* dst_scale,
+    uint8_t* const* dst_t, float* const* dst_t_scale, const bfz_adamw* hp,
+    const bfz_step_options* opts, const float* grad_scale, void* stream) {
+    const char* where = "bfz_fold_adamw_fp8_step_unpack_t_clip";
+    const int rc = check_grad_scale(grad_scale, where);
+    return rc ? rc
+              : fold_step_unpack_t(plan, grad, master, m, v, codes, scale_inv, dst_fp8, dst_scale,
+                                   dst_t, dst_t_scale, hp, opts, grad_scale, stream, where);
 }
 
 extern "C" int bfz_transpose_pow2(const bfz_plan* plan, const uint8_t* codes,

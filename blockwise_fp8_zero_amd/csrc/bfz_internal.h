@@ -56,6 +56,7 @@ struct StepScalars {
     int32_t has_decay;
     int32_t pow2;          // power-of-two tile scales
     int64_t state_stride;  // floats from one tile of master / m / v to the next
+    const float* grad_scale;  // device scalar the gradient is multiplied by, or null
 };
 
 // Kernel launchers (kernels.hip).  They return a hipError_t value as int.
@@ -84,6 +85,11 @@ const char* hip_error_string(int err);
 
 // Error reporting (abi.cpp): records the message for bfz_last_error().
 int fail(int code, const char* fmt, ...);
+
+// Checks shared by the plan's entry points (abi.cpp): the plan's table is on
+// the current device; every weight it owns tiles of has a pointer.
+int check_plan(const bfz_plan* plan, const char* where);
+int check_weights(const bfz_plan* plan, const void* const* ptrs, const char* where);
 
 }  // namespace bfz
 

@@ -1,0 +1,541 @@
+// Token embedding from a row-major table (f32, bf16, fp16, or E4M3 codes
+// with their 128x128 tile scales), and the table's gradient by sorted tokens.
+//
+//   out[n]    = scale * table[id[n]]           (zero for an id outside the table)
+//   dtable[v] = (dtable[v] +) scale * sum over n with id[n] = v of dout[n]
+//
+// Both move bytes and compute next to nothing: the bound is HBM, or at few
+// tokens the launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "ops_device.h"
+#include "ops_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace bfz {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------------
+// Lookup.  A thread moves one piece of kVec elements; a workgroup takes one
+// token (rows of 256 pieces or more) or 256 / pieces tokens.
+// ---------------------------------------------------------------------
+
+// kVec consecutive table elements as floats.
+template <class T, int kVec>
+struct Piece {
+    static __device__ __forceinline__ void load(const T* p, float (&x)[kVec]) {
+        if constexpr (kVec == 8) {
+            load8(p, x);
+        } else {
+#pragma unroll
+            for (int l = 0; l < kVec; ++l) x[l] = Elem<T>::get(p[l]);
+        }
+    }
+};
+
+template <int kVec>
+struct Piece<uint8_t, kVec> {
+    static __device__ __forceinline__ void load(const uint8_t* p, float (&x)[kVec]) {
+        typedef uint32_t words __attribute__((ext_vector_type(kVec / 4 > 0 ? kVec / 4 : 1)));
+        words w;
+        if constexpr (kVec == 1) w = *p;
+        else w = *reinterpret_cast<const words*>(p);
+#pragma unroll
+        for (int l = 0; l < kVec; ++l) {
+            uint32_t v;
+            if constexpr (kVec <= 4) v = (uint32_t)w[0];
+            else v = w[l >> 2];
+            switch (l & 3) {
+                case 0: x[l] = __builtin_amdgcn_cvt_f32_fp8((int)v, 0); break;
+                case 1: x[l] = __builtin_amdgcn_cvt_f32_fp8((int)v, 1); break;
+                case 2: x[l] = __builtin_amdgcn_cvt_f32_fp8((int)v, 2); break;
+                default: x[l] = __builtin_amdgcn_cvt_f32_fp8((int)v, 3); break;
+            }
+        }
+    }
+};
+
+template <class T, int kVec>
+__device__ __forceinline__ void store_piece(T* p, const float (&x)[kVec]) {
+    if constexpr (kVec >= 8) {
+#pragma unroll
+        for (int h = 0; h < kVec / 8; ++h) {
+            float y[8];
+#pragma unroll
+            for (int l = 0; l < 8; ++l) y[l] = x[8 * h + l];
+            store8(p + 8 * h, y);
+        }
+    } else if constexpr (kVec == 4) {
+        typedef uint32_t words __attribute__((ext_vector_type(sizeof(T))));  // 4 elements
+        words w;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int l = 0; l < 4; ++l) w[l] = __float_as_uint(x[l]);
+        } else {
+            w[0] = pack2<T>(x[0], x[1]);
+            w[1] = pack2<T>(x[2], x[3]);
+        }
+        *reinterpret_cast<words*>(p) = w;
+    } else {
+#pragma unroll
+        for (int l = 0; l < kVec; ++l) p[l] = Elem<T>::to(x[l]);
+    }
+}
+
+template <class T, class O, int kVec>
+__global__ __launch_bounds__(kThreads) void embed_kernel(EmbedArgs a, int32_t pieces, int32_t tokens_per_wg) {
+    const T* table = static_cast<const T*>(a.table);
+    O* out = static_cast<O*>(a.out);
+    const int64_t wb = (a.dim + kTileDim - 1) / kTileDim;
+    const int local = tokens_per_wg > 1 ? (int)threadIdx.x / pieces : 0;
+    const int first = (int)threadIdx.x - local * pieces;
+    if (local >= tokens_per_wg) return;
+    for (int64_t n = (int64_t)blockIdx.x * tokens_per_wg + local; n < a.n; n += (int64_t)gridDim.x * tokens_per_wg) {
+        const int64_t row = row_of(a.ids, a.ids64, n, a.vocab);
+        O* dst = out + n * a.out_ld;
+        for (int p = first; p < pieces; p += kThreads) {
+            const int64_t c = (int64_t)p * kVec;
+            float x[kVec];
+#pragma unroll
+            for (int l = 0; l < kVec; ++l) x[l] = 0.0f;
+            if (row >= 0) {
+                Piece<T, kVec>::load(table + row * a.table_ld + c, x);
+                float s = a.scale;
+                if constexpr (sizeof(T) == 1) s *= a.grid[(row / kTileDim) * wb + c / kTileDim];
+#pragma unroll
+                for (int l = 0; l < kVec; ++l) x[l] *= s;
+            }
+            store_piece<O, kVec>(dst + c, x);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------
+// Stable sort of the tokens by id.  Runs of kRun tokens are ranked by
+// counting (every token against every token of its run: the run's ids sit
+// in LDS and are read by all lanes at once, two VALU operations per pair),
+// then runs are merged sixteen at a time by binary search: a token's place
+// is its place in its own run plus, for each other run, how many of that
+// run's come before it.  Ids outside the table get the key `vocab` and sort
+// last.  Two launches up to 32768 tokens, one more for each factor of 16.
+// ---------------------------------------------------------------------
+constexpr int kRun = 2048;
+constexpr int kRankWaves = 8, kRankThreads = 64 * kRankWaves;
+constexpr int kMergeRuns = 16;
+
+// A workgroup ranks 64 tokens of a run: wave w counts over ids
+// [256 w, 256 w + 256) of it.
+__global__ __launch_bounds__(kRankThreads) void rank_runs_kernel(const void* ids, int ids64, int64_t n, int64_t vocab,
+                                                                 int32_t* keys, int32_t* pos) {
+    typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+    __shared__ alignas(16) int32_t run[kRun];
+    __shared__ int32_t count[kRankWaves][64];
+    const int64_t base = (int64_t)(blockIdx.x / (kRun / 64)) * kRun;
+    const int group = (int)(blockIdx.x % (kRun / 64)) * 64;
+    const int len = (int)(n - base < kRun ? n - base : kRun);
+    if (group >= len) return;
+    for (int j = threadIdx.x; j < kRun; j += kRankThreads) {
+        int32_t k = 0x7FFFFFFF;  // past the end: after every key
+        if (j < len) {
+            const int64_t r = row_of(ids, ids64, base + j, vocab);
+            k = r < 0 ? (int32_t)vocab : (int32_t)r;
+        }
+        run[j] = k;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int i = group + lane;
+    const int32_t key = run[i];
+    const int j0 = w * (kRun / kRankWaves), j1 = j0 + kRun / kRankWaves;
+    int32_t before = 0;
+    if (j0 < len) {
+        if (j1 <= group) {  // all of them stand before the 64: equal ids count
+            for (int j = j0; j < j1; j += 4) {
+                const i32x4 k = *reinterpret_cast<const i32x4*>(&run[j]);
+#pragma unroll
+                for (int l = 0; l < 4; ++l) before += k[l] <= key;
+            }
+        } else if (j0 >= group + 64) {
+            for (int j = j0; j < j1; j += 4) {
+                const i32x4 k = *reinterpret_cast<const i32x4*>(&run[j]);
+#pragma unroll
+                for (int l = 0; l < 4; ++l) before += k[l] < key;
+            }
+        } else {
+            for (int j = j0; j < j1; j += 4) {
+                const i32x4 k = *reinterpret_cast<const i32x4*>(&run[j]);
+#pragma unroll
+                for (int l = 0; l < 4; ++l) before += k[l] < key || (k[l] == key && j + l < i);
+            }
+        }
+    }
+    count[w][lane] = before;
+    __syncthreads();
+    if (w != 0 || i >= len) return;
+#pragma unroll
+    for (int x = 1; x < kRankWaves; ++x) before += count[x][lane];
+    keys[base + before] = key;
+    pos[base + before] = (int32_t)(base + i);
+}
+
+// Merge of groups of kMergeRuns sorted runs of `len` tokens each.  The
+// sixteen searches of a token advance together, so their loads overlap.
+__global__ __launch_bounds__(kThreads) void merge_runs_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ pos,
+                                                              int32_t* __restrict__ out_keys, int32_t* __restrict__ out_pos,
+                                                              int64_t n, int64_t len, int steps) {
+    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (t >= n) return;
+    const int64_t group = t / (len * kMergeRuns) * (len * kMergeRuns);
+    const int mine = (int)((t - group) / len);
+    const int32_t key = keys[t];
+    // of run r: how many come before this token; searched in [lo, lo + left)
+    int32_t lo[kMergeRuns], left[kMergeRuns];
+#pragma unroll
+    for (int r = 0; r < kMergeRuns; ++r) {
+        const int64_t have = n - (group + r * len);
+        lo[r] = 0;
+        left[r] = (int32_t)(r == mine || have <= 0 ? 0 : have < len ? have : len);
+    }
+    for (int s = 0; s < steps; ++s) {
+#pragma unroll
+        for (int r = 0; r < kMergeRuns; ++r) {
+            // an ended search reads its last place again and keeps its answer
+            const int32_t half = left[r] >> 1;
+            const int64_t at = group + r * len + lo[r] + half;
+            const int32_t k = keys[at < n ? at : n - 1];
+            const bool open = left[r] > 0, before = k < key || (k == key && r < mine);
+            lo[r] = open && before ? lo[r] + half + 1 : lo[r];
+            left[r] = !open ? 0 : before ? left[r] - half - 1 : half;
+        }
+    }
+    int64_t at = t - mine * len;
+#pragma unroll
+    for (int r = 0; r < kMergeRuns; ++r) at += lo[r];
+    out_keys[at] = key;
+    out_pos[at] = pos[t];
+}
+
+// First index in [lo, n) whose key is >= v (or > v).
+template <bool kUpper>
+__device__ __forceinline__ int64_t bound_of(const int32_t* keys, int64_t lo, int64_t n, int64_t v) {
+    int64_t left = n - lo;
+    while (left > 0) {
+        const int64_t half = left >> 1;
+        const int64_t k = keys[lo + half];
+        const bool before = kUpper ? k <= v : k < v;
+        lo = before ? lo + half + 1 : lo;
+        left = before ? left - half - 1 : half;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------------
+// Sums by segment.  A workgroup takes `per` consecutive sorted tokens and
+// 256 * kVec columns, adds rows in ascending position, and writes a row of
+// the gradient whose tokens all lie in its range; a row that continues over
+// a border goes to two float partials per range (the part that began before
+// it, the part that goes on after it), which join_kernel adds in order.
+// The order of every sum is fixed by the sorted tokens and `per`, so two
+// runs give the same bits.  Workgroups past the ranges write the zero rows
+// of tokens that do not occur (kFillRows rows each), so the whole gradient
+// is written once.
+// ---------------------------------------------------------------------
+constexpr int kFillRows = 16;
+constexpr int kMaxPer = 32;
+
+struct SegmentArgs {
+    const int32_t* keys;
+    const int32_t* pos;
+    float* head;  // [ranges][dim4]: the part of a range that continues a row begun before it
+    float* tail;  // [ranges][dim4]: the part that goes on in the next range
+    int64_t n, vocab, dim, dim4, dout_ld, dtable_ld, ranges;
+    int32_t slabs, per;
+    float scale;
+    int32_t accumulate;
+};
+
+template <class O, int kVec>
+__device__ __forceinline__ void write_row(O* dst, const float (&sum)[kVec], const SegmentArgs& a) {
+    float y[kVec];
+#pragma unroll
+    for (int l = 0; l < kVec; ++l) y[l] = sum[l] * a.scale;
+    if (a.accumulate) {
+        float old[kVec];
+        if constexpr (kVec == 4 && sizeof(O) == 4) {
+            typedef float f4 __attribute__((ext_vector_type(4)));
+            const f4 o = *reinterpret_cast<const f4*>(dst);
+#pragma unroll
+            for (int l = 0; l < 4; ++l) old[l] = o[l];
+        } else {
+#pragma unroll
+            for (int l = 0; l < kVec; ++l) old[l] = Elem<O>::get(dst[l]);
+        }
+#pragma unroll
+        for (int l = 0; l < kVec; ++l) y[l] = old[l] + y[l];
+    }
+    store_piece<O, kVec>(dst, y);
+}
+
+template <int kVec>
+__device__ __forceinline__ void store_partial(float* p, const float (&x)[kVec]) {
+#pragma unroll
+    for (int l = 0; l < kVec; ++l) p[l] = x[l];
+}
+
+template <class I, class O, int kVec>
+__global__ __launch_bounds__(kThreads) void segment_kernel(const void* dout_p, void* dtable_p, SegmentArgs a) {
+    const I* dout = static_cast<const I*>(dout_p);
+    O* dtable = static_cast<O*>(dtable_p);
+    __shared__ int32_t key[kMaxPer + 2], row[kMaxPer];
+    __shared__ int32_t absent[kFillRows];
+    const int64_t sums = a.ranges * a.slabs;
+    if (blockIdx.x >= sums) {  // rows of tokens that do not occur
+        const int64_t v0 = (blockIdx.x - sums) * kFillRows;
+        if (threadIdx.x < kFillRows) {
+            const int64_t v = v0 + threadIdx.x;
+            bool none = false;
+            if (v < a.vocab) {
+                const int64_t at = bound_of<false>(a.keys, 0, a.n, v);
+                none = at == a.n || a.keys[at] != v;
+            }
+            absent[threadIdx.x] = none;
+        }
+        __syncthreads();
+        float zero[kVec];
+#pragma unroll
+        for (int l = 0; l < kVec; ++l) zero[l] = 0.0f;
+        for (int r = 0; r < kFillRows; ++r) {
+            if (!absent[r]) continue;
+            O* dst = dtable + (v0 + r) * a.dtable_ld;
+            for (int64_t c = (int64_t)threadIdx.x * kVec; c < a.dim; c += kThreads * kVec) store_piece<O, kVec>(dst + c, zero);
+        }
+        return;
+    }
+    const int64_t range = blockIdx.x / a.slabs;
+    const int64_t c = ((int64_t)(blockIdx.x % a.slabs) * kThreads + threadIdx.x) * kVec;
+    const int64_t e0 = range * a.per;
+    const int count = (int)(a.n - e0 < a.per ? a.n - e0 : a.per);
+    if (threadIdx.x < count + 2) {  // the neighbours' keys too; -1 outside
+        const int64_t e = e0 + (int64_t)threadIdx.x - 1;
+        key[threadIdx.x] = e >= 0 && e < a.n ? a.keys[e] : -1;
+    }
+    if (threadIdx.x < count) row[threadIdx.x] = a.pos[e0 + threadIdx.x];
+    __syncthreads();
+    if (c >= a.dim) return;
+    float acc[kVec];
+#pragma unroll
+    for (int l = 0; l < kVec; ++l) acc[l] = 0.0f;
+    bool began = key[1] != key[0];
+    for (int b = 0; b < count; b += 8) {
+        float x[8][kVec];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)  // past the end the last row again: loaded, not used
+            Piece<I, kVec>::load(dout + (int64_t)row[min(b + u, count - 1)] * a.dout_ld + c, x[u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (b + u >= count) break;
+#pragma unroll
+            for (int l = 0; l < kVec; ++l) acc[l] += x[u][l];
+            const int32_t k = key[b + u + 1];
+            if (b + u + 1 < count && key[b + u + 2] == k) continue;
+            const bool ends = key[b + u + 2] != k;
+            if (k < a.vocab) {
+                if (began && ends) write_row<O, kVec>(dtable + (int64_t)k * a.dtable_ld + c, acc, a);
+                else store_partial<kVec>((began ? a.tail : a.head) + range * a.dim4 + c, acc);
+            }
+            began = true;
+#pragma unroll
+            for (int l = 0; l < kVec; ++l) acc[l] = 0.0f;
+        }
+    }
+}
+
+// Rows that cross ranges: the range a row begins in adds its tail and the
+// heads of the ranges the row goes on through.
+template <class O, int kVec>
+__global__ __launch_bounds__(kThreads) void join_kernel(void* dtable_p, SegmentArgs a) {
+    O* dtable = static_cast<O*>(dtable_p);
+    const int64_t range = blockIdx.x / a.slabs;
+    const int64_t c = ((int64_t)(blockIdx.x % a.slabs) * kThreads + threadIdx.x) * kVec;
+    const int64_t e0 = range * a.per, e1 = e0 + a.per;
+    if (e1 >= a.n) return;
+    const int32_t k = a.keys[e1 - 1];
+    if (k >= a.vocab || a.keys[e1] != k) return;                              // does not go on
+    if (a.keys[e0] == k && e0 > 0 && a.keys[e0 - 1] == k) return;            // began earlier
+    if (c >= a.dim) return;
+    const int64_t last = (bound_of<true>(a.keys, e1, a.n, k) - 1) / a.per;
+    float acc[kVec];
+#pragma unroll
+    for (int l = 0; l < kVec; ++l) acc[l] = a.tail[range * a.dim4 + c + l];
+#pragma unroll 8
+    for (int64_t r = range + 1; r <= last; ++r) {
+#pragma unroll
+        for (int l = 0; l < kVec; ++l) acc[l] += a.head[r * a.dim4 + c + l];
+    }
+    write_row<O, kVec>(dtable + (int64_t)k * a.dtable_ld + c, acc, a);
+}
+
+// Tokens per range: long ranges write fewer partials, short ones give a
+// small batch more workgroups.
+constexpr int64_t kLongTokens = 16384;
+int32_t range_tokens(int64_t n) { return n >= kLongTokens ? 32 : 8; }
+
+int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+bool aligned_rows(const void* p, int64_t ld, int64_t dim, int size, int vec) {
+    const int64_t bytes = std::min<int64_t>(16, (int64_t)vec * size);
+    return dim % vec == 0 && (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && (ld * size) % bytes == 0;
+}
+
+template <class T, class O, int kVec>
+int embed_vec(const EmbedArgs& a, void* stream) {
+    const int64_t pieces = a.dim / kVec;
+    const int32_t per_wg = pieces >= kThreads ? 1 : (int32_t)(kThreads / pieces);
+    const int64_t wgs = std::min<int64_t>((a.n + per_wg - 1) / per_wg, 1 << 22);
+    hipLaunchKernelGGL((embed_kernel<T, O, kVec>), dim3((uint32_t)wgs), dim3(kThreads), 0, (hipStream_t)stream, a,
+                       (int32_t)pieces, per_wg);
+    return hipGetLastError();
+}
+
+template <class T, class O>
+int embed_types(const EmbedArgs& a, void* stream) {
+    const auto fits = [&](int vec) {
+        return aligned_rows(a.table, a.table_ld, a.dim, sizeof(T), vec) && aligned_rows(a.out, a.out_ld, a.dim, sizeof(O), vec);
+    };
+    if constexpr (sizeof(T) == 1)
+        if (fits(16)) return embed_vec<T, O, 16>(a, stream);
+    if (fits(8)) return embed_vec<T, O, 8>(a, stream);
+    if (fits(4)) return embed_vec<T, O, 4>(a, stream);
+    return embed_vec<T, O, 1>(a, stream);
+}
+
+template <class T>
+int embed_out(const EmbedArgs& a, void* stream) {
+    switch (a.out_type) {
+        case kF32: return embed_types<T, float>(a, stream);
+        case kBF16: return embed_types<T, bf16_t>(a, stream);
+        default: return embed_types<T, f16_t>(a, stream);
+    }
+}
+
+struct GradWork {
+    int32_t *keys[2], *pos[2];
+    float *head, *tail;
+    int64_t bytes;
+};
+
+GradWork grad_work(void* work, int64_t n, int64_t dim) {
+    GradWork g;
+    char* p = static_cast<char*>(work);
+    int64_t at = 0;
+    const auto take = [&](int64_t bytes) {
+        char* q = p + at;
+        at += align_up(bytes, 256);
+        return q;
+    };
+    for (int k = 0; k < 2; ++k) {
+        g.keys[k] = reinterpret_cast<int32_t*>(take(4 * n));
+        g.pos[k] = reinterpret_cast<int32_t*>(take(4 * n));
+    }
+    const int64_t ranges = (n + range_tokens(n) - 1) / range_tokens(n);
+    g.head = reinterpret_cast<float*>(take(ranges * align_up(dim, 4) * 4));
+    g.tail = reinterpret_cast<float*>(take(ranges * align_up(dim, 4) * 4));
+    g.bytes = at;
+    return g;
+}
+
+template <class I, class O, int kVec>
+int segments(const EmbedGradArgs& a, SegmentArgs s, void* stream) {
+    s.slabs = (int32_t)((a.dim + kThreads * kVec - 1) / (kThreads * kVec));
+    const int64_t sums = s.ranges * s.slabs;
+    const int64_t fills = a.accumulate ? 0 : (a.vocab + kFillRows - 1) / kFillRows;
+    if (sums + fills == 0) return hipSuccess;
+    hipLaunchKernelGGL((segment_kernel<I, O, kVec>), dim3((uint32_t)(sums + fills)), dim3(kThreads), 0, (hipStream_t)stream,
+                       a.dout, a.dtable, s);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || s.ranges <= 1) return err;
+    hipLaunchKernelGGL((join_kernel<O, kVec>), dim3((uint32_t)sums), dim3(kThreads), 0, (hipStream_t)stream, a.dtable, s);
+    return hipGetLastError();
+}
+
+template <class I, class O>
+int segments_vec(const EmbedGradArgs& a, const SegmentArgs& s, void* stream) {
+    if (aligned_rows(a.dout, a.dout_ld, a.dim, sizeof(I), 4) && aligned_rows(a.dtable, a.dtable_ld, a.dim, sizeof(O), 4))
+        return segments<I, O, 4>(a, s, stream);
+    return segments<I, O, 1>(a, s, stream);
+}
+
+template <class I>
+int segments_out(const EmbedGradArgs& a, const SegmentArgs& s, void* stream) {
+    switch (a.dtable_type) {
+        case kF32: return segments_vec<I, float>(a, s, stream);
+        case kBF16: return segments_vec<I, bf16_t>(a, s, stream);
+        default: return segments_vec<I, f16_t>(a, s, stream);
+    }
+}
+
+}  // namespace
+
+int launch_embed(const EmbedArgs& a, void* stream) {
+    if (a.n == 0 || a.dim == 0) return hipSuccess;
+    switch (a.table_type) {
+        case kF32: return embed_out<float>(a, stream);
+        case kBF16: return embed_out<bf16_t>(a, stream);
+        case kF16: return embed_out<f16_t>(a, stream);
+        default: return embed_out<uint8_t>(a, stream);
+    }
+}
+
+// Enough for every count of tokens up to n (just below kLongTokens, the
+// shorter ranges have more partials than somewhat above it).
+int64_t embed_grad_work_bytes(int64_t n, int64_t dim) {
+    return std::max(grad_work(nullptr, n, dim).bytes, grad_work(nullptr, std::min(n, kLongTokens - 1), dim).bytes);
+}
+
+int launch_embed_grad(const EmbedGradArgs& a, void* work, void* stream) {
+    const GradWork g = grad_work(work, a.n, a.dim);
+    int at = 0;
+    if (a.n > 0) {
+        const int64_t runs = (a.n + kRun - 1) / kRun;
+        hipLaunchKernelGGL(rank_runs_kernel, dim3((uint32_t)(runs * (kRun / 64))), dim3(kRankThreads), 0, (hipStream_t)stream,
+                           a.ids, a.ids64, a.n, a.vocab, g.keys[0], g.pos[0]);
+        hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        for (int64_t len = kRun; len < a.n; len *= kMergeRuns) {
+            int steps = 1;  // a search over m entries takes at most bits(m) steps
+            while ((int64_t(1) << steps) <= len) ++steps;
+            hipLaunchKernelGGL(merge_runs_kernel, dim3((uint32_t)((a.n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                               (hipStream_t)stream, g.keys[at], g.pos[at], g.keys[at ^ 1], g.pos[at ^ 1], a.n, len, steps);
+            err = hipGetLastError();
+            if (err != hipSuccess) return err;
+            at ^= 1;
+        }
+    }
+    SegmentArgs s{};
+    s.keys = g.keys[at];
+    s.pos = g.pos[at];
+    s.head = g.head;
+    s.tail = g.tail;
+    s.n = a.n;
+    s.vocab = a.vocab;
+    s.dim = a.dim;
+    s.dim4 = align_up(a.dim, 4);
+    s.dout_ld = a.dout_ld;
+    s.dtable_ld = a.dtable_ld;
+    s.per = range_tokens(a.n);
+    s.ranges = (a.n + s.per - 1) / s.per;
+    s.scale = a.scale;
+    s.accumulate = a.accumulate;
+    switch (a.dout_type) {
+        case kF32: return segments_out<float>(a, s, stream);
+        case kBF16: return segments_out<bf16_t>(a, s, stream);
+        default: return segments_out<f16_t>(a, s, stream);
+    }
+}
+
+}  // namespace bfz

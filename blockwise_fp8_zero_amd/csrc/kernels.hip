@@ -342,7 +342,10 @@ struct RowMajorCodes {
     }
 };
 
-template <class GradFn, class Out = RowMajorCodes>
+// kClip: the gradient is multiplied by *s.grad_scale (one binary32 product,
+// as a separate pass over it would) before the update sees it.  A template
+// flag, so that the steps without it are compiled as before.
+template <bool kClip, class GradFn, class Out = RowMajorCodes>
 __device__ __forceinline__ float step_tile(int64_t tile, float* __restrict__ master,
                                            float* __restrict__ mom1, float* __restrict__ mom2,
                                            uint32_t* __restrict__ codes,
@@ -370,6 +373,13 @@ __device__ __forceinline__ float step_tile(int64_t tile, float* __restrict__ mas
     }
 #pragma unroll
     for (int k = 0; k < kStepVec; ++k) g[k] = grad_at.finish(k, graw[k]);
+    if constexpr (kClip) {
+        const float c = *s.grad_scale;
+#pragma unroll
+        for (int k = 0; k < kStepVec; ++k)
+#pragma unroll
+            for (int l = 0; l < 4; ++l) g[k][l] *= c;
+    }
     float amax = 0.0f;
 #pragma unroll
     for (int k = 0; k < kStepVec; ++k) {
@@ -423,6 +433,7 @@ __device__ __forceinline__ float step_tile(int64_t tile, float* __restrict__ mas
     return scale;
 }
 
+template <bool kClip>
 __global__ __launch_bounds__(kStepThreads) void step_kernel(
     float* __restrict__ master, const float* __restrict__ grad, float* __restrict__ mom1,
     float* __restrict__ mom2, uint32_t* __restrict__ codes, float* __restrict__ scale_inv,
@@ -430,12 +441,13 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(
     extern __shared__ float wave_amax[];
     const int64_t tile = step_tile_of(blockIdx.x, n_tiles);
     const TileMajorGrad g{TileBlock(grad + tile * kTileElems, kTileElems * 4)};
-    step_tile(tile, master, mom1, mom2, codes, scale_inv, s, g, wave_amax);
+    step_tile<kClip>(tile, master, mom1, mom2, codes, scale_inv, s, g, wave_amax);
 }
 
 // The same step, with the gradient fold fused in: slot s of this launch
 // reads its gradient from the row-major weight its table entry names.
 // master/m/v/codes/scale_inv and entries point at the launch's first slot.
+template <bool kClip>
 __global__ __launch_bounds__(kStepThreads) void fold_step_kernel(
     const TileEntry* __restrict__ entries, PackArgs grads, float* __restrict__ master,
     float* __restrict__ mom1, float* __restrict__ mom2, uint32_t* __restrict__ codes,
@@ -444,13 +456,14 @@ __global__ __launch_bounds__(kStepThreads) void fold_step_kernel(
     const int64_t slot = step_tile_of(blockIdx.x, n_slots);
     const TileEntry t = entries[slot];
     with_row_major_grad(t, grads, [&](const auto& g) {
-        step_tile(slot, master, mom1, mom2, codes, scale_inv, s, g, wave_amax);
+        step_tile<kClip>(slot, master, mom1, mom2, codes, scale_inv, s, g, wave_amax);
     });
 }
 
 // Fold, step and unfold in one pass: as fold_step_kernel, and each owned
 // tile's codes and scale also land in the row-major FP8 weight and scale
 // grid its entry names.  codes / scale_inv may be null (row-major only).
+template <bool kClip>
 __global__ __launch_bounds__(kStepThreads) void fold_step_unfold_kernel(
     const TileEntry* __restrict__ entries, PackArgs grads, UnpackArgs outs,
     float* __restrict__ master, float* __restrict__ mom1, float* __restrict__ mom2,
@@ -466,7 +479,7 @@ __global__ __launch_bounds__(kStepThreads) void fold_step_unfold_kernel(
         out.vec = ((t.ld & 3) == 0) && ((reinterpret_cast<uintptr_t>(d) & 3u) == 0);
     }
     with_row_major_grad(t, grads, [&](const auto& g) {
-        step_tile(slot, master, mom1, mom2, codes, scale_inv, s, g, wave_amax, out);
+        step_tile<kClip>(slot, master, mom1, mom2, codes, scale_inv, s, g, wave_amax, out);
     });
 }
 
@@ -882,6 +895,7 @@ struct StagedCodes {
 //     transpose_pow2_kernel (two lanes per bank on both sides);
 //  3. 8 lanes per W^T row, the 1024 threads covering the tile's 128 columns
 //     at once: wt_row.
+template <bool kClip>
 __global__ __launch_bounds__(kStepThreads) void fold_step_unfold_t_kernel(
     const TileEntry* __restrict__ entries, PackArgs grads, UnpackArgs outs, TransposeArgs touts,
     float* __restrict__ master, float* __restrict__ mom1, float* __restrict__ mom2,
@@ -903,7 +917,7 @@ __global__ __launch_bounds__(kStepThreads) void fold_step_unfold_t_kernel(
     }
     float scale = 0.0f;
     with_row_major_grad(t, grads, [&](const auto& g) {
-        scale = step_tile(slot, master, mom1, mom2, codes, scale_inv, s, g, wave_amax, out);
+        scale = step_tile<kClip>(slot, master, mom1, mom2, codes, scale_inv, s, g, wave_amax, out);
     });
     __syncthreads();
     {
@@ -965,17 +979,19 @@ hipError_t reserve_lds(const void* kernel, std::atomic<uint64_t>& ready) {
     return hipSuccess;
 }
 
-std::atomic<uint64_t> g_step_lds{0}, g_fold_step_lds{0}, g_fold_step_unfold_lds{0},
-    g_fold_step_unfold_t_lds{0};
+// per kernel: without and with the gradient's scale
+std::atomic<uint64_t> g_step_lds[2], g_fold_step_lds[2], g_fold_step_unfold_lds[2],
+    g_fold_step_unfold_t_lds[2];
 
 }  // namespace
 
 int launch_step(float* master, const float* grad, float* m, float* v, uint8_t* codes,
                 float* scale_inv, int64_t n_tiles, const StepScalars& s, void* stream) {
     if (n_tiles == 0) return hipSuccess;
-    hipError_t err = reserve_lds(reinterpret_cast<const void*>(step_kernel), g_step_lds);
+    const auto kernel = s.grad_scale ? step_kernel<true> : step_kernel<false>;
+    hipError_t err = reserve_lds(reinterpret_cast<const void*>(kernel), g_step_lds[s.grad_scale != nullptr]);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(step_kernel, dim3((uint32_t)n_tiles), dim3(kStepThreads), kStepLdsBytes,
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)n_tiles), dim3(kStepThreads), kStepLdsBytes,
                        (hipStream_t)stream, master, grad, m, v,
                        reinterpret_cast<uint32_t*>(codes), scale_inv, s, n_tiles);
     return hipGetLastError();
@@ -985,9 +1001,10 @@ int launch_fold_step(const TileEntry* d_entries, int64_t n_slots, const PackArgs
                      float* master, float* m, float* v, uint8_t* codes, float* scale_inv,
                      const StepScalars& s, void* stream) {
     if (n_slots == 0) return hipSuccess;
-    hipError_t err = reserve_lds(reinterpret_cast<const void*>(fold_step_kernel), g_fold_step_lds);
+    const auto kernel = s.grad_scale ? fold_step_kernel<true> : fold_step_kernel<false>;
+    hipError_t err = reserve_lds(reinterpret_cast<const void*>(kernel), g_fold_step_lds[s.grad_scale != nullptr]);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(fold_step_kernel, dim3((uint32_t)n_slots), dim3(kStepThreads),
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)n_slots), dim3(kStepThreads),
                        kStepLdsBytes, (hipStream_t)stream, d_entries, grads, master, m, v,
                        reinterpret_cast<uint32_t*>(codes), scale_inv, s, n_slots);
     return hipGetLastError();
@@ -997,10 +1014,10 @@ int launch_fold_step_unfold(const TileEntry* d_entries, int64_t n_slots, const P
                             const UnpackArgs& outs, float* master, float* m, float* v,
                             uint8_t* codes, float* scale_inv, const StepScalars& s, void* stream) {
     if (n_slots == 0) return hipSuccess;
-    hipError_t err = reserve_lds(reinterpret_cast<const void*>(fold_step_unfold_kernel),
-                                 g_fold_step_unfold_lds);
+    const auto kernel = s.grad_scale ? fold_step_unfold_kernel<true> : fold_step_unfold_kernel<false>;
+    hipError_t err = reserve_lds(reinterpret_cast<const void*>(kernel), g_fold_step_unfold_lds[s.grad_scale != nullptr]);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(fold_step_unfold_kernel, dim3((uint32_t)n_slots), dim3(kStepThreads),
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)n_slots), dim3(kStepThreads),
                        kStepLdsBytes, (hipStream_t)stream, d_entries, grads, outs, master, m, v,
                        reinterpret_cast<uint32_t*>(codes), scale_inv, s, n_slots);
     return hipGetLastError();
@@ -1035,10 +1052,10 @@ int launch_fold_step_unfold_t(const TileEntry* d_entries, int64_t n_slots, const
                               float* m, float* v, uint8_t* codes, float* scale_inv,
                               const StepScalars& s, void* stream) {
     if (n_slots == 0) return hipSuccess;
-    hipError_t err = reserve_lds(reinterpret_cast<const void*>(fold_step_unfold_t_kernel),
-                                 g_fold_step_unfold_t_lds);
+    const auto kernel = s.grad_scale ? fold_step_unfold_t_kernel<true> : fold_step_unfold_t_kernel<false>;
+    hipError_t err = reserve_lds(reinterpret_cast<const void*>(kernel), g_fold_step_unfold_t_lds[s.grad_scale != nullptr]);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(fold_step_unfold_t_kernel, dim3((uint32_t)n_slots), dim3(kStepThreads),
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)n_slots), dim3(kStepThreads),
                        kStepLdsBytes, (hipStream_t)stream, d_entries, grads, outs, touts, master, m, v,
                        reinterpret_cast<uint32_t*>(codes), scale_inv, s, n_slots);
     return hipGetLastError();

@@ -1,0 +1,43 @@
+"""Token embedding and its gradient (include/bfz.h: bfz_embed,
+bfz_embed_grad).  The table may be the row-major FP8 weight and scale grid
+that the step writes; the gradient is the row-major one the step reads.
+"""
+from . import _check, _stream, lib
+from ._tensors import id_vector, matrix, tile_grid, work_pointer
+
+
+def _same(name, got, want):
+    if tuple(got) != tuple(want):
+        raise ValueError(f"{name}: is {tuple(got)}, need {tuple(want)}")
+
+
+def embed(ids, table, out, scale=1.0, grid=None, stream=None):
+    """out[k] = scale * table[ids[k]]; a zero row for an id outside the table.
+    ids: int64 or int32, any shape; table: (vocab, dim) float32, bfloat16,
+    float16, or E4M3 codes (uint8) with their tile scales `grid`; out:
+    (ids.numel(), dim) float32, bfloat16 or float16.  Rows may be strided."""
+    p, wide, n = id_vector(ids, "ids")
+    t, tcode, vocab, dim, tld = matrix(table, "table", codes=True)
+    o, ocode, rows, cols, old = matrix(out, "out")
+    _same("out", (rows, cols), (n, dim))
+    _check(lib().bfz_embed(p, wide, n, t, tcode, tile_grid(grid, tcode, vocab, dim), vocab, dim, tld, float(scale),
+                           o, ocode, old, _stream(stream)))
+
+
+def embed_grad_workspace(n, dim, device="cuda"):
+    """Workspace of embed_grad for up to n tokens of width dim."""
+    import torch
+    return torch.empty(max(16, int(lib().bfz_embed_grad_work_bytes(int(n), int(dim)))), dtype=torch.uint8, device=device)
+
+
+def embed_grad(ids, dout, dtable, work, scale=1.0, accumulate=False, stream=None):
+    """dtable[v] = scale * sum of dout[k] over ids[k] = v, in ascending k; with
+    accumulate the sums are added to dtable and other rows left alone.  dout:
+    (ids.numel(), dim), dtable: (vocab, dim); float32, bfloat16 or float16."""
+    p, wide, n = id_vector(ids, "ids")
+    d, dcode, rows, dim, dld = matrix(dout, "dout")
+    t, tcode, vocab, cols, tld = matrix(dtable, "dtable")
+    _same("dout", (rows, dim), (n, cols))
+    need = lib().bfz_embed_grad_work_bytes(n, dim)
+    _check(lib().bfz_embed_grad(p, wide, n, d, dcode, dld, vocab, dim, float(scale), int(bool(accumulate)), t, tcode,
+                                tld, work_pointer(work, need), _stream(stream)))

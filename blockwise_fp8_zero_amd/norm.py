@@ -1,0 +1,84 @@
+"""Global gradient norm over many tensors, and clipping (include/bfz.h:
+bfz_grad_norm, bfz_shard_grad_norm, bfz_clip_coef, bfz_clip_grads).
+
+    work = bfz.norm_workspace()                                # once
+    bfz.shard_grad_norm(plan, grads, norm, work, max_norm=1.0, coef=coef)
+    bfz.fold_adamw_fp8_step_unpack(plan, grads, ..., hp, grad_scale=coef)
+
+Over several ranks: shard_grad_norm(..., sumsq=s), all_reduce(s), clip_coef(s,
+1.0, norm, coef), then the step.
+"""
+import ctypes as C
+
+from . import _check, _ptr_array, _scalar, _stream, _weight_sizes, lib
+from ._tensors import dtype_code, work_pointer
+
+
+class _Tensor(C.Structure):
+    """bfz_tensor."""
+    _fields_ = [("data", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+def norm_workspace(device="cuda"):
+    """Workspace of the norm calls: zeroed here once, then kept as they leave
+    it.  Calls that may run at the same time (two streams) need one each."""
+    import torch
+    return torch.zeros(int(lib().bfz_norm_work_bytes()), dtype=torch.uint8, device=device)
+
+
+def _list(tensors, name):
+    arr = (_Tensor * max(1, len(tensors)))()
+    for k, t in enumerate(tensors):
+        code = dtype_code(t, f"{name}[{k}]")
+        if not t.is_contiguous():
+            raise TypeError(f"{name}[{k}]: need a contiguous tensor")
+        arr[k] = _Tensor(t.data_ptr(), t.numel(), code, 0)
+    return arr
+
+
+def _results(norm, coef, sumsq):
+    import torch
+    return (None if sumsq is None else _scalar(sumsq, "sumsq", torch.float64),
+            None if norm is None else _scalar(norm, "norm"), None if coef is None else _scalar(coef, "coef"))
+
+
+def _limit(max_norm):
+    return float("inf") if max_norm is None else float(max_norm)
+
+
+def grad_norm(grads, norm, work, max_norm=None, coef=None, sumsq=None, stream=None):
+    """norm = sqrt(sum of g^2 over all of grads) and coef = min(1, max_norm /
+    (norm + 1e-6)), float32 device scalars; sumsq: float64.  Each of the three
+    may be None; max_norm None never clips.  grads: float32, bfloat16 or
+    float16 device tensors of any shapes, mixed as they come."""
+    arr = _list(grads, "grads")
+    s, n, c = _results(norm, coef, sumsq)
+    _check(lib().bfz_grad_norm(C.cast(arr, C.c_void_p), len(grads), _limit(max_norm), s, n, c,
+                               work_pointer(work, lib().bfz_norm_work_bytes()), _stream(stream)))
+
+
+def shard_grad_norm(plan, grads, norm, work, max_norm=None, coef=None, sumsq=None, stream=None):
+    """grad_norm over the tiles the plan's rank owns, read from the row-major
+    float32 gradients grads[p] (None for weights the rank does not touch)."""
+    import torch
+    arr = _ptr_array(grads, torch.float32, "grads", _weight_sizes(plan))
+    s, n, c = _results(norm, coef, sumsq)
+    _check(lib().bfz_shard_grad_norm(plan.handle, C.cast(arr, C.c_void_p), _limit(max_norm), s, n, c,
+                                     work_pointer(work, lib().bfz_norm_work_bytes()), _stream(stream)))
+
+
+def clip_coef(sumsq, max_norm, norm, coef, stream=None):
+    """norm and coef from a device sumsq (float64), e.g. after an all-reduce."""
+    s, n, c = _results(norm, coef, sumsq)
+    _check(lib().bfz_clip_coef(s, _limit(max_norm), n, c, _stream(stream)))
+
+
+def clip_grads(grads, coef, outs=None, stream=None):
+    """outs[k] = grads[k] * coef, rounded once to outs[k]'s type; outs None
+    clips in place."""
+    outs = grads if outs is None else outs
+    if len(outs) != len(grads):
+        raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
+    a, b = _list(grads, "grads"), _list(outs, "outs")
+    _check(lib().bfz_clip_grads(C.cast(a, C.c_void_p), C.cast(b, C.c_void_p), len(grads), _scalar(coef, "coef"),
+                                _stream(stream)))

@@ -351,6 +351,133 @@ int bfz_transpose_pow2(const bfz_plan* plan, const uint8_t* codes, const float* 
  */
 int bfz_e4m3_encode(const float* in, uint8_t* out, int64_t n, void* stream);
 
+/*
+ * The step with its gradient multiplied by a device scalar as it is read
+ * (clipping, see bfz_shard_grad_norm): the same results, bit for bit, as
+ * the call without _clip on gradients g * *grad_scale (one binary32
+ * product), with no pass over the gradients of its own.  grad_scale: device
+ * float, 4-byte aligned, read when the kernel runs.  Other arguments,
+ * results and errors as in adamw_fp8_step_ex, fold_adamw_fp8_step,
+ * fold_adamw_fp8_step_unpack and fold_adamw_fp8_step_unpack_t; a NULL
+ * grad_scale gives BFZ_EINVAL.
+ */
+int bfz_adamw_fp8_step_clip(float* master, const float* grad, float* m, float* v, uint8_t* codes,
+                            float* scale_inv, int64_t n_tiles, const bfz_adamw* hp,
+                            const bfz_step_options* opts, const float* grad_scale, void* stream);
+int bfz_fold_adamw_fp8_step_clip(const bfz_plan* plan, const float* const* grad, float* master,
+                                 float* m, float* v, uint8_t* codes, float* scale_inv,
+                                 const bfz_adamw* hp, const bfz_step_options* opts,
+                                 const float* grad_scale, void* stream);
+int bfz_fold_adamw_fp8_step_unpack_clip(const bfz_plan* plan, const float* const* grad,
+                                        float* master, float* m, float* v, uint8_t* codes,
+                                        float* scale_inv, uint8_t* const* dst_fp8,
+                                        float* const* dst_scale, const bfz_adamw* hp,
+                                        const bfz_step_options* opts, const float* grad_scale,
+                                        void* stream);
+int bfz_fold_adamw_fp8_step_unpack_t_clip(const bfz_plan* plan, const float* const* grad,
+                                          float* master, float* m, float* v, uint8_t* codes,
+                                          float* scale_inv, uint8_t* const* dst_fp8,
+                                          float* const* dst_scale, uint8_t* const* dst_t,
+                                          float* const* dst_t_scale, const bfz_adamw* hp,
+                                          const bfz_step_options* opts, const float* grad_scale,
+                                          void* stream);
+
+/* ---- operators around the step ------------------------------------------
+ * Conventions as above: device pointers are the caller's, calls enqueue
+ * kernels on `stream` and neither allocate nor synchronize.  Strides count
+ * elements; inner strides are 1. */
+
+/* Element types of the operators' tensors. */
+#define BFZ_F32 0
+#define BFZ_BF16 1
+#define BFZ_F16 2
+#define BFZ_E4M3 3 /* codes, with a grid of one float scale per 128x128 tile */
+
+/* n elements back to back at any element alignment. */
+typedef struct {
+    void* data;
+    int64_t n;
+    int32_t dtype; /* BFZ_F32, BFZ_BF16 or BFZ_F16 */
+    int32_t reserved; /* 0 */
+} bfz_tensor;
+
+/*
+ * Global gradient norm over a list of tensors:
+ *   sumsq = sum of g^2 over all of them,  norm = sqrt(sumsq),
+ *   coef  = min(1, max_norm / (norm + 1e-6)).
+ * Squares and sums are binary64 in an order that the sizes alone fix: two
+ * runs give the same bits, and no finite gradient overflows.  grads: host
+ * array of n_tensors (n = 0 elements allowed; n_tensors = 0 gives 0, 0, 1).
+ * max_norm > 0; +Inf never clips.  A NaN among the gradients makes all
+ * three NaN; an Inf makes norm Inf and coef 0 (NaN when max_norm is Inf).
+ * sumsq (double, 8-byte aligned), norm and coef (float): device scalars,
+ * each may be NULL.  work: bfz_norm_work_bytes() of device memory, 16-byte
+ * aligned, zeroed by the caller once before its first use and kept as the
+ * calls leave it; calls that may run at the same time need one each.
+ * One launch for 96 tensors, one more for each further 96.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int64_t bfz_norm_work_bytes(void);
+int bfz_grad_norm(const bfz_tensor* grads, int32_t n_tensors, double max_norm, double* sumsq,
+                  float* norm, float* coef, void* work, void* stream);
+
+/*
+ * The same over the tiles that the plan's rank owns (every valid element of
+ * them, padding excluded), read from the row-major FP32 gradients as
+ * fold_adamw_fp8_step reads them.  The ranks' sumsq add up to the whole
+ * model's: all-reduce it, then bfz_clip_coef.  grad: as in
+ * fold_adamw_fp8_step.  Errors: as bfz_grad_norm, and BFZ_ESTATE.
+ */
+int bfz_shard_grad_norm(const bfz_plan* plan, const float* const* grad, double max_norm,
+                        double* sumsq, float* norm, float* coef, void* work, void* stream);
+
+/* norm and coef (each may be NULL) from a device sumsq.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP. */
+int bfz_clip_coef(const double* sumsq, double max_norm, float* norm, float* coef, void* stream);
+
+/*
+ * Clipping: outs[k] = grads[k] * *coef, product in binary32, rounded once to
+ * outs[k].dtype.  outs[k].n must equal grads[k].n; outs[k].data may be
+ * grads[k].data itself when the types are equal, and must not overlap any
+ * gradient otherwise.  coef: device float.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int bfz_clip_grads(const bfz_tensor* grads, const bfz_tensor* outs, int32_t n_tensors,
+                   const float* coef, void* stream);
+
+/*
+ * Token embedding: out[k][:] = scale * table[ids[k]][:], product in binary32,
+ * rounded once to out's type.  An id outside [0, vocab) gives a zero row.
+ * ids: n of int64 (ids64 != 0) or int32.  table: [vocab, dim], rows table_ld
+ * elements apart; BFZ_E4M3 codes take grid, the row-major scale grid
+ * [ceil(vocab/128), ceil(dim/128)] that unpack_fp8 writes beside them (value =
+ * code * its tile's scale); other types need grid NULL.  out: [n, dim], rows
+ * out_ld apart, BFZ_F32, BFZ_BF16 or BFZ_F16.  Any element alignment; rows on
+ * 16-byte boundaries move fastest.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int bfz_embed(const void* ids, int32_t ids64, int64_t n, const void* table, int32_t table_dtype,
+              const float* grid, int64_t vocab, int64_t dim, int64_t table_ld, float scale,
+              void* out, int32_t out_dtype, int64_t out_ld, void* stream);
+
+/*
+ * Its gradient: dtable[v][:] = scale * sum of dout[k][:] over the k with
+ * ids[k] = v, in ascending k, summed in binary32; ids outside [0, vocab) add
+ * nothing.  accumulate = 0: the whole table is written, zero rows included;
+ * otherwise rows that occur are added to dtable and the others not touched.
+ * The tokens are sorted first, so every sum has a fixed order: two runs give
+ * the same bits.  dout: [n, dim]; dtable: [vocab, dim]; each BFZ_F32, BFZ_BF16
+ * or BFZ_F16.  work: bfz_embed_grad_work_bytes(n, dim) of device memory,
+ * 16-byte aligned, not shared by calls that may run at the same time.
+ * At most 2^27 tokens and 2^27 rows.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int64_t bfz_embed_grad_work_bytes(int64_t n, int64_t dim);
+int bfz_embed_grad(const void* ids, int32_t ids64, int64_t n, const void* dout,
+                   int32_t dout_dtype, int64_t dout_ld, int64_t vocab, int64_t dim, float scale,
+                   int32_t accumulate, void* dtable, int32_t dtable_dtype, int64_t dtable_ld,
+                   void* work, void* stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char* bfz_last_error(void);
 
