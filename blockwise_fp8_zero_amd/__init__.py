@@ -89,6 +89,11 @@ def lib():
         L.bfz_embed_grad_work_bytes.argtypes = [i64, i64]
         L.bfz_embed_grad_work_bytes.restype = i64
         L.bfz_embed_grad.argtypes = [P, i32, i64, P, i32, i64, i64, i64, f32, i32, P, i32, i64, P, P]
+        L.bfz_vocab_loss_work_bytes.argtypes = [i64, i64, i64, i32, i32]
+        L.bfz_vocab_loss_work_bytes.restype = i64
+        L.bfz_vocab_loss.argtypes = [P, i64, i64, P, i32, i64, P, i64, i64, P, i32, P, P, P, P]
+        L.bfz_vocab_loss_grad.argtypes = [P, i64, i64, P, i32, i64, P, i64, i64, P, i32, P, P, P, i64, P, i32, i64, i32,
+                                          P, P]
         L.bfz_last_error.argtypes = []
         L.bfz_last_error.restype = C.c_char_p
         _lib = L
@@ -436,3 +441,4 @@ def e4m3_encode(x, out, stream=None):
 
 from .norm import clip_coef, clip_grads, grad_norm, norm_workspace, shard_grad_norm  # noqa: E402
 from .embedding import embed, embed_grad, embed_grad_workspace  # noqa: E402
+from .vocab_loss import vocab_loss, vocab_loss_grad, vocab_loss_workspace  # noqa: E402

@@ -7,7 +7,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbfz.so")
-SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip", "ops_abi.cpp", "norm.hip", "embedding.hip"]
+SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip", "ops_abi.cpp", "norm.hip", "embedding.hip",
+           "vocab_loss.hip"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

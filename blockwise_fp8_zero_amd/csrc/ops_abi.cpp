@@ -228,3 +228,105 @@ extern "C" int bfz_embed_grad(const void* ids, int32_t ids64, int64_t n, const v
     const EmbedGradArgs a{ids, ids64, dout_dtype, dtable_dtype, dout, dtable, n, vocab, dim, dout_ld, dtable_ld, scale, accumulate};
     return launched(where, launch_embed_grad(a, work, stream));
 }
+
+namespace {
+
+int check_loss(const void* hidden, int64_t hidden_ld, int64_t n, const void* weight, int32_t weight_dtype, int64_t weight_ld,
+               const float* grid, int64_t vocab, int64_t dim, const void* targets, int32_t targets64, const void* work,
+               const char* where) {
+    if (n < 0 || vocab < 1 || dim < 1 || n > (int64_t(1) << 24) || vocab > (int64_t(1) << 27) || dim > (int64_t(1) << 20))
+        return fail(BFZ_EINVAL, "%s: need 0 <= n <= 2^24, 1 <= vocab <= 2^27, 1 <= dim <= 2^20", where);
+    // a launch counts its work-items in 32 bits: under 2^23 tiles of 512
+    if (((vocab + 255) / 256) * ((n + 63) / 64) >= (int64_t(1) << 23))
+        return fail(BFZ_EINVAL, "%s: %lld tokens by %lld rows are too many for one call", where, (long long)n, (long long)vocab);
+    if (weight_dtype != kBF16 && weight_dtype != kE4M3)
+        return fail(BFZ_EINVAL, "%s: the weight must be BFZ_BF16 or BFZ_E4M3", where);
+    if ((weight_dtype == kE4M3) != (grid != nullptr))
+        return fail(BFZ_EINVAL, "%s: E4M3 codes need their scale grid, bf16 weights none", where);
+    if (!aligned(grid, 4)) return fail(BFZ_EALIGN, "%s: grid must be 4-byte aligned", where);
+    if (hidden_ld > (int64_t(1) << 21) || weight_ld > (int64_t(1) << 21))
+        return fail(BFZ_EINVAL, "%s: strides are at most 2^21", where);
+    int rc = check_matrix(hidden, kBF16, n, dim, hidden_ld, "hidden", where);
+    if (!rc) rc = check_matrix(weight, weight_dtype, vocab, dim, weight_ld, "weight", where);
+    if (rc) return rc;
+    if (n > 0 && !targets) return fail(BFZ_EINVAL, "%s: null pointer", where);
+    if (!aligned(targets, targets64 ? 8 : 4)) return fail(BFZ_EALIGN, "%s: targets must be aligned to their elements", where);
+    if (!work) return fail(BFZ_EINVAL, "%s: null workspace", where);
+    if (!aligned(work, 256)) return fail(BFZ_EALIGN, "%s: the workspace must be 256-byte aligned", where);
+    return BFZ_OK;
+}
+
+}  // namespace
+
+extern "C" int64_t bfz_vocab_loss_work_bytes(int64_t n, int64_t vocab, int64_t dim, int32_t weight_dtype, int32_t grad) {
+    if (n < 0 || vocab < 1 || dim < 1 || n > (int64_t(1) << 24) || vocab > (int64_t(1) << 27) || dim > (int64_t(1) << 20) ||
+        (weight_dtype != kBF16 && weight_dtype != kE4M3))
+        return 0;
+    return vocab_loss_work_bytes(n, vocab, dim, weight_dtype == kE4M3, grad != 0);
+}
+
+extern "C" int bfz_vocab_loss(const void* hidden, int64_t hidden_ld, int64_t n, const void* weight, int32_t weight_dtype,
+                              int64_t weight_ld, const float* grid, int64_t vocab, int64_t dim, const void* targets,
+                              int32_t targets64, float* loss, float* lse, void* work, void* stream) {
+    const char* where = "bfz_vocab_loss";
+    const int rc = check_loss(hidden, hidden_ld, n, weight, weight_dtype, weight_ld, grid, vocab, dim, targets, targets64, work, where);
+    if (rc) return rc;
+    if (n > 0 && (!loss || !lse)) return fail(BFZ_EINVAL, "%s: null pointer", where);
+    if (!aligned(loss, 4) || !aligned(lse, 4)) return fail(BFZ_EALIGN, "%s: loss and lse must be 4-byte aligned", where);
+    VocabLossArgs a{};
+    a.hidden = hidden;
+    a.weight = weight;
+    a.grid = grid;
+    a.targets = targets;
+    a.targets64 = targets64;
+    a.fp8 = weight_dtype == kE4M3;
+    a.n = n;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.hidden_ld = hidden_ld;
+    a.weight_ld = weight_ld;
+    a.loss = loss;
+    a.lse = lse;
+    return launched(where, launch_vocab_loss(a, work, stream));
+}
+
+extern "C" int bfz_vocab_loss_grad(const void* hidden, int64_t hidden_ld, int64_t n, const void* weight, int32_t weight_dtype,
+                                   int64_t weight_ld, const float* grid, int64_t vocab, int64_t dim, const void* targets,
+                                   int32_t targets64, const float* lse, const float* dloss, void* dhidden, int64_t dhidden_ld,
+                                   void* dweight, int32_t dweight_dtype, int64_t dweight_ld, int32_t accumulate, void* work,
+                                   void* stream) {
+    const char* where = "bfz_vocab_loss_grad";
+    int rc = check_loss(hidden, hidden_ld, n, weight, weight_dtype, weight_ld, grid, vocab, dim, targets, targets64, work, where);
+    if (rc) return rc;
+    if (n > 0 && (!lse || !dloss)) return fail(BFZ_EINVAL, "%s: null pointer", where);
+    if (!aligned(lse, 4) || !aligned(dloss, 4)) return fail(BFZ_EALIGN, "%s: lse and dloss must be 4-byte aligned", where);
+    if (dhidden) rc = check_matrix(dhidden, kBF16, n, dim, dhidden_ld, "dhidden", where);
+    if (rc) return rc;
+    if (dweight) {
+        if (dweight_dtype != kBF16 && dweight_dtype != kF32)
+            return fail(BFZ_EINVAL, "%s: dweight must be BFZ_BF16 or BFZ_F32", where);
+        rc = check_matrix(dweight, dweight_dtype, vocab, dim, dweight_ld, "dweight", where);
+        if (rc) return rc;
+    }
+    VocabLossArgs a{};
+    a.hidden = hidden;
+    a.weight = weight;
+    a.grid = grid;
+    a.targets = targets;
+    a.targets64 = targets64;
+    a.fp8 = weight_dtype == kE4M3;
+    a.n = n;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.hidden_ld = hidden_ld;
+    a.weight_ld = weight_ld;
+    a.lse = const_cast<float*>(lse);
+    a.dloss = dloss;
+    a.dhidden = dhidden;
+    a.dhidden_ld = dhidden_ld;
+    a.dweight = dweight;
+    a.dweight_type = dweight_dtype;
+    a.dweight_ld = dweight_ld;
+    a.accumulate = accumulate;
+    return launched(where, launch_vocab_loss_grad(a, work, stream));
+}

@@ -1,0 +1,412 @@
+// The matrix product under the vocabulary loss and its gradient:
+//
+//   D[m][n] = sum over k of A[m][k] B[n][k]
+//
+// in binary32 on the matrix cores, from bf16 or E4M3 A and bf16 B, with the
+// result handed in registers to an epilogue (softmax statistics, gradient of
+// the logits, or a plain store).
+//
+// A workgroup of 8 waves owns a 256 x kBN tile and walks k in steps of 64.
+// Each step's operands go from memory straight into LDS (16 bytes a lane),
+// one step ahead of their use: while a step is multiplied, the next one is in
+// flight.  Every step has two halves of 32 k, and a half's fragments are read
+// from LDS while the other half is multiplied, so that one barrier a step is
+// enough and it falls where all reads of the step are done.
+//
+// Operands come in two layouts.  KC: k is contiguous (rows of m or n).  KR: m
+// or n is contiguous (rows of k); its fragments are read with the LDS
+// transpose instructions, so that no operand is ever transposed in memory.
+// LDS rows have no padding (the direct loads write lanes back to back);
+// instead a row's 16- or 32-byte pieces are permuted by an XOR with its row
+// number, chosen so that the lanes that read together touch all banks.
+//
+// E4M3 codes become bf16 exactly; their tile scales are applied to the
+// binary32 sums.  A wave's rows lie in one 128-row tile, so its scale
+// changes only with k: the sums are kept in units of the current tile's scale
+// and multiplied by old / new scale every 128 k.  (A second set of sums in
+// unscaled units would not fit the registers.)  Where a scale is less than
+// 2^-60 of the unit in use, the tile's codes are multiplied by 2^-127
+// instead: what it adds is below 2^-60 of that unit.
+#pragma once
+
+#include "ops_device.h"
+#include "ops_internal.h"
+
+namespace bfz {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kGemmThreads = 512, kGemmWaves = 8;
+constexpr int kBM = 256;
+constexpr int kBK = 64;
+
+struct Operand {
+    const void* p;
+    int64_t ld;      // bytes from row to row
+    int64_t extent;  // valid m (or n)
+    int64_t k;       // valid k; beyond both, zero
+};
+
+struct GemmArgs {
+    Operand a, b;
+    int64_t k;             // k to walk
+    int64_t k_per_split;   // multiple of 128
+    const float* grid;     // scale of A's tile (m / 128, k / 128), or null
+    int64_t grid_m, grid_k;      // its strides
+    int64_t blocks_m, blocks_k;  // its sizes
+    int32_t tiles_m, tiles_n, splits, group_m;
+};
+
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // beyond every buffer: loads give zero
+constexpr uint32_t kBufferBytes = 0x80000000u;
+
+__device__ __forceinline__ i32x4 buffer_of(const char* base) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    r[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu));
+    r[2] = (int)kBufferBytes;
+    r[3] = 0x00020000;
+    return r;
+}
+
+// 16 bytes a lane from memory to LDS at lds + 16 * lane.  In assembly, so
+// that the compiler does not wait for it at the next LDS read: it has no
+// result register, and wait_loads() stands before the barrier that publishes
+// what it wrote.
+__device__ __forceinline__ void load_to_lds(const i32x4& buf, uint32_t offset, uint32_t lds) {
+    __asm__ volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds"
+        :
+        : "s"(lds), "v"(offset), "s"(buf)
+        : "memory");
+}
+
+__device__ __forceinline__ void wait_loads() { __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+    return (uint32_t)reinterpret_cast<uintptr_t>((lds_char*)p);
+}
+
+template <class T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+    return *(__attribute__((address_space(3))) const T*)(uintptr_t)at;
+}
+
+// ---- operand layouts ----------------------------------------------------------
+// kRows: the tile's extent in m or n.  Each gives: bytes of a stage; the loads a
+// wave issues for it (offset of load j; which k, or row of k, a lane's load
+// covers, for the tail); the registers of a fragment and how it is read.
+
+template <int kRows>
+struct BF16KC {
+    static constexpr int kBytes = kRows * kBK * 2;
+    static constexpr int kLoads = kBytes / 1024 / kGemmWaves;
+    static_assert(kLoads >= 1, "a stage has a load for each wave");
+    static constexpr bool kScaled = false;
+    typedef bf16x8 Frag;
+    uint32_t at[2];  // LDS offset of tile 0's fragment, by half
+    __device__ __forceinline__ static const char* base(const Operand& o, int64_t row0, int64_t k0) {
+        return static_cast<const char*>(o.p) + row0 * o.ld + k0 * 2;
+    }
+    __device__ __forceinline__ static int64_t advance(const Operand&) { return kBK * 2; }
+    __device__ __forceinline__ static int k_of(int, int, int lane) { return 8 * ((lane & 7) ^ (lane >> 3)); }
+    __device__ __forceinline__ static uint32_t offset(const Operand& o, int64_t row0, int j, int wave, int lane) {
+        const int row = (j * kGemmWaves + wave) * 8 + (lane >> 3);
+        return row0 + row < o.extent ? (uint32_t)(row * o.ld) + 16u * ((lane & 7) ^ (lane >> 3)) : kNowhere;
+    }
+    __device__ __forceinline__ BF16KC(uint32_t lds, int row0, int lane) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) at[h] = lds + (row0 + (lane & 15)) * 128 + (((4 * h + (lane >> 4)) ^ (lane & 7)) << 4);
+    }
+    __device__ __forceinline__ Frag read(uint32_t stage, int h, int t) const {
+        return lds_read<bf16x8>(at[h] + stage + t * 2048);
+    }
+    __device__ __forceinline__ static bf16x8 value(const Frag& f, float) { return f; }
+};
+
+__device__ __forceinline__ bf16x8 codes_to_bf16(const u32x2& c, float keep) {
+    bf16x8 r;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[w], keep, false);
+        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[w], keep, true);
+        r[4 * w] = lo[0];
+        r[4 * w + 1] = lo[1];
+        r[4 * w + 2] = hi[0];
+        r[4 * w + 3] = hi[1];
+    }
+    return r;
+}
+
+template <int kRows>
+struct FP8KC {
+    static constexpr int kBytes = kRows * kBK;
+    static constexpr int kLoads = kBytes / 1024 / kGemmWaves;
+    static constexpr bool kScaled = true;
+    typedef u32x2 Frag;
+    uint32_t at[2];
+    __device__ __forceinline__ static const char* base(const Operand& o, int64_t row0, int64_t k0) {
+        return static_cast<const char*>(o.p) + row0 * o.ld + k0;
+    }
+    __device__ __forceinline__ static int64_t advance(const Operand&) { return kBK; }
+    __device__ __forceinline__ static int k_of(int, int, int lane) { return 16 * ((lane & 3) ^ ((lane >> 3) & 3)); }
+    __device__ __forceinline__ static uint32_t offset(const Operand& o, int64_t row0, int j, int wave, int lane) {
+        const int row = (j * kGemmWaves + wave) * 16 + (lane >> 2);
+        return row0 + row < o.extent ? (uint32_t)(row * o.ld) + 16u * ((lane & 3) ^ ((lane >> 3) & 3)) : kNowhere;
+    }
+    __device__ __forceinline__ FP8KC(uint32_t lds, int row0, int lane) {
+        const int g = lane >> 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            at[h] = lds + (row0 + (lane & 15)) * 64 + (((2 * h + (g >> 1)) ^ ((lane >> 1) & 3)) << 4) + 8 * (g & 1);
+    }
+    __device__ __forceinline__ Frag read(uint32_t stage, int h, int t) const {
+        return lds_read<u32x2>(at[h] + stage + t * 1024);
+    }
+    __device__ __forceinline__ static bf16x8 value(const Frag& f, float keep) { return codes_to_bf16(f, keep); }
+};
+
+// kTiles: the 16-wide tiles a wave reads.
+template <int kRows, int kTiles>
+struct BF16KR {
+    static constexpr int kBytes = kRows * kBK * 2;
+    static constexpr int kLoads = kBytes / 1024 / kGemmWaves;
+    static constexpr int kPieces = kRows * 2 / 16;  // 16-byte pieces of a row
+    static_assert(kRows == 256, "the permutation spans a 512-byte row");
+    static constexpr bool kScaled = false;
+    typedef bf16x8 Frag;
+    uint32_t at[kTiles];
+    __device__ __forceinline__ static const char* base(const Operand& o, int64_t row0, int64_t k0) {
+        return static_cast<const char*>(o.p) + k0 * o.ld + row0 * 2;
+    }
+    __device__ __forceinline__ static int64_t advance(const Operand& o) { return kBK * o.ld; }
+    __device__ __forceinline__ static int k_of(int j, int wave, int lane) { return (j * kGemmWaves + wave) * 2 + (lane >> 5); }
+    __device__ __forceinline__ static uint32_t offset(const Operand& o, int64_t row0, int j, int wave, int lane) {
+        const int k = k_of(j, wave, lane);
+        const int x = (k & 3) | (((k >> 3) & 3) << 2);
+        const int piece = (lane & 31) ^ (x << 1);
+        return row0 + 8 * piece < o.extent ? (uint32_t)(k * o.ld) + 16u * piece : kNowhere;
+    }
+    __device__ __forceinline__ BF16KR(uint32_t lds, int row0, int lane) {
+        const int k = 8 * (lane >> 4) + ((lane & 15) >> 2);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+            at[t] = lds + k * 512 + (((row0 / 16 + t) ^ (lane >> 2)) << 5) + 8 * (lane & 3);
+    }
+    __device__ __forceinline__ Frag read(uint32_t stage, int h, int t) const {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const uint32_t p = at[t] + stage + h * 32 * 512;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)p);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(p + 4 * 512));
+        const s16x8 r = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        return __builtin_bit_cast(bf16x8, r);
+    }
+    __device__ __forceinline__ static bf16x8 value(const Frag& f, float) { return f; }
+};
+
+template <int kRows, int kTiles>
+struct FP8KR {
+    static constexpr int kBytes = kRows * kBK;
+    static constexpr int kLoads = kBytes / 1024 / kGemmWaves;
+    static_assert(kRows == 256, "the permutation spans a 256-byte row");
+    static constexpr bool kScaled = true;
+    typedef u32x2 Frag;
+    uint32_t at[kTiles];
+    __device__ __forceinline__ static const char* base(const Operand& o, int64_t row0, int64_t k0) {
+        return static_cast<const char*>(o.p) + k0 * o.ld + row0;
+    }
+    __device__ __forceinline__ static int64_t advance(const Operand& o) { return kBK * o.ld; }
+    __device__ __forceinline__ static int k_of(int j, int wave, int lane) { return (j * kGemmWaves + wave) * 4 + (lane >> 4); }
+    __device__ __forceinline__ static uint32_t offset(const Operand& o, int64_t row0, int j, int wave, int lane) {
+        const int k = k_of(j, wave, lane);
+        const int piece = (lane & 15) ^ (k & 15);
+        return row0 + 16 * piece < o.extent ? (uint32_t)(k * o.ld) + 16u * piece : kNowhere;
+    }
+    __device__ __forceinline__ FP8KR(uint32_t lds, int row0, int lane) {
+        const int k = 8 * (lane >> 4) + ((lane & 15) >> 1);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+            at[t] = lds + k * 256 + (((row0 / 16 + t) ^ (k & 15)) << 4) + 8 * (lane & 1);
+    }
+    __device__ __forceinline__ Frag read(uint32_t stage, int h, int t) const {
+        typedef int i32x2 __attribute__((ext_vector_type(2)));
+        typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+        const i32x2 r = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(uintptr_t)(at[t] + stage + h * 32 * 256));
+        return __builtin_bit_cast(u32x2, r);
+    }
+    __device__ __forceinline__ static bf16x8 value(const Frag& f, float keep) { return codes_to_bf16(f, keep); }
+};
+
+// ---- tile order -----------------------------------------------------------------
+// Workgroups are dealt to the 8 XCDs in turn; each XCD takes one contiguous
+// eighth of the tiles, in groups of group_m tiles of m by all n, so the
+// workgroups that run on it together share operands in its L2.
+__device__ __forceinline__ void tile_of(const GemmArgs& g, int& tm, int& tn, int& split) {
+    const int total = g.tiles_m * g.tiles_n * g.splits;
+    const int b = blockIdx.x, x = b & 7, each = total >> 3, more = total & 7;
+    int l = x * each + min(x, more) + (b >> 3);
+    split = l / (g.tiles_m * g.tiles_n);
+    l -= split * g.tiles_m * g.tiles_n;
+    const int group = l / (g.group_m * g.tiles_n);
+    const int m0 = group * g.group_m;
+    const int width = min(g.group_m, g.tiles_m - m0);
+    const int in = l - group * g.group_m * g.tiles_n;
+    tm = m0 + in % width;
+    tn = in / width;
+}
+
+// Where a wave's results lie: its rows m0 + 16 t + 4 (lane / 16) + i, i < 4, of
+// columns n0 + 16 u + lane % 16.
+struct WaveTile {
+    int64_t m0, n0;
+    int tile_m, wave_m, split, lane;
+};
+
+template <class A, class B, int kBN, int kWavesM, class Epilogue>
+__global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilogue epilogue) {
+    constexpr int kWavesN = kGemmWaves / kWavesM;
+    constexpr int kTM = kBM / kWavesM / 16, kTN = kBN / kWavesN / 16;
+    constexpr int kStage = A::kBytes + B::kBytes;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / kWavesN, wn = wave % kWavesN;
+    int tm, tn, split;
+    tile_of(g, tm, tn, split);
+    const int64_t m0 = (int64_t)tm * kBM, n0 = (int64_t)tn * kBN;
+    const int64_t k0 = split * g.k_per_split;
+    const int64_t k1 = min(g.k, k0 + g.k_per_split);
+    const int steps = (int)((max(k1 - k0, (int64_t)0) + kBK - 1) / kBK);
+
+    const uint32_t lds = lds_address(smem);
+    const A fa(lds, wm * kTM * 16, lane);
+    const B fb(lds + A::kBytes, wn * kTN * 16, lane);
+    uint32_t off_a[A::kLoads], off_b[B::kLoads];
+#pragma unroll
+    for (int j = 0; j < A::kLoads; ++j) off_a[j] = A::offset(g.a, m0, j, wave, lane);
+#pragma unroll
+    for (int j = 0; j < B::kLoads; ++j) off_b[j] = B::offset(g.b, n0, j, wave, lane);
+    const char* base_a = A::base(g.a, m0, k0);
+    const char* base_b = B::base(g.b, n0, k0);
+    const int64_t adv_a = A::advance(g.a), adv_b = B::advance(g.b);
+    const uint32_t lds_a = lds + wave * 1024, lds_b = lds_a + A::kBytes;
+
+    // loads of step s into its buffer; past the end of k they give zero
+    auto issue = [&](int s) {
+        const uint32_t stage = (s & 1) ? kStage : 0;
+        const i32x4 ra = buffer_of(base_a), rb = buffer_of(base_b);
+        base_a += adv_a;
+        base_b += adv_b;
+        const int64_t left_a = g.a.k - (k0 + (int64_t)s * kBK), left_b = g.b.k - (k0 + (int64_t)s * kBK);
+        if (left_a >= kBK && left_b >= kBK) {
+#pragma unroll
+            for (int j = 0; j < A::kLoads; ++j) load_to_lds(ra, off_a[j], lds_a + stage + j * (kGemmWaves * 1024));
+#pragma unroll
+            for (int j = 0; j < B::kLoads; ++j) load_to_lds(rb, off_b[j], lds_b + stage + j * (kGemmWaves * 1024));
+        } else {
+#pragma unroll
+            for (int j = 0; j < A::kLoads; ++j)
+                load_to_lds(ra, A::k_of(j, wave, lane) < left_a ? off_a[j] : kNowhere, lds_a + stage + j * (kGemmWaves * 1024));
+#pragma unroll
+            for (int j = 0; j < B::kLoads; ++j)
+                load_to_lds(rb, B::k_of(j, wave, lane) < left_b ? off_b[j] : kNowhere, lds_b + stage + j * (kGemmWaves * 1024));
+        }
+    };
+
+    f32x4 acc[kTM][kTN];
+#pragma unroll
+    for (int t = 0; t < kTM; ++t)
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    typename A::Frag a[2][kTM];
+    typename B::Frag b[2][kTN];
+    auto read_half = [&](int s, int h) {
+        const uint32_t stage = (s & 1) ? kStage : 0;
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) b[h][u] = fb.read(stage, h, u);
+#pragma unroll
+        for (int t = 0; t < kTM; ++t) a[h][t] = fa.read(stage, h, t);
+    };
+
+    // scale of this wave's A tiles in 128-k block kb
+    float unit = 1.0f, keep = 1.0f;
+    const float* grid_row = nullptr;
+    if constexpr (A::kScaled) grid_row = g.grid + min((m0 + wm * kTM * 16) / kTileDim, g.blocks_m - 1) * g.grid_m;
+    auto scale_at = [&](int64_t kb) { return grid_row[min(kb, g.blocks_k - 1) * g.grid_k]; };
+    float next_scale = 1.0f;
+    if constexpr (A::kScaled) {
+        unit = scale_at(k0 / kTileDim);
+        next_scale = scale_at(k0 / kTileDim + 1);
+    }
+
+    auto multiply = [&](int h) {
+#pragma unroll
+        for (int t = 0; t < kTM; ++t) {
+            const bf16x8 av = A::value(a[h][t], keep);
+#pragma unroll
+            for (int u = 0; u < kTN; ++u)
+                acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, B::value(b[h][u], 1.0f), acc[t][u], 0, 0, 0);
+        }
+    };
+
+    if (steps > 0) {
+        issue(0);
+        if (steps > 1) issue(1);
+        wait_loads();
+        __builtin_amdgcn_s_barrier();
+        read_half(0, 0);
+        for (int s = 0; s < steps; ++s) {
+            if constexpr (A::kScaled) {
+                if ((s & 1) == 0 && s > 0) {
+                    const float scale = next_scale;
+                    next_scale = scale_at(k0 / kTileDim + s / 2 + 1);
+                    const float ratio = unit / scale;
+                    if (ratio <= 0x1p60f) {
+                        keep = 1.0f;
+                        unit = scale;
+                        if (ratio != 1.0f) {
+#pragma unroll
+                            for (int t = 0; t < kTM; ++t)
+#pragma unroll
+                                for (int u = 0; u < kTN; ++u)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) acc[t][u][i] *= ratio;
+                        }
+                    } else {
+                        keep = 0.0f;  // the conversion takes it as 2^-127
+                    }
+                }
+            }
+            read_half(s, 1);
+            multiply(0);
+            wait_loads();
+            __builtin_amdgcn_s_barrier();
+            if (s + 2 < steps) issue(s + 2);
+            if (s + 1 < steps) read_half(s + 1, 0);
+            multiply(1);
+        }
+    }
+    if constexpr (A::kScaled) {
+#pragma unroll
+        for (int t = 0; t < kTM; ++t)
+#pragma unroll
+            for (int u = 0; u < kTN; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][u][i] *= unit;
+    }
+    const WaveTile w{m0 + wm * kTM * 16, n0 + wn * kTN * 16, tm, wm, split, lane};
+    epilogue.template run<kTM, kTN>(acc, w);
+}
+
+}  // namespace bfz

@@ -1,0 +1,63 @@
+"""Softmax cross entropy over a large vocabulary, and its gradient, without
+the logits in memory (include/bfz.h: bfz_vocab_loss, bfz_vocab_loss_grad).  The
+head's weight may be the row-major FP8 weight and scale grid that the step
+writes.
+"""
+from . import _check, _dev, _stream, lib
+from ._tensors import BF16, E4M3, F32, id_vector, matrix, tile_grid, work_pointer
+
+
+def vocab_loss_workspace(n, vocab, dim, weight_dtype=None, grad=True, device="cuda"):
+    """Workspace of vocab_loss and, with grad, vocab_loss_grad for n tokens.
+    weight_dtype: torch.bfloat16, or torch.uint8 (the default) for E4M3 codes."""
+    import torch
+    code = BF16 if weight_dtype == torch.bfloat16 else E4M3
+    need = int(lib().bfz_vocab_loss_work_bytes(int(n), int(vocab), int(dim), code, int(bool(grad))))
+    return torch.empty(max(16, need), dtype=torch.uint8, device=device)
+
+
+def _operands(hidden, weight, targets, grid):
+    h, hcode, n, dim, hld = matrix(hidden, "hidden")
+    w, wcode, vocab, cols, wld = matrix(weight, "weight", codes=True)
+    t, wide, count = id_vector(targets, "targets")
+    if hcode != BF16 or wcode not in (BF16, E4M3):
+        raise TypeError("hidden: need bfloat16; weight: bfloat16 or E4M3 codes")
+    if cols != dim or count != n:
+        raise ValueError(f"hidden is {(n, dim)}, weight {(vocab, cols)}, targets {count}")
+    return [h, hld, n, w, wcode, wld, tile_grid(grid, wcode, vocab, dim), vocab, dim, t, wide], n, vocab, dim, wcode
+
+
+def _work(work, n, vocab, dim, wcode, grad):
+    return work_pointer(work, lib().bfz_vocab_loss_work_bytes(n, vocab, dim, wcode, grad))
+
+
+def vocab_loss(hidden, weight, targets, loss, lse, work, grid=None, stream=None):
+    """loss[k] = lse[k] - z[k, targets[k]] and lse[k] = log sum exp z[k] with
+    z = hidden weight^T; loss 0 for a target outside the vocabulary.  hidden:
+    (n, dim) bfloat16; weight: (vocab, dim) bfloat16, or E4M3 codes (uint8) with
+    their tile scales `grid`; targets: int64 or int32; loss, lse: float32 (n)."""
+    import torch
+    args, n, vocab, dim, wcode = _operands(hidden, weight, targets, grid)
+    _check(lib().bfz_vocab_loss(*args, _dev(loss, torch.float32, "loss", n), _dev(lse, torch.float32, "lse", n),
+                                _work(work, n, vocab, dim, wcode, 0), _stream(stream)))
+
+
+def vocab_loss_grad(hidden, weight, targets, lse, dloss, dhidden, dweight, work, grid=None, accumulate=False,
+                    stream=None):
+    """Gradient of sum(dloss * loss): dhidden (n, dim) bfloat16 and dweight
+    (vocab, dim) bfloat16 or float32, each may be None.  lse: as vocab_loss
+    wrote it; dloss: float32 (n).  accumulate adds to dweight."""
+    import torch
+    args, n, vocab, dim, wcode = _operands(hidden, weight, targets, grid)
+    dh = dw = (None, 0, 0, 0, 0)
+    if dhidden is not None:
+        dh = matrix(dhidden, "dhidden")
+        if dh[1] != BF16 or dh[2:4] != (n, dim):
+            raise ValueError(f"dhidden: need bfloat16 {(n, dim)}")
+    if dweight is not None:
+        dw = matrix(dweight, "dweight")
+        if dw[1] not in (BF16, F32) or dw[2:4] != (vocab, dim):
+            raise ValueError(f"dweight: need bfloat16 or float32 {(vocab, dim)}")
+    _check(lib().bfz_vocab_loss_grad(*args, _dev(lse, torch.float32, "lse", n), _dev(dloss, torch.float32, "dloss", n),
+                                     dh[0], dh[4], dw[0], dw[1], dw[4], int(bool(accumulate)),
+                                     _work(work, n, vocab, dim, wcode, 1), _stream(stream)))

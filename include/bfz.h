@@ -478,6 +478,49 @@ int bfz_embed_grad(const void* ids, int32_t ids64, int64_t n, const void* dout,
                    int32_t accumulate, void* dtable, int32_t dtable_dtype, int64_t dtable_ld,
                    void* work, void* stream);
 
+/*
+ * Softmax cross entropy over a large vocabulary.  With z = hidden weight^T
+ * (products of bf16 and bf16 or E4M3 values, summed in binary32) and
+ * t = targets[k]:
+ *   lse[k]  = log sum_v exp z[k][v]
+ *   loss[k] = lse[k] - z[k][t], or 0 when t lies outside [0, vocab)
+ * The logits are reduced as they are computed, never stored.
+ * hidden: bf16 [n, dim], rows hidden_ld elements apart.  weight: [vocab, dim],
+ * BFZ_BF16 (grid NULL) or BFZ_E4M3 codes with their row-major scale grid
+ * [ceil(vocab/128), ceil(dim/128)], as the step writes both.  Rows that start
+ * on 16-byte boundaries and are a multiple of 16 bytes wide are read in
+ * place; others are first copied into the workspace.  targets: n of int64
+ * (targets64 != 0) or int32.  loss, lse: n floats.
+ * work: bfz_vocab_loss_work_bytes(n, vocab, dim, weight_dtype, grad) of device
+ * memory, 256-byte aligned, not shared by calls that may run at the same time
+ * (grad != 0 covers both calls; 0: bad sizes).  At most 2^24 tokens, 2^27
+ * rows, dim 2^20, strides 2^21.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int64_t bfz_vocab_loss_work_bytes(int64_t n, int64_t vocab, int64_t dim, int32_t weight_dtype,
+                                  int32_t grad);
+int bfz_vocab_loss(const void* hidden, int64_t hidden_ld, int64_t n, const void* weight,
+                   int32_t weight_dtype, int64_t weight_ld, const float* grid, int64_t vocab,
+                   int64_t dim, const void* targets, int32_t targets64, float* loss, float* lse,
+                   void* work, void* stream);
+
+/*
+ * Its gradient for the upstream gradient dloss[k] of each loss:
+ *   dz[k][v] = dloss[k] (exp(z[k][v] - lse[k]) - [v = t]), 0 for a target
+ *   outside [0, vocab);  dhidden = dz weight;  dweight = dz^T hidden.
+ * lse: as bfz_vocab_loss wrote it.  dz is rounded to bf16 before the two
+ * products, which sum in binary32.  dhidden (bf16 [n, dim]) and dweight
+ * (BFZ_BF16 or BFZ_F32 [vocab, dim]) are written whole, each may be NULL;
+ * accumulate != 0 adds to dweight instead.  Every sum has a fixed order:
+ * two runs give the same bits.  Other arguments, limits and errors as above.
+ */
+int bfz_vocab_loss_grad(const void* hidden, int64_t hidden_ld, int64_t n, const void* weight,
+                        int32_t weight_dtype, int64_t weight_ld, const float* grid, int64_t vocab,
+                        int64_t dim, const void* targets, int32_t targets64, const float* lse,
+                        const float* dloss, void* dhidden, int64_t dhidden_ld, void* dweight,
+                        int32_t dweight_dtype, int64_t dweight_ld, int32_t accumulate, void* work,
+                        void* stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char* bfz_last_error(void);
 

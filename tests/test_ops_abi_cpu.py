@@ -126,3 +126,46 @@ def test_binding_refuses_host_tensors():
         bfz.embed(torch.zeros(4, dtype=torch.long), x, x)
     with pytest.raises(TypeError):
         bfz.embed_grad(torch.zeros(4, dtype=torch.long), x, x, x)
+
+
+def _loss(grad=False, hidden=A, hld=8, n=4, weight=B, wt=1, wld=8, grid=None, V=10, d=8, t=P(0x40000), wide=1, loss=P(0x50000),
+          lse=P(0x60000), work=W, dloss=P(0x70000), dh=P(0x80000), dhld=8, dw=P(0x90000), dwt=1, dwld=8):
+    L = bfz.lib()
+    if not grad:
+        return L.bfz_vocab_loss(hidden, hld, n, weight, wt, wld, grid, V, d, t, wide, loss, lse, work, None)
+    return L.bfz_vocab_loss_grad(hidden, hld, n, weight, wt, wld, grid, V, d, t, wide, lse, dloss, dh, dhld, dw, dwt, dwld, 0, work,
+                                 None)
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("kw,rc", [
+    (dict(hidden=None), EINVAL), (dict(weight=None), EINVAL), (dict(t=None), EINVAL), (dict(lse=None), EINVAL), (dict(work=None), EINVAL),
+    (dict(n=-1), EINVAL), (dict(V=0), EINVAL), (dict(d=0), EINVAL), (dict(n=1 << 25), EINVAL), (dict(V=1 << 28), EINVAL),
+    (dict(d=1 << 21, hld=1 << 21, wld=1 << 21), EINVAL), (dict(n=1 << 24, V=1 << 27), EINVAL), (dict(wt=0), EINVAL), (dict(wt=3), EINVAL),
+    (dict(grid=A), EINVAL), (dict(wt=3, grid=P(0x1002)), EALIGN), (dict(hld=7), EINVAL), (dict(wld=7), EINVAL), (dict(wld=1 << 22), EINVAL),
+    (dict(hidden=P(0x1001)), EALIGN), (dict(weight=P(0x1001)), EALIGN), (dict(t=P(0x1004)), EALIGN), (dict(t=P(0x1002), wide=0), EALIGN),
+    (dict(lse=P(0x1002)), EALIGN), (dict(work=P(0x1010)), EALIGN),
+])
+def test_vocab_loss_refusals(grad, kw, rc):
+    assert _loss(grad, **kw) == rc
+    assert "bfz_vocab_loss" in bfz.lib().bfz_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(dloss=None), EINVAL), (dict(dloss=P(0x1002)), EALIGN), (dict(dh=P(0x1001)), EALIGN), (dict(dhld=7), EINVAL),
+    (dict(dwt=2), EINVAL), (dict(dwt=3), EINVAL), (dict(dwld=7), EINVAL), (dict(dw=P(0x1002), dwt=0), EALIGN),
+])
+def test_vocab_loss_grad_refusals(kw, rc):
+    assert _loss(True, **kw) == rc
+
+
+def test_vocab_loss_refuses_a_null_loss():
+    assert _loss(loss=None) == EINVAL and _loss(loss=P(0x1001)) == EALIGN
+
+
+def test_vocab_loss_work_sizes():
+    f = bfz.lib().bfz_vocab_loss_work_bytes
+    assert f(-1, 10, 8, 1, 0) == 0 and f(4, 0, 8, 1, 0) == 0 and f(4, 10, 8, 0, 0) == 0
+    assert 0 < f(4, 10, 8, 1, 0) <= f(4, 10, 8, 1, 1)
+    # dz and the padded copy are bounded, whatever the vocabulary
+    assert f(8192, 1 << 20, 4096, 3, 1) < 4 << 30
