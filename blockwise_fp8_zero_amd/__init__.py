@@ -194,6 +194,10 @@ class Plan:
         _check(lib().bfz_plan_create(C.cast(arr, C.c_void_p), len(self.dims), D, rank, C.byref(h)))
         self._h = h
         self.D, self.rank = D, rank
+        # elements of each weight, cells of its scale grid and of its transposed copy's
+        self._sizes = [E * H * W for E, H, W in self.dims]
+        self._grids = [E * (-(-H // TILE)) * (-(-W // TILE)) for E, H, W in self.dims]
+        self._t_grids = [E * W * (-(-H // TILE)) for E, H, W in self.dims]
 
     def upload(self):
         """Copy the table to the current device if the plan has none yet."""
@@ -255,30 +259,35 @@ def _ptr_array(tensors, dtype, name, sizes):
     """Host array of the per-weight device pointers; tensor p (or None) must
     hold at least sizes[p] elements -- the kernels address it through the
     plan's table, so a smaller tensor would be read or written past its end."""
+    import torch
     n = len(sizes)
     if len(tensors) > n:
         raise ValueError(f"{name}: {len(tensors)} tensors for {n} weights")
     arr = (C.c_void_p * max(1, n))()
-    for k in range(n):
-        t = tensors[k] if k < len(tensors) else None
-        if t is not None:
-            arr[k] = _dev(t, dtype, f"{name}[{k}]", sizes[k]).value
+    for k, t in enumerate(tensors):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+            raise TypeError(f"{name}[{k}]: need a contiguous {dtype} CUDA tensor")
+        if t.numel() < sizes[k]:
+            raise ValueError(f"{name}[{k}]: needs at least {sizes[k]} elements, has {t.numel()}")
+        arr[k] = t.data_ptr()
     return arr
 
 
 def _weight_sizes(plan):
     """Elements of each row-major weight (E H W)."""
-    return [E * H * W for E, H, W in plan.dims]
+    return plan._sizes
 
 
 def _grid_sizes(plan):
     """Cells of each row-major scale grid (E ceil(H/128) ceil(W/128))."""
-    return [E * (-(-H // TILE)) * (-(-W // TILE)) for E, H, W in plan.dims]
+    return plan._grids
 
 
 def _t_grid_sizes(plan):
     """Cells of each transposed copy's scale grid (E W ceil(H/128))."""
-    return [E * W * (-(-H // TILE)) for E, H, W in plan.dims]
+    return plan._t_grids
 
 
 def pack_shard(plan: Plan, srcs, dst, stream=None):

@@ -117,29 +117,51 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(EmbedArgs a, int32_t pi
 
 // ---------------------------------------------------------------------
 // Stable sort of the tokens by id.  Runs of kRun tokens are ranked by
-// counting (every token against every token of its run: the run's ids sit
-// in LDS and are read by all lanes at once, two VALU operations per pair),
-// then runs are merged sixteen at a time by binary search: a token's place
-// is its place in its own run plus, for each other run, how many of that
-// run's come before it.  Ids outside the table get the key `vocab` and sort
-// last.  Two launches up to 32768 tokens, one more for each factor of 16.
+// counting: every token is compared with every token of its run, two VALU
+// operations a pair, the ids read from LDS by all lanes at once.  Then up to
+// sixteen runs at a time are merged by binary search: a token's place is its
+// place in its own run plus, for each other run, how many of that run's come
+// before it.  Ids outside the table get the key `vocab` and sort last.  One
+// launch up to 4096 tokens, two up to 65536, one more for each factor of 16.
 // ---------------------------------------------------------------------
-constexpr int kRun = 2048;
-constexpr int kRankWaves = 8, kRankThreads = 64 * kRankWaves;
+constexpr int kRun = 4096;
+constexpr int kRankWaves = 16, kRankThreads = 64 * kRankWaves;
 constexpr int kMergeRuns = 16;
 
-// A workgroup ranks 64 tokens of a run: wave w counts over ids
-// [256 w, 256 w + 256) of it.
+// How many keys of run[j0, j1) come before token i, whose key is `key`;
+// kTies: 1 when all of them stand before token i, -1 after, 0 mixed.
+template <int kTies>
+__device__ __forceinline__ int32_t count_before(const int32_t* run, int j0, int j1, int i, int32_t key) {
+    typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+    int32_t before = 0;
+#pragma unroll 2
+    for (int j = j0; j < j1; j += 16) {
+        i32x4 k[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) k[q] = *reinterpret_cast<const i32x4*>(&run[j + 4 * q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                if (kTies > 0) before += k[q][l] <= key;
+                else if (kTies < 0) before += k[q][l] < key;
+                else before += k[q][l] < key || (k[q][l] == key && j + 4 * q + l < i);
+            }
+    }
+    return before;
+}
+
+// A workgroup ranks 64 tokens of a run: its waves share out the run's ids.
 __global__ __launch_bounds__(kRankThreads) void rank_runs_kernel(const void* ids, int ids64, int64_t n, int64_t vocab,
                                                                  int32_t* keys, int32_t* pos) {
-    typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
     __shared__ alignas(16) int32_t run[kRun];
     __shared__ int32_t count[kRankWaves][64];
     const int64_t base = (int64_t)(blockIdx.x / (kRun / 64)) * kRun;
     const int group = (int)(blockIdx.x % (kRun / 64)) * 64;
     const int len = (int)(n - base < kRun ? n - base : kRun);
     if (group >= len) return;
-    for (int j = threadIdx.x; j < kRun; j += kRankThreads) {
+    const int share = (len + kRankWaves * 16 - 1) / (kRankWaves * 16) * 16;  // ids per wave
+    for (int j = threadIdx.x; j < share * kRankWaves; j += kRankThreads) {
         int32_t k = 0x7FFFFFFF;  // past the end: after every key
         if (j < len) {
             const int64_t r = row_of(ids, ids64, base + j, vocab);
@@ -148,32 +170,14 @@ __global__ __launch_bounds__(kRankThreads) void rank_runs_kernel(const void* ids
         run[j] = k;
     }
     __syncthreads();
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = group + lane;
-    const int32_t key = run[i];
-    const int j0 = w * (kRun / kRankWaves), j1 = j0 + kRun / kRankWaves;
-    int32_t before = 0;
-    if (j0 < len) {
-        if (j1 <= group) {  // all of them stand before the 64: equal ids count
-            for (int j = j0; j < j1; j += 4) {
-                const i32x4 k = *reinterpret_cast<const i32x4*>(&run[j]);
-#pragma unroll
-                for (int l = 0; l < 4; ++l) before += k[l] <= key;
-            }
-        } else if (j0 >= group + 64) {
-            for (int j = j0; j < j1; j += 4) {
-                const i32x4 k = *reinterpret_cast<const i32x4*>(&run[j]);
-#pragma unroll
-                for (int l = 0; l < 4; ++l) before += k[l] < key;
-            }
-        } else {
-            for (int j = j0; j < j1; j += 4) {
-                const i32x4 k = *reinterpret_cast<const i32x4*>(&run[j]);
-#pragma unroll
-                for (int l = 0; l < 4; ++l) before += k[l] < key || (k[l] == key && j + l < i);
-            }
-        }
-    }
+    const int32_t key = i < len ? run[i] : 0;
+    const int j0 = w * share, j1 = j0 + share;
+    int32_t before;
+    if (j1 <= group) before = count_before<1>(run, j0, j1, i, key);
+    else if (j0 >= group + 64) before = count_before<-1>(run, j0, j1, i, key);
+    else before = count_before<0>(run, j0, j1, i, key);
     count[w][lane] = before;
     __syncthreads();
     if (w != 0 || i >= len) return;
@@ -183,27 +187,28 @@ __global__ __launch_bounds__(kRankThreads) void rank_runs_kernel(const void* ids
     pos[base + before] = (int32_t)(base + i);
 }
 
-// Merge of groups of kMergeRuns sorted runs of `len` tokens each.  The
-// sixteen searches of a token advance together, so their loads overlap.
+// Merge of groups of kRuns sorted runs of `len` tokens each.  The searches of
+// a token advance together, so their loads overlap.
+template <int kRuns>
 __global__ __launch_bounds__(kThreads) void merge_runs_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ pos,
                                                               int32_t* __restrict__ out_keys, int32_t* __restrict__ out_pos,
                                                               int64_t n, int64_t len, int steps) {
     const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (t >= n) return;
-    const int64_t group = t / (len * kMergeRuns) * (len * kMergeRuns);
+    const int64_t group = t / (len * kRuns) * (len * kRuns);
     const int mine = (int)((t - group) / len);
     const int32_t key = keys[t];
     // of run r: how many come before this token; searched in [lo, lo + left)
-    int32_t lo[kMergeRuns], left[kMergeRuns];
+    int32_t lo[kRuns], left[kRuns];
 #pragma unroll
-    for (int r = 0; r < kMergeRuns; ++r) {
+    for (int r = 0; r < kRuns; ++r) {
         const int64_t have = n - (group + r * len);
         lo[r] = 0;
         left[r] = (int32_t)(r == mine || have <= 0 ? 0 : have < len ? have : len);
     }
     for (int s = 0; s < steps; ++s) {
 #pragma unroll
-        for (int r = 0; r < kMergeRuns; ++r) {
+        for (int r = 0; r < kRuns; ++r) {
             // an ended search reads its last place again and keeps its answer
             const int32_t half = left[r] >> 1;
             const int64_t at = group + r * len + lo[r] + half;
@@ -215,9 +220,15 @@ __global__ __launch_bounds__(kThreads) void merge_runs_kernel(const int32_t* __r
     }
     int64_t at = t - mine * len;
 #pragma unroll
-    for (int r = 0; r < kMergeRuns; ++r) at += lo[r];
+    for (int r = 0; r < kRuns; ++r) at += lo[r];
     out_keys[at] = key;
     out_pos[at] = pos[t];
+}
+
+template <int kRuns>
+void merge_runs(const int32_t* keys, const int32_t* pos, int32_t* out_keys, int32_t* out_pos, int64_t n, int64_t len, int steps, void* stream) {
+    hipLaunchKernelGGL(merge_runs_kernel<kRuns>, dim3((uint32_t)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, (hipStream_t)stream,
+                       keys, pos, out_keys, out_pos, n, len, steps);
 }
 
 // First index in [lo, n) whose key is >= v (or > v).
@@ -509,8 +520,8 @@ int launch_embed_grad(const EmbedGradArgs& a, void* work, void* stream) {
         for (int64_t len = kRun; len < a.n; len *= kMergeRuns) {
             int steps = 1;  // a search over m entries takes at most bits(m) steps
             while ((int64_t(1) << steps) <= len) ++steps;
-            hipLaunchKernelGGL(merge_runs_kernel, dim3((uint32_t)((a.n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                               (hipStream_t)stream, g.keys[at], g.pos[at], g.keys[at ^ 1], g.pos[at ^ 1], a.n, len, steps);
+            const auto merge = a.n <= 2 * len ? merge_runs<2> : a.n <= 4 * len ? merge_runs<4> : a.n <= 8 * len ? merge_runs<8> : merge_runs<kMergeRuns>;
+            merge(g.keys[at], g.pos[at], g.keys[at ^ 1], g.pos[at ^ 1], a.n, len, steps, stream);
             err = hipGetLastError();
             if (err != hipSuccess) return err;
             at ^= 1;

@@ -5,9 +5,8 @@
 //
 // Squares and sums are binary64: a binary32 square neither overflows nor
 // underflows there, and a sum over 10^9 terms keeps 2^-53 * sqrt(10^9) of
-// relative error.  The sum's order is fixed by the sizes alone: workgroup b
-// takes chunks b, b + G, ... of the list, adds its threads in a tree, and
-// the last workgroup to finish adds the G partial sums in index order, so
+// relative error.  The sum's order is fixed by the sizes alone: each
+// workgroup takes a fixed share, adds its threads in a tree, and the last workgroup to finish adds the G partial sums in index order, so
 // two runs give the same bits.
 #include <hip/hip_runtime.h>
 
@@ -105,8 +104,10 @@ __device__ __forceinline__ void write_coef(double sumsq, double max_norm, float*
 // The end of a sum kernel: publish this workgroup's partial; the last one to
 // arrive adds them all (thread t takes t, t + 256, ...), adds the earlier
 // launches' sum and, in the last launch, writes the results.  The partials
-// cross XCDs, whose L2s are separate: they are published and read with
-// agent-scope atomics around the ticket.
+// cross XCDs, whose L2s are separate: they are written, counted and read with
+// agent-scope atomics, which act beyond the L2s, and the wait puts a
+// workgroup's partial there before it is counted.  (An acquire-release ticket
+// writes back and invalidates caches once per workgroup.)
 __device__ __forceinline__ void finish_sum(double acc, const NormOut& out, void* work) {
     __shared__ double lds[kThreads / 64];
     __shared__ uint32_t arrived;
@@ -115,11 +116,11 @@ __device__ __forceinline__ void finish_sum(double acc, const NormOut& out, void*
     const double s = block_sum(acc, lds);
     if (threadIdx.x == 0) {
         __hip_atomic_store(&partial[blockIdx.x], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        arrived = __hip_atomic_fetch_add(&w->ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        arrived = __hip_atomic_fetch_add(&w->ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (arrived != gridDim.x - 1) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     double t = 0.0;
     for (uint32_t b = threadIdx.x; b < gridDim.x; b += kThreads)
         t += __hip_atomic_load(&partial[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -144,17 +145,26 @@ __device__ __forceinline__ int find_tensor(const TensorList& list, uint32_t c) {
     return lo;
 }
 
+// Workgroup b takes the consecutive chunks [b C / G, (b + 1) C / G): equal
+// shares, and the tensor is searched for once and then walked.
 __global__ __launch_bounds__(kThreads) void list_sumsq_kernel(TensorList list, NormOut out, void* work) {
     double acc = 0.0;
-    for (uint32_t c = blockIdx.x; c < list.chunks; c += gridDim.x) {
-        const int k = find_tensor(list, c);
+    uint32_t c = (uint32_t)((uint64_t)blockIdx.x * list.chunks / gridDim.x);
+    const uint32_t end = (uint32_t)((uint64_t)(blockIdx.x + 1) * list.chunks / gridDim.x);
+    int k = c < end ? find_tensor(list, c) : 0;
+    while (c < end) {
+        const uint32_t next = k + 1 < list.count ? list.chunk0[k + 1] : list.chunks;
+        const uint32_t stop = next < end ? next : end;
         const int64_t e0 = (int64_t)(c - list.chunk0[k]) * list.chunk_elems;
-        const int64_t e1 = e0 + list.chunk_elems < list.n[k] ? e0 + list.chunk_elems : list.n[k];
+        const int64_t e1 = (int64_t)(stop - list.chunk0[k]) * list.chunk_elems;
+        const int64_t e = e1 < list.n[k] ? e1 : list.n[k];
         switch (list.in_type[k]) {
-            case kF32: acc = sum_range((const float*)list.in[k], e0, e1, acc); break;
-            case kBF16: acc = sum_range((const bf16_t*)list.in[k], e0, e1, acc); break;
-            default: acc = sum_range((const f16_t*)list.in[k], e0, e1, acc); break;
+            case kF32: acc = sum_range((const float*)list.in[k], e0, e, acc); break;
+            case kBF16: acc = sum_range((const bf16_t*)list.in[k], e0, e, acc); break;
+            default: acc = sum_range((const f16_t*)list.in[k], e0, e, acc); break;
         }
+        c = stop;
+        ++k;
     }
     finish_sum(acc, out, work);
 }
@@ -244,16 +254,21 @@ __device__ __forceinline__ void clip_to(const I* in, void* out, int type, int64_
 
 __global__ __launch_bounds__(kThreads) void clip_kernel(TensorList list, const float* __restrict__ coef_p) {
     const float coef = *coef_p;
-    for (uint32_t c = blockIdx.x; c < list.chunks; c += gridDim.x) {
-        const int k = find_tensor(list, c);
+    uint32_t c = (uint32_t)((uint64_t)blockIdx.x * list.chunks / gridDim.x);
+    const uint32_t end = (uint32_t)((uint64_t)(blockIdx.x + 1) * list.chunks / gridDim.x);
+    for (int k = c < end ? find_tensor(list, c) : 0; c < end; ++k) {
+        const uint32_t next = k + 1 < list.count ? list.chunk0[k + 1] : list.chunks;
+        const uint32_t stop = next < end ? next : end;
+        const int64_t e0 = (int64_t)(c - list.chunk0[k]) * list.chunk_elems;
+        const int64_t e1 = (int64_t)(stop - list.chunk0[k]) * list.chunk_elems;
+        const int64_t e = e1 < list.n[k] ? e1 : list.n[k];
+        c = stop;
         // nothing to clip and nowhere else to write it: g * 1 = g
         if (coef == 1.0f && list.in[k] == list.out[k]) continue;
-        const int64_t e0 = (int64_t)(c - list.chunk0[k]) * list.chunk_elems;
-        const int64_t e1 = e0 + list.chunk_elems < list.n[k] ? e0 + list.chunk_elems : list.n[k];
         switch (list.in_type[k]) {
-            case kF32: clip_to((const float*)list.in[k], list.out[k], list.out_type[k], e0, e1, coef); break;
-            case kBF16: clip_to((const bf16_t*)list.in[k], list.out[k], list.out_type[k], e0, e1, coef); break;
-            default: clip_to((const f16_t*)list.in[k], list.out[k], list.out_type[k], e0, e1, coef); break;
+            case kF32: clip_to((const float*)list.in[k], list.out[k], list.out_type[k], e0, e, coef); break;
+            case kBF16: clip_to((const bf16_t*)list.in[k], list.out[k], list.out_type[k], e0, e, coef); break;
+            default: clip_to((const f16_t*)list.in[k], list.out[k], list.out_type[k], e0, e, coef); break;
         }
     }
 }

@@ -44,24 +44,19 @@ int check_tensor(const bfz_tensor& t, int32_t k, const char* what, const char* w
     return BFZ_OK;
 }
 
-// Elements one workgroup takes at a time: short lists are cut finer, so that
-// a single small weight still spreads over the device (4096 elements are
-// four 16-byte loads a thread); long ones coarser, so that the search for
-// a chunk's tensor stays rare.
-int64_t chunk_elems(int64_t total) { return total > (int64_t(1) << 25) ? 32768 : total > (int64_t(1) << 22) ? 16384 : 4096; }
+// Elements of a chunk, the unit that tensors are shared out by: four 16-byte
+// float loads a thread of a workgroup, so that one small weight spreads over
+// the device.
+constexpr int64_t kChunkElems = 4096;
 
 // Calls launch(list, first, last) for runs of kListTensors tensors; empty
 // tensors are left out.  outs may be null.
 template <class F>
 int for_lists(const bfz_tensor* grads, const bfz_tensor* outs, int32_t n, F&& launch) {
-    int64_t total = 0;
     int32_t left = 0;
-    for (int32_t k = 0; k < n; ++k) {
-        total += grads[k].n;
-        left += grads[k].n > 0;
-    }
+    for (int32_t k = 0; k < n; ++k) left += grads[k].n > 0;
     TensorList list{};
-    list.chunk_elems = chunk_elems(total);
+    list.chunk_elems = kChunkElems;
     bool first = true;
     if (left == 0) return launch(list, true, true);
     int64_t chunks = 0;

@@ -112,6 +112,7 @@ struct BF16KC {
     static constexpr int kBytes = kRows * kBK * 2;
     static constexpr int kLoads = kBytes / 1024 / kGemmWaves;
     static_assert(kLoads >= 1, "a stage has a load for each wave");
+    static constexpr int kReads = 1;  // LDS instructions a fragment
     static constexpr bool kScaled = false;
     typedef bf16x8 Frag;
     uint32_t at[2];  // LDS offset of tile 0's fragment, by half
@@ -152,6 +153,7 @@ template <int kRows>
 struct FP8KC {
     static constexpr int kBytes = kRows * kBK;
     static constexpr int kLoads = kBytes / 1024 / kGemmWaves;
+    static constexpr int kReads = 1;  // LDS instructions a fragment
     static constexpr bool kScaled = true;
     typedef u32x2 Frag;
     uint32_t at[2];
@@ -183,6 +185,7 @@ struct BF16KR {
     static constexpr int kLoads = kBytes / 1024 / kGemmWaves;
     static constexpr int kPieces = kRows * 2 / 16;  // 16-byte pieces of a row
     static_assert(kRows == 256, "the permutation spans a 512-byte row");
+    static constexpr int kReads = 2;  // LDS instructions a fragment
     static constexpr bool kScaled = false;
     typedef bf16x8 Frag;
     uint32_t at[kTiles];
@@ -221,6 +224,7 @@ struct FP8KR {
     static constexpr int kBytes = kRows * kBK;
     static constexpr int kLoads = kBytes / 1024 / kGemmWaves;
     static_assert(kRows == 256, "the permutation spans a 256-byte row");
+    static constexpr int kReads = 1;  // LDS instructions a fragment
     static constexpr bool kScaled = true;
     typedef u32x2 Frag;
     uint32_t at[kTiles];
@@ -279,6 +283,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
     constexpr int kWavesN = kGemmWaves / kWavesM;
     constexpr int kTM = kBM / kWavesM / 16, kTN = kBN / kWavesN / 16;
     constexpr int kStage = A::kBytes + B::kBytes;
+    constexpr uint32_t kOther = kStage;  // the second buffer; XOR with it toggles 0 and kStage
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / kWavesN, wn = wave % kWavesN;
@@ -302,26 +307,22 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
     const int64_t adv_a = A::advance(g.a), adv_b = B::advance(g.b);
     const uint32_t lds_a = lds + wave * 1024, lds_b = lds_a + A::kBytes;
 
-    // loads of step s into its buffer; past the end of k they give zero
-    auto issue = [&](int s) {
-        const uint32_t stage = (s & 1) ? kStage : 0;
+    // loads of the next step into buffer `stage`; past the end of k they give
+    // zero (no branch: the lanes' offsets are selected)
+    int64_t left_a = g.a.k - k0, left_b = g.b.k - k0;
+    auto issue = [&](uint32_t stage) {
         const i32x4 ra = buffer_of(base_a), rb = buffer_of(base_b);
         base_a += adv_a;
         base_b += adv_b;
-        const int64_t left_a = g.a.k - (k0 + (int64_t)s * kBK), left_b = g.b.k - (k0 + (int64_t)s * kBK);
-        if (left_a >= kBK && left_b >= kBK) {
+        const int la = (int)max((int64_t)0, min(left_a, (int64_t)kBK)), lb = (int)max((int64_t)0, min(left_b, (int64_t)kBK));
+        left_a -= kBK;
+        left_b -= kBK;
 #pragma unroll
-            for (int j = 0; j < A::kLoads; ++j) load_to_lds(ra, off_a[j], lds_a + stage + j * (kGemmWaves * 1024));
+        for (int j = 0; j < A::kLoads; ++j)
+            load_to_lds(ra, A::k_of(j, wave, lane) < la ? off_a[j] : kNowhere, lds_a + stage + j * (kGemmWaves * 1024));
 #pragma unroll
-            for (int j = 0; j < B::kLoads; ++j) load_to_lds(rb, off_b[j], lds_b + stage + j * (kGemmWaves * 1024));
-        } else {
-#pragma unroll
-            for (int j = 0; j < A::kLoads; ++j)
-                load_to_lds(ra, A::k_of(j, wave, lane) < left_a ? off_a[j] : kNowhere, lds_a + stage + j * (kGemmWaves * 1024));
-#pragma unroll
-            for (int j = 0; j < B::kLoads; ++j)
-                load_to_lds(rb, B::k_of(j, wave, lane) < left_b ? off_b[j] : kNowhere, lds_b + stage + j * (kGemmWaves * 1024));
-        }
+        for (int j = 0; j < B::kLoads; ++j)
+            load_to_lds(rb, B::k_of(j, wave, lane) < lb ? off_b[j] : kNowhere, lds_b + stage + j * (kGemmWaves * 1024));
     };
 
     f32x4 acc[kTM][kTN];
@@ -331,8 +332,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
         for (int u = 0; u < kTN; ++u) acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     typename A::Frag a[2][kTM];
     typename B::Frag b[2][kTN];
-    auto read_half = [&](int s, int h) {
-        const uint32_t stage = (s & 1) ? kStage : 0;
+    auto read_half = [&](uint32_t stage, int h) {
 #pragma unroll
         for (int u = 0; u < kTN; ++u) b[h][u] = fb.read(stage, h, u);
 #pragma unroll
@@ -346,8 +346,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
     auto scale_at = [&](int64_t kb) { return grid_row[min(kb, g.blocks_k - 1) * g.grid_k]; };
     float next_scale = 1.0f;
     if constexpr (A::kScaled) {
-        unit = scale_at(k0 / kTileDim);
-        next_scale = scale_at(k0 / kTileDim + 1);
+        unit = next_scale = scale_at(k0 / kTileDim);
     }
 
     auto multiply = [&](int h) {
@@ -360,42 +359,59 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
         }
     };
 
+    // One step from buffer `stage`.  The reads of the other half come first in
+    // each half and are spread over its multiplications.
+    constexpr int kReads = A::kReads * kTM + B::kReads * kTN;
+    auto spread = [&] {
+#pragma unroll
+        for (int i = 0; i < kReads; ++i) {
+            if constexpr (A::kScaled) __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // conversions
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                            // an LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                            // a matrix instruction
+        }
+    };
+    auto step = [&](uint32_t stage) {
+        read_half(stage, 1);
+        multiply(0);
+        spread();
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        issue(stage);
+        read_half(stage ^ kOther, 0);
+        multiply(1);
+        spread();
+        __builtin_amdgcn_sched_barrier(0);
+    };
     if (steps > 0) {
         issue(0);
-        if (steps > 1) issue(1);
+        issue(kOther);
         wait_loads();
         __builtin_amdgcn_s_barrier();
         read_half(0, 0);
-        for (int s = 0; s < steps; ++s) {
+        for (int s = 0;;) {
             if constexpr (A::kScaled) {
-                if ((s & 1) == 0 && s > 0) {
-                    const float scale = next_scale;
-                    next_scale = scale_at(k0 / kTileDim + s / 2 + 1);
-                    const float ratio = unit / scale;
-                    if (ratio <= 0x1p60f) {
-                        keep = 1.0f;
-                        unit = scale;
-                        if (ratio != 1.0f) {
+                const float scale = next_scale;
+                next_scale = scale_at(k0 / kTileDim + s / 2 + 1);
+                const float ratio = unit / scale;
+                const bool use = ratio <= 0x1p60f;
+                const float by = use ? ratio : 1.0f;
+                unit = use ? scale : unit;
+                keep = use ? 1.0f : 0.0f;  // the conversion takes 0 as 2^-127
 #pragma unroll
-                            for (int t = 0; t < kTM; ++t)
+                for (int t = 0; t < kTM; ++t)
 #pragma unroll
-                                for (int u = 0; u < kTN; ++u)
+                    for (int u = 0; u < kTN; ++u)
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) acc[t][u][i] *= ratio;
-                        }
-                    } else {
-                        keep = 0.0f;  // the conversion takes it as 2^-127
-                    }
-                }
+                        for (int i = 0; i < 4; ++i) acc[t][u][i] *= by;
             }
-            read_half(s, 1);
-            multiply(0);
-            wait_loads();
-            __builtin_amdgcn_s_barrier();
-            if (s + 2 < steps) issue(s + 2);
-            if (s + 1 < steps) read_half(s + 1, 0);
-            multiply(1);
+            step(0);
+            if (++s >= steps) break;
+            step(kOther);
+            if (++s >= steps) break;
         }
+        wait_loads();  // the loads issued past the end
     }
     if constexpr (A::kScaled) {
 #pragma unroll
@@ -407,6 +423,93 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
     }
     const WaveTile w{m0 + wm * kTM * 16, n0 + wn * kTN * 16, tm, wm, split, lane};
     epilogue.template run<kTM, kTN>(acc, w);
+}
+
+// ---- few tokens -------------------------------------------------------------------
+// The same product for up to 16 tokens a workgroup, bound by reading A once.
+// Nothing is staged: four waves of a workgroup take 32 rows of A and share out
+// its k in blocks of 128; a lane loads 32 k of one row of A and of one token
+// straight into registers, the four lanes of a row 64 bytes side by side, two
+// blocks ahead.  Which k a matrix instruction takes is free as long as A and B
+// agree.  The waves' sums meet in LDS.  Here a block's sums fit beside the total, so tile scales
+// are applied block by block.
+constexpr int kFewRows = 32, kFewTokens = 16, kFewWaves = 4;
+
+template <bool kFp8, class Epilogue>
+__global__ __launch_bounds__(64 * kFewWaves) void few_tokens_kernel(GemmArgs g, Epilogue epilogue) {
+    constexpr int kSize = kFp8 ? 1 : 2;
+    constexpr int kALoads = 2 * kSize, kBLoads = 4;  // 16-byte loads of 32 k
+    constexpr int kAhead = 2;
+    __shared__ f32x4 part[kFewWaves][2][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, r = lane & 15;
+    const int tm = blockIdx.x % g.tiles_m, tn = blockIdx.x / g.tiles_m;
+    const int64_t m0 = (int64_t)tm * kFewRows, n0 = (int64_t)tn * kFewTokens;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(g.a.p) + m0 * g.a.ld), (short)0, (int)kBufferBytes, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(g.b.p) + n0 * g.b.ld), (short)0, (int)kBufferBytes, 0x00020000);
+    uint32_t row_a[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) row_a[t] = m0 + 16 * t + r < g.a.extent ? (uint32_t)((16 * t + r) * g.a.ld) : kNowhere;
+    const uint32_t row_b = n0 + r < g.b.extent ? (uint32_t)(r * g.b.ld) : kNowhere;
+    const float* scales = kFp8 ? g.grid + m0 / kTileDim * g.grid_m : nullptr;
+    const int blocks = (int)((g.k + 127) / 128);
+
+    f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int b0 = wave; b0 < blocks; b0 += kFewWaves * kAhead) {
+        u32x4 a[kAhead][2][kALoads], b[kAhead][kBLoads];
+        float scale[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int block = b0 + x * kFewWaves;
+            const int64_t k0 = (int64_t)block * 128;
+            if constexpr (kFp8) scale[x] = scales[min((int64_t)block, g.blocks_k - 1) * g.grid_k];
+#pragma unroll
+            for (int l = 0; l < kALoads; ++l) {
+                const int64_t k = k0 + (4 * l + q) * (16 / kSize);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const bool in = k < g.a.k && row_a[t] != kNowhere;
+                    a[x][t][l] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? (int)(row_a[t] + (uint32_t)(k * kSize)) : (int)kNowhere, 0, 2));
+                }
+            }
+#pragma unroll
+            for (int l = 0; l < kBLoads; ++l) {
+                // the k of instruction l: of E4M3, half l % 2 of A's 16 codes
+                const int64_t k = kFp8 ? k0 + 64 * (l >> 1) + 16 * q + 8 * (l & 1) : k0 + 32 * l + 8 * q;
+                const bool in = k < g.b.k && row_b != kNowhere;
+                b[x][l] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, in ? (int)(row_b + (uint32_t)(k * 2)) : (int)kNowhere, 0, 0));
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f32x4 sum = kFp8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    bf16x8 av;
+                    if constexpr (kFp8) av = codes_to_bf16(u32x2{a[x][t][j >> 1][2 * (j & 1)], a[x][t][j >> 1][2 * (j & 1) + 1]}, 1.0f);
+                    else av = __builtin_bit_cast(bf16x8, a[x][t][j]);
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, __builtin_bit_cast(bf16x8, b[x][j]), sum, 0, 0, 0);
+                }
+                acc[t] = kFp8 ? acc[t] + sum * scale[x] : sum;
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) part[wave][t][lane] = acc[t];
+    __syncthreads();
+    if (wave != 0) return;
+    f32x4 sums[2][1];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        sums[t][0] = part[0][t][lane];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) sums[t][0] += part[w][t][lane];
+    }
+    const WaveTile w{m0, n0, tm, 0, 0, lane};
+    epilogue.template run<2, 1>(sums, w);
 }
 
 }  // namespace bfz

@@ -15,7 +15,11 @@
 // dz, rounded to bf16 (the matrix cores' input type: each dz is off by at
 // most 2^-8 of itself, which the sums over v and n average out); then
 // dz W adds onto dh's binary32 sums and dz^T h gives the piece's rows of dW.
-// A piece is as large as its dz may be, so that the products stay long.
+// dz is rounded in units of the largest dloss, by which the results are
+// multiplied in binary32: where dloss is the same for all tokens, as in a
+// mean, the target's p - 1 then rounds by what p holds, not by an error of
+// dloss that all tokens share (at 1013 tokens the gradients' error went from
+// 0.0035 to 0.0018, that of rounding them to bf16 alone).  A piece is as large as its dz may be, so that the products stay long.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -27,12 +31,6 @@ namespace bfz {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-
-// 2^x with subnormal results, which the instruction alone gives as zero.
-__device__ __forceinline__ float exp2_full(float x) {
-    const bool low = x < -126.0f;
-    return __builtin_amdgcn_exp2f(low ? x + 64.0f : x) * (low ? 0x1p-64f : 1.0f);
-}
 
 __device__ __forceinline__ int64_t target_of(const void* targets, int wide, int64_t n, int64_t vocab) {
     return row_of(targets, wide, n, vocab);
@@ -51,37 +49,51 @@ struct StatsEpilogue {
     __device__ __forceinline__ void run(const f32x4 (&acc)[kTM][kTN], const WaveTile& w) const {
         const int64_t v0 = first + w.m0 + 4 * (w.lane >> 4);
         const int64_t slot = slots0 + (int64_t)w.tile_m * waves_m + w.wave_m;
+        const bool whole = first + w.m0 + 16 * kTM <= vocab;  // all rows are in the vocabulary
 #pragma unroll
         for (int u = 0; u < kTN; ++u) {
             const int64_t token = w.n0 + 16 * u + (w.lane & 15);
             const bool there = token < n;
             const int64_t t = there ? target_of(targets, targets64, token, vocab) : -1;
-            const int64_t at = t - v0;
-            float top = -INFINITY, mine = 0.0f;
-            bool hit = false;
+            float top = -INFINITY, sum = 0.0f;
+            if (whole) {
 #pragma unroll
-            for (int r = 0; r < kTM; ++r)
+                for (int r = 0; r < kTM; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float z = acc[r][u][i];
-                    if (v0 + 16 * r + i < vocab) top = fmaxf(top, z);
-                    if (at == 16 * r + i) {
-                        mine = z;
-                        hit = true;
-                    }
-                }
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, acc[r][u][i]);
+            } else {
+#pragma unroll
+                for (int r = 0; r < kTM; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (v0 + 16 * r + i < vocab) top = fmaxf(top, acc[r][u][i]);
+            }
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
-            float sum = 0.0f;
+            if (whole) {
 #pragma unroll
-            for (int r = 0; r < kTM; ++r)
+                for (int r = 0; r < kTM; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (v0 + 16 * r + i < vocab) sum += __builtin_amdgcn_exp2f((acc[r][u][i] - top) * kLog2e);
+                    for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f((acc[r][u][i] - top) * kLog2e);
+            } else {
+#pragma unroll
+                for (int r = 0; r < kTM; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (v0 + 16 * r + i < vocab) sum += __builtin_amdgcn_exp2f((acc[r][u][i] - top) * kLog2e);
+            }
             sum += __shfl_xor(sum, 16, 64);
             sum += __shfl_xor(sum, 32, 64);
             if (there && w.lane < 16) partial[slot * n + token] = make_float2(top, sum);
-            if (there && hit) target_logit[token] = mine;
+            // a target among these rows: for one token in a thousand
+            const int64_t at = t - v0;
+            if (__any(t >= 0 && at >= 0 && at < 16 * kTM)) {
+#pragma unroll
+                for (int r = 0; r < kTM; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t >= 0 && at == 16 * r + i) target_logit[token] = acc[r][u][i];
+            }
         }
     }
 };
@@ -92,29 +104,51 @@ struct LogitGradEpilogue {
     int64_t width, first, vocab, n;
     const float* lse;
     const float* dloss;
+    const float* unit;
     const void* targets;
     int32_t targets64;
     template <int kTM, int kTN>
     __device__ __forceinline__ void run(const f32x4 (&acc)[kTM][kTN], const WaveTile& w) const {
         const int64_t m0 = w.m0 + 4 * (w.lane >> 4);
+        const float most = *unit;
+        const bool whole = first + w.m0 + 16 * kTM <= vocab;  // all rows are in the vocabulary
 #pragma unroll
         for (int u = 0; u < kTN; ++u) {
             const int64_t token = w.n0 + 16 * u + (w.lane & 15);
-            if (token >= n) continue;
-            const int64_t t = target_of(targets, targets64, token, vocab);
-            const float up = t < 0 ? 0.0f : dloss[token], l = t < 0 ? 0.0f : lse[token];
+            const bool there = token < n;
+            const int64_t t = there ? target_of(targets, targets64, token, vocab) : -1;
+            const float up = t < 0 ? 0.0f : dloss[token] / most;
+            // p = 2^(z log2e - lse log2e), as 2^64 p and a factor, since the
+            // instruction gives zero for subnormal results; a token without a
+            // target gets p = 0
+            const float shift = t < 0 ? -INFINITY : 64.0f - lse[token] * kLog2e;
+            const float factor = up * 0x1p-64f;
             const int64_t at = t - first - m0;
+            float x[kTM][4];
+#pragma unroll
+            for (int r = 0; r < kTM; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[r][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[r][u][i], kLog2e, shift)) * factor;
+            // a target among these rows: for one token in a thousand
+            if (__any(t >= 0 && at >= 0 && at < 16 * kTM)) {
+#pragma unroll
+                for (int r = 0; r < kTM; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t >= 0 && at == 16 * r + i) x[r][i] -= up;
+            }
+            if (!whole) {
+#pragma unroll
+                for (int r = 0; r < kTM; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (first + m0 + 16 * r + i >= vocab) x[r][i] = 0.0f;
+            }
+            if (!there) continue;
             bf16_t* row = dz + token * width + m0;
 #pragma unroll
             for (int r = 0; r < kTM; ++r) {
-                float x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = exp2_full((acc[r][u][i] - l) * kLog2e);
-                    x[i] = at == 16 * r + i ? (p - 1.0f) * up : p * up;
-                    if (t < 0 || first + m0 + 16 * r + i >= vocab) x[i] = 0.0f;
-                }
-                const u32x2 y = {pack2<bf16_t>(x[0], x[1]), pack2<bf16_t>(x[2], x[3])};
+                const u32x2 y = {pack2<bf16_t>(x[r][0], x[r][1]), pack2<bf16_t>(x[r][2], x[r][3])};
                 *reinterpret_cast<u32x2*>(row + 16 * r) = y;
             }
         }
@@ -151,10 +185,12 @@ template <class O>
 struct WeightGradEpilogue {
     O* dw;
     int64_t ld, dim, first, vocab;
+    const float* unit;
     int32_t add, vec;  // vec: 4 elements at a time are aligned
     template <int kTM, int kTN>
     __device__ __forceinline__ void run(const f32x4 (&acc)[kTM][kTN], const WaveTile& w) const {
         const int64_t m0 = w.m0 + 4 * (w.lane >> 4);
+        const float most = *unit;
 #pragma unroll
         for (int u = 0; u < kTN; ++u) {
             const int64_t v = first + w.n0 + 16 * u + (w.lane & 15);
@@ -162,7 +198,7 @@ struct WeightGradEpilogue {
             O* row = dw + v * ld + m0;
 #pragma unroll
             for (int r = 0; r < kTM; ++r) {
-                const f32x4 x = acc[r][u];
+                const f32x4 x = acc[r][u] * most;
                 O* p = row + 16 * r;
                 if (vec && m0 + 16 * r + 4 <= dim) {
                     if constexpr (sizeof(O) == 4) {
@@ -201,15 +237,22 @@ __global__ __launch_bounds__(kJoinTokens* kJoinSlots) void join_stats_kernel(con
     const int64_t token = (int64_t)blockIdx.x * kJoinTokens + x;
     float top = -INFINITY, sum = 0.0f;
     if (token < n)
-        for (int64_t s = y; s < slots; s += kJoinSlots) {
-            const float2 p = partial[s * n + token];
+        for (int64_t s0 = y; s0 < slots; s0 += 8 * kJoinSlots) {
+            float2 p[8];  // loaded together: with one token the loads' latency is the time
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int64_t s = s0 + u * kJoinSlots;
+                p[u] = s < slots ? partial[s * n + token] : make_float2(-INFINITY, 0.0f);
+            }
+            float t = top;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) t = fmaxf(t, p[u].x);
             // a slot beyond the vocabulary has maximum -inf and sum 0 (one of
             // NaN logits has sum NaN, which stays)
-            const float t = fmaxf(top, p.x);
-            if (p.y != 0.0f) {
-                sum = (sum == 0.0f ? 0.0f : sum * __builtin_amdgcn_exp2f((top - t) * kLog2e)) + p.y * __builtin_amdgcn_exp2f((p.x - t) * kLog2e);
-                top = t;
-            }
+            sum = sum == 0.0f ? 0.0f : sum * __builtin_amdgcn_exp2f((top - t) * kLog2e);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) sum += p[u].y == 0.0f ? 0.0f : p[u].y * __builtin_amdgcn_exp2f((p[u].x - t) * kLog2e);
+            top = t;
         }
     tops[y][x] = top;
     sums[y][x] = sum;
@@ -239,14 +282,33 @@ __global__ void pad_rows_kernel(const T* __restrict__ src, int64_t ld, int64_t r
         for (int64_t c = threadIdx.x; c < width; c += blockDim.x) dst[r * width + c] = c < dim ? src[r * ld + c] : (T)0;
 }
 
-// dh = sum of the slabs, rounded to bf16.
+// Largest |dloss| of the tokens that count; 1 where there is none.
+__global__ __launch_bounds__(1024) void upstream_unit_kernel(const float* __restrict__ dloss, const void* targets, int32_t targets64,
+                                                             int64_t vocab, int64_t n, float* unit) {
+    __shared__ float tops[16];
+    float top = 0.0f;
+    for (int64_t i = threadIdx.x; i < n; i += 1024)
+        if (target_of(targets, targets64, i, vocab) >= 0) top = fmaxf(top, fabsf(dloss[i]));
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int k = 1; k < 16; ++k) top = fmaxf(top, tops[k]);
+    *unit = top > 0.0f && top < INFINITY ? top : 1.0f;
+}
+
+// dh = unit * sum of the slabs, rounded to bf16.
 __global__ __launch_bounds__(256) void finish_hidden_kernel(const float* __restrict__ sums, int64_t slab, int32_t slabs, int64_t ld,
-                                                            int64_t dim, int64_t n, bf16_t* __restrict__ out, int64_t out_ld, int32_t vec) {
+                                                            int64_t dim, int64_t n, const float* __restrict__ unit,
+                                                            bf16_t* __restrict__ out, int64_t out_ld, int32_t vec) {
+    const float whole = *unit;
     const int64_t quads = (dim + 3) / 4;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * quads; i += (int64_t)gridDim.x * 256) {
         const int64_t token = i / quads, c = 4 * (i - token * quads);
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int32_t s = 0; s < slabs; ++s) x += *reinterpret_cast<const f32x4*>(sums + s * slab + token * ld + c);
+        x *= whole;
         bf16_t* p = out + token * out_ld + c;
         if (vec) {
             const u32x2 y = {pack2<bf16_t>(x[0], x[1]), pack2<bf16_t>(x[2], x[3])};
@@ -270,28 +332,92 @@ int64_t piece_rows(int64_t n, int64_t vocab, int64_t dim) {
     return std::min(rows, up(vocab, 256));
 }
 
-// Splits of k that give a product of few tiles enough workgroups.
-int splits_of(int64_t tiles, int64_t k) {
-    int64_t s = 1;
-    while (tiles * s < 384 && k / (s * 2) >= 512) s *= 2;
-    return (int)s;
-}
-
 struct Work {
     float2* partial;
     float* target_logit;
     void *hidden, *weight;  // padded copies
     bf16_t* dz;
     float* sums;
+    float* unit;
     int64_t bytes;
 };
 
-int bn_of(int64_t n) { return n <= 64 ? 64 : n <= 128 ? 128 : 256; }
-int waves_m_of(int bn) { return bn == 64 ? 8 : bn == 128 ? 4 : 2; }
+constexpr int waves_m_of(int bn) { return bn == 64 ? 8 : 4; }
 
-int hidden_splits(int64_t n, int64_t dim, int64_t piece) {
-    return splits_of((up(dim, kBM) / kBM) * (up(n, bn_of(n)) / bn_of(n)), piece);
+// Time of a product of `tiles` 256 x bn tiles and `steps` steps of k, in
+// microseconds, fitted to what the kernels take (8 shapes from 100 x 100000 x
+// 512 to 8192 x 32768 x 4096): a step of a 256-wide tile takes 1.2 us on an idle
+// device and 1.6 on a full one, of a 128-wide one 0.8 to 1.06, of a 64-wide one
+// 0.72 to 0.82, and 1.06 where two such workgroups share a CU.  A tile's first
+// loads and its epilogue take about four steps' time.
+double product_us(int64_t tiles, int bn, int64_t steps) {
+    const double load = double(std::min<int64_t>(tiles, 256)) / 256;
+    if (bn == 64 && tiles > 256) return double((tiles + 511) / 512) * 1.06 * double(steps + 4);
+    const double step = bn == 256 ? 1.2 + 0.4 * load : bn == 128 ? 0.8 + 0.26 * load : 0.72 + 0.1 * load;
+    return double((tiles + 255) / 256) * step * double(steps + 4);
 }
+
+constexpr int kWidths[] = {256, 128, 64};
+
+// Rows of a product's long side that fill whole rounds of the device with
+// 256-wide tiles, and the width for the rest, where that beats one width for
+// all (1013 x 50001 x 1000 has 3.06 rounds of tiles).
+struct Rows {
+    int64_t full;  // rows of the first launch, 0: none
+    int bn;        // width of the only, or second, launch
+};
+
+// Width in tokens of the logits' tiles: wide ones reuse more, narrow ones
+// fill the device and its last round (512 x 16384 x 2048: 607, 907 and 861
+// TFLOP/s at 256, 128 and 64; 1013 x 50001 x 1000: 644, 531 and 499).
+// `kFewTokens` tokens and less are read without LDS.
+int best_width(int64_t n, int64_t rows, int64_t dim, double* least) {
+    int best = 0;
+    for (int bn : kWidths) {
+        const double us = product_us(up(rows, kBM) / kBM * (up(n, bn) / bn), bn, up(dim, kBK) / kBK);
+        if (!best || us < *least) best = bn, *least = us;
+    }
+    return best;
+}
+Rows logits_rows(int64_t n, int64_t rows, int64_t dim) {
+    if (n <= kFewTokens) return Rows{0, kFewTokens};
+    double whole, rest;
+    const int bn = best_width(n, rows, dim, &whole);
+    const int64_t across = up(n, 256) / 256, tiles = up(rows, kBM) / kBM * across;
+    const int64_t full = tiles / 256 * 256 / across * kBM;
+    if (full == 0 || full >= rows) return Rows{0, bn};
+    const int rest_bn = best_width(n, rows - full, dim, &rest);
+    const double both = product_us(full / kBM * across, 256, up(dim, kBK) / kBK) + rest;
+    return both < whole ? Rows{full, rest_bn} : Rows{0, bn};
+}
+
+// Of dh: few tiles and a long k (the piece's rows), so k is split too; each
+// split's binary32 sums are written and read again at the end, at some 5 TB/s.
+// Chosen against measured (microseconds, both kernels): 1013 x 50001 x 1000
+// 256 wide in 16 (101; in 4: 263, 64 wide in 8: 114), 512 x 16384 x 2048 128
+// wide in 8 (44; 256 wide in 16: 49), 2048 x 32768 x 4096 256 wide in 2 (437;
+// in 1: 715, in 4: 459).
+struct HiddenShape {
+    int bn, splits;
+};
+HiddenShape hidden_shape(int64_t n, int64_t dim, int64_t piece) {
+    HiddenShape best{0, 1};
+    double least = 0.0;
+    for (int bn : kWidths)
+        for (int s = 1; s <= 64 && (s == 1 || piece / s >= 256); s *= 2) {
+            const int64_t tiles = up(dim, kBM) / kBM * (up(n, bn) / bn);
+            const double us = product_us(tiles * s, bn, up(piece, kBK) / kBK / s) + 1.6e-6 * double(n) * double(dim) * s;
+            if (!best.bn || us < least) best = HiddenShape{bn, s}, least = us;
+        }
+    return best;
+}
+
+// Partial statistics of a token: one for each wave's rows, 8 of a tile at most
+// (a tile of few tokens has one for 32 rows).
+int64_t stat_slots(int64_t rows, int width) {
+    return width == kFewTokens ? up(rows, kFewRows) / kFewRows : up(rows, kBM) / kBM * waves_m_of(width);
+}
+int64_t most_slots(int64_t vocab) { return up(vocab, kBM) / kBM * 8; }
 
 Work work_of(void* work, int64_t n, int64_t vocab, int64_t dim, int fp8, int grad) {
     Work w{};
@@ -307,13 +433,14 @@ Work work_of(void* work, int64_t n, int64_t vocab, int64_t dim, int fp8, int gra
     w.weight = take(piece * width * (fp8 ? 1 : 2));
     const int64_t mark = at;
     // the loss and its gradient run one after the other: one space for both
-    w.partial = reinterpret_cast<float2*>(take((up(vocab, kBM) / kBM + 1) * waves_m_of(bn_of(n)) * n * 8));
+    w.partial = reinterpret_cast<float2*>(take(most_slots(vocab) * n * 8));
     w.target_logit = reinterpret_cast<float*>(take(n * 4));
     w.bytes = at;
     if (grad) {
         at = mark;
+        w.unit = reinterpret_cast<float*>(take(4));
         w.dz = reinterpret_cast<bf16_t*>(take(n * piece * 2));
-        w.sums = reinterpret_cast<float*>(take(hidden_splits(n, dim, piece) * n * width * 4));
+        w.sums = reinterpret_cast<float*>(take(hidden_shape(n, dim, piece).splits * n * width * 4));
         w.bytes = std::max(w.bytes, at);
     }
     return w;
@@ -352,25 +479,35 @@ int launch_gemm(GemmArgs g, const Epilogue& e, void* stream) {
 // whose B has tokens in its rows.
 template <template <int> class A, int kBN, class Epilogue>
 int launch_kc(const GemmArgs& g, const Epilogue& e, void* stream) {
-    return launch_gemm<A<kBM>, BF16KC<kBN>, kBN, kBN == 64 ? 8 : kBN == 128 ? 4 : 2, Epilogue>(g, e, stream);
+    return launch_gemm<A<kBM>, BF16KC<kBN>, kBN, waves_m_of(kBN), Epilogue>(g, e, stream);
 }
 template <template <int, int> class A, int kBN, class Epilogue>
 int launch_kr(const GemmArgs& g, const Epilogue& e, void* stream) {
-    constexpr int kWavesM = kBN == 64 ? 8 : kBN == 128 ? 4 : 2;
+    constexpr int kWavesM = waves_m_of(kBN);
     return launch_gemm<A<kBM, kBM / kWavesM / 16>, BF16KC<kBN>, kBN, kWavesM, Epilogue>(g, e, stream);
 }
 
+template <bool kFp8, class Epilogue>
+int launch_few(GemmArgs g, const Epilogue& e, void* stream) {
+    g.tiles_m = (int32_t)(up(g.a.extent, kFewRows) / kFewRows);
+    g.tiles_n = (int32_t)(up(g.b.extent, kFewTokens) / kFewTokens);
+    hipLaunchKernelGGL((few_tokens_kernel<kFp8, Epilogue>), dim3((uint32_t)(g.tiles_m * g.tiles_n)), dim3(64 * kFewWaves), 0,
+                       (hipStream_t)stream, g, e);
+    return hipGetLastError();
+}
+
 template <class Epilogue>
-int logits(int fp8, int64_t n, const GemmArgs& g, const Epilogue& e, void* stream) {
-    switch (bn_of(n)) {
+int logits_launch(int fp8, int width, const GemmArgs& g, const Epilogue& e, void* stream) {
+    switch (width) {
+        case kFewTokens: return fp8 ? launch_few<true>(g, e, stream) : launch_few<false>(g, e, stream);
         case 64: return fp8 ? launch_kc<FP8KC, 64>(g, e, stream) : launch_kc<BF16KC, 64>(g, e, stream);
         case 128: return fp8 ? launch_kc<FP8KC, 128>(g, e, stream) : launch_kc<BF16KC, 128>(g, e, stream);
         default: return fp8 ? launch_kc<FP8KC, 256>(g, e, stream) : launch_kc<BF16KC, 256>(g, e, stream);
     }
 }
 
-int hidden_grad(int fp8, int64_t n, const GemmArgs& g, const SumEpilogue& e, void* stream) {
-    switch (bn_of(n)) {
+int hidden_grad(int fp8, int bn, const GemmArgs& g, const SumEpilogue& e, void* stream) {
+    switch (bn) {
         case 64: return fp8 ? launch_kr<FP8KR, 64>(g, e, stream) : launch_kr<BF16KR, 64>(g, e, stream);
         case 128: return fp8 ? launch_kr<FP8KR, 128>(g, e, stream) : launch_kr<BF16KR, 128>(g, e, stream);
         default: return fp8 ? launch_kr<FP8KR, 256>(g, e, stream) : launch_kr<BF16KR, 256>(g, e, stream);
@@ -433,6 +570,45 @@ void set_grid(const VocabLossArgs& a, int64_t first, bool vocab_is_m, GemmArgs* 
     g->blocks_k = vocab_is_m ? wb : rows;
 }
 
+// The logits of `rows` vocabulary rows from `first`, read from `weight`, in one
+// launch or two; epilogue(at, count, width) gives that of rows [at, at + count)
+// of them.
+template <class F>
+int logits(const VocabLossArgs& a, const Source& s, const Operand& weight, int64_t first, int64_t rows, F&& epilogue, void* stream) {
+    const Rows r = logits_rows(a.n, rows, a.dim);
+    for (int64_t at = 0; at < rows;) {
+        const int64_t count = at < r.full ? r.full : rows - at;
+        const int width = at < r.full ? 256 : r.bn;
+        GemmArgs g{};
+        g.a = Operand{static_cast<const char*>(weight.p) + at * weight.ld, weight.ld, count, weight.k};
+        g.b = s.hidden;
+        g.k = a.dim;
+        set_grid(a, first + at, true, &g);
+        const auto e = epilogue(at, count, width);
+        const int err = logits_launch(a.fp8, width, g, e, stream);
+        if (err) return err;
+        at += count;
+    }
+    return hipSuccess;
+}
+
+// Rows [first, first + rows) of dW = dz^T h: m is the hidden width, n the
+// vocabulary rows.
+int weight_grad(const VocabLossArgs& a, const Work& w, const Source& s, int64_t first, int64_t rows, int64_t width, void* stream) {
+    GemmArgs d{};
+    d.a = Operand{s.hidden.p, s.hidden.ld, a.n > 0 ? s.hidden.k : a.dim, a.n};
+    d.b = Operand{w.dz, width * 2, rows, a.n};
+    d.k = a.n;
+    const bool f32 = a.dweight_type == kF32;
+    const int32_t vec = a.dweight_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % (f32 ? 16 : 8) == 0;
+    if (f32) {
+        const WeightGradEpilogue<float> e{static_cast<float*>(a.dweight), a.dweight_ld, a.dim, first, a.vocab, w.unit, a.accumulate, vec};
+        return launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<float>>(d, e, stream);
+    }
+    const WeightGradEpilogue<bf16_t> e{static_cast<bf16_t*>(a.dweight), a.dweight_ld, a.dim, first, a.vocab, w.unit, a.accumulate, vec};
+    return launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<bf16_t>>(d, e, stream);
+}
+
 }  // namespace
 
 int64_t vocab_loss_work_bytes(int64_t n, int64_t vocab, int64_t dim, int fp8, int grad) {
@@ -445,21 +621,20 @@ int launch_vocab_loss(const VocabLossArgs& a, void* work, void* stream) {
     Source s;
     int err = source_of(a, w, &s, stream);
     if (err) return err;
-    const int waves_m = waves_m_of(bn_of(a.n));
     const int64_t piece = s.copy_weight ? piece_rows(a.n, a.vocab, a.dim) : a.vocab;
     int64_t slots = 0;
     for (int64_t first = 0; first < a.vocab; first += piece) {
         const int64_t rows = std::min(piece, a.vocab - first);
-        GemmArgs g{};
-        err = weight_piece(a, w, s, first, rows, &g.a, stream);
+        Operand weight;
+        err = weight_piece(a, w, s, first, rows, &weight, stream);
         if (err) return err;
-        g.b = s.hidden;
-        g.k = a.dim;
-        set_grid(a, first, true, &g);
-        const StatsEpilogue e{w.partial, w.target_logit, a.targets, a.targets64, first, a.vocab, a.n, slots, waves_m};
-        err = logits(a.fp8, a.n, g, e, stream);
+        err = logits(a, s, weight, first, rows, [&](int64_t at, int64_t count, int width) {
+            const StatsEpilogue e{w.partial, w.target_logit, a.targets, a.targets64, first + at, a.vocab, a.n, slots,
+                                  width == kFewTokens ? 1 : waves_m_of(width)};
+            slots += stat_slots(count, width);
+            return e;
+        }, stream);
         if (err) return err;
-        slots += up(rows, kBM) / kBM * waves_m;
     }
     hipLaunchKernelGGL(join_stats_kernel, dim3((uint32_t)(up(a.n, kJoinTokens) / kJoinTokens)), dim3(kJoinTokens * kJoinSlots), 0,
                        (hipStream_t)stream, w.partial, slots, w.target_logit, a.targets, a.targets64, a.vocab, a.n, a.loss, a.lse);
@@ -472,51 +647,37 @@ int launch_vocab_loss_grad(const VocabLossArgs& a, void* work, void* stream) {
     int err = hipSuccess;
     if (a.n > 0) err = source_of(a, w, &s, stream);
     if (err) return err;
+    hipLaunchKernelGGL(upstream_unit_kernel, dim3(1), dim3(1024), 0, (hipStream_t)stream, a.dloss, a.targets, a.targets64, a.vocab, a.n,
+                       w.unit);
+    err = hipGetLastError();
+    if (err) return err;
     const int64_t piece = piece_rows(a.n, a.vocab, a.dim);
-    const int splits = hidden_splits(a.n, a.dim, piece);
+    const HiddenShape shape = hidden_shape(a.n, a.dim, piece);
     for (int64_t first = 0; first < a.vocab; first += piece) {
         const int64_t rows = std::min(piece, a.vocab - first);
         const int64_t width = up(rows, kBM);
-        GemmArgs g{};
         Operand weight{};
         if (a.n > 0) {
             err = weight_piece(a, w, s, first, rows, &weight, stream);
             if (err) return err;
-            g.a = weight;
-            g.b = s.hidden;
-            g.k = a.dim;
-            set_grid(a, first, true, &g);
-            const LogitGradEpilogue e{w.dz, width, first, a.vocab, a.n, a.lse, a.dloss, a.targets, a.targets64};
-            err = logits(a.fp8, a.n, g, e, stream);
+            err = logits(a, s, weight, first, rows, [&](int64_t at, int64_t, int) {
+                return LogitGradEpilogue{w.dz + at, width, first + at, a.vocab, a.n, a.lse, a.dloss, w.unit, a.targets, a.targets64};
+            }, stream);
             if (err) return err;
         }
         if (a.dhidden && a.n > 0) {
             GemmArgs h{};
             h.a = Operand{weight.p, weight.ld, weight.k, rows};
-            h.b = Operand{w.dz, width * 2, a.n, width};
+            h.b = Operand{w.dz, width * 2, a.n, up(rows, kFewRows)};  // written that far, zeros at the end
             h.k = rows;
-            h.splits = splits;
+            h.splits = shape.splits;
             set_grid(a, first, false, &h);
             const SumEpilogue e{w.sums, s.width, a.n * s.width, s.width, a.n, first > 0};
-            err = hidden_grad(a.fp8, a.n, h, e, stream);
+            err = hidden_grad(a.fp8, shape.bn, h, e, stream);
             if (err) return err;
         }
         if (a.dweight) {
-            GemmArgs d{};
-            d.a = Operand{s.hidden.p, s.hidden.ld, s.hidden.k, a.n};
-            d.b = Operand{w.dz, width * 2, width, a.n};
-            d.k = a.n;
-            if (a.n == 0) d.a.extent = a.dim, d.b.extent = rows;
-            const bool f32 = a.dweight_type == kF32;
-            const int64_t unit = f32 ? 16 : 8;
-            const int32_t vec = a.dweight_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % unit == 0;
-            if (f32) {
-                const WeightGradEpilogue<float> e{static_cast<float*>(a.dweight), a.dweight_ld, a.dim, first, a.vocab, a.accumulate, vec};
-                err = launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<float>>(d, e, stream);
-            } else {
-                const WeightGradEpilogue<bf16_t> e{static_cast<bf16_t*>(a.dweight), a.dweight_ld, a.dim, first, a.vocab, a.accumulate, vec};
-                err = launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<bf16_t>>(d, e, stream);
-            }
+            err = weight_grad(a, w, s, first, rows, width, stream);
             if (err) return err;
         }
     }
@@ -524,8 +685,8 @@ int launch_vocab_loss_grad(const VocabLossArgs& a, void* work, void* stream) {
     const int32_t vec = a.dim % 4 == 0 && a.dhidden_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.dhidden) % 8 == 0;
     const int64_t quads = a.n * ((a.dim + 3) / 4);
     hipLaunchKernelGGL(finish_hidden_kernel, dim3((uint32_t)std::min<int64_t>((quads + 255) / 256, 16384)), dim3(256), 0,
-                       (hipStream_t)stream, w.sums, a.n * s.width, splits, s.width, a.dim, a.n, static_cast<bf16_t*>(a.dhidden),
-                       a.dhidden_ld, vec);
+                       (hipStream_t)stream, w.sums, a.n * s.width, shape.splits, s.width, a.dim, a.n, w.unit,
+                       static_cast<bf16_t*>(a.dhidden), a.dhidden_ld, vec);
     return hipGetLastError();
 }
 

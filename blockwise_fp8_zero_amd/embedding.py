@@ -2,8 +2,8 @@
 bfz_embed_grad).  The table may be the row-major FP8 weight and scale grid
 that the step writes; the gradient is the row-major one the step reads.
 """
-from . import _check, _stream, lib
-from ._tensors import id_vector, matrix, tile_grid, work_pointer
+from . import _check, lib
+from ._tensors import id_vector, matrix, raw_stream, tile_grid, work_pointer
 
 
 def _same(name, got, want):
@@ -21,7 +21,7 @@ def embed(ids, table, out, scale=1.0, grid=None, stream=None):
     o, ocode, rows, cols, old = matrix(out, "out")
     _same("out", (rows, cols), (n, dim))
     _check(lib().bfz_embed(p, wide, n, t, tcode, tile_grid(grid, tcode, vocab, dim), vocab, dim, tld, float(scale),
-                           o, ocode, old, _stream(stream)))
+                           o, ocode, old, raw_stream(stream)))
 
 
 def embed_grad_workspace(n, dim, device="cuda"):
@@ -40,4 +40,4 @@ def embed_grad(ids, dout, dtable, work, scale=1.0, accumulate=False, stream=None
     _same("dout", (rows, dim), (n, cols))
     need = lib().bfz_embed_grad_work_bytes(n, dim)
     _check(lib().bfz_embed_grad(p, wide, n, d, dcode, dld, vocab, dim, float(scale), int(bool(accumulate)), t, tcode,
-                                tld, work_pointer(work, need), _stream(stream)))
+                                tld, work_pointer(work, need), raw_stream(stream)))

@@ -10,36 +10,36 @@ Over several ranks: shard_grad_norm(..., sumsq=s), all_reduce(s), clip_coef(s,
 """
 import ctypes as C
 
-from . import _check, _ptr_array, _scalar, _stream, _weight_sizes, lib
-from ._tensors import dtype_code, work_pointer
+from . import _check, _ptr_array, _weight_sizes, lib
+from ._tensors import _load, dtype_code, raw_stream, scalar, work_pointer
 
 
-class _Tensor(C.Structure):
-    """bfz_tensor."""
-    _fields_ = [("data", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32), ("reserved", C.c_int32)]
+def _work_bytes(_known=[]):
+    if not _known:
+        _known.append(int(lib().bfz_norm_work_bytes()))
+    return _known[0]
 
 
 def norm_workspace(device="cuda"):
     """Workspace of the norm calls: zeroed here once, then kept as they leave
     it.  Calls that may run at the same time (two streams) need one each."""
     import torch
-    return torch.zeros(int(lib().bfz_norm_work_bytes()), dtype=torch.uint8, device=device)
+    return torch.zeros(_work_bytes(), dtype=torch.uint8, device=device)
 
 
 def _list(tensors, name):
-    arr = (_Tensor * max(1, len(tensors)))()
-    for k, t in enumerate(tensors):
-        code = dtype_code(t, f"{name}[{k}]")
+    """bfz_tensor[]: three 64-bit words each (the type and a zero share one)."""
+    words = []
+    for t in tensors:
+        code = dtype_code(t, name)
         if not t.is_contiguous():
-            raise TypeError(f"{name}[{k}]: need a contiguous tensor")
-        arr[k] = _Tensor(t.data_ptr(), t.numel(), code, 0)
-    return arr
+            raise TypeError(f"{name}: need contiguous tensors")
+        words += (t.data_ptr(), t.numel(), code)
+    return (C.c_int64 * max(1, len(words)))(*words)
 
 
 def _results(norm, coef, sumsq):
-    import torch
-    return (None if sumsq is None else _scalar(sumsq, "sumsq", torch.float64),
-            None if norm is None else _scalar(norm, "norm"), None if coef is None else _scalar(coef, "coef"))
+    return (None if sumsq is None else scalar(sumsq, "sumsq", _load().float64)), scalar(norm, "norm"), scalar(coef, "coef")
 
 
 def _limit(max_norm):
@@ -53,8 +53,9 @@ def grad_norm(grads, norm, work, max_norm=None, coef=None, sumsq=None, stream=No
     float16 device tensors of any shapes, mixed as they come."""
     arr = _list(grads, "grads")
     s, n, c = _results(norm, coef, sumsq)
-    _check(lib().bfz_grad_norm(C.cast(arr, C.c_void_p), len(grads), _limit(max_norm), s, n, c,
-                               work_pointer(work, lib().bfz_norm_work_bytes()), _stream(stream)))
+    rc = lib().bfz_grad_norm(arr, len(grads), _limit(max_norm), s, n, c, work_pointer(work, _work_bytes()), raw_stream(stream))
+    if rc:
+        _check(rc)
 
 
 def shard_grad_norm(plan, grads, norm, work, max_norm=None, coef=None, sumsq=None, stream=None):
@@ -63,14 +64,14 @@ def shard_grad_norm(plan, grads, norm, work, max_norm=None, coef=None, sumsq=Non
     import torch
     arr = _ptr_array(grads, torch.float32, "grads", _weight_sizes(plan))
     s, n, c = _results(norm, coef, sumsq)
-    _check(lib().bfz_shard_grad_norm(plan.handle, C.cast(arr, C.c_void_p), _limit(max_norm), s, n, c,
-                                     work_pointer(work, lib().bfz_norm_work_bytes()), _stream(stream)))
+    _check(lib().bfz_shard_grad_norm(plan.handle, arr, _limit(max_norm), s, n, c, work_pointer(work, _work_bytes()),
+                                     raw_stream(stream)))
 
 
 def clip_coef(sumsq, max_norm, norm, coef, stream=None):
     """norm and coef from a device sumsq (float64), e.g. after an all-reduce."""
     s, n, c = _results(norm, coef, sumsq)
-    _check(lib().bfz_clip_coef(s, _limit(max_norm), n, c, _stream(stream)))
+    _check(lib().bfz_clip_coef(s, _limit(max_norm), n, c, raw_stream(stream)))
 
 
 def clip_grads(grads, coef, outs=None, stream=None):
@@ -79,6 +80,6 @@ def clip_grads(grads, coef, outs=None, stream=None):
     outs = grads if outs is None else outs
     if len(outs) != len(grads):
         raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
-    a, b = _list(grads, "grads"), _list(outs, "outs")
-    _check(lib().bfz_clip_grads(C.cast(a, C.c_void_p), C.cast(b, C.c_void_p), len(grads), _scalar(coef, "coef"),
-                                _stream(stream)))
+    a = _list(grads, "grads")
+    b = a if outs is grads else _list(outs, "outs")
+    _check(lib().bfz_clip_grads(a, b, len(grads), scalar(coef, "coef"), raw_stream(stream)))

@@ -3,8 +3,8 @@ the logits in memory (include/bfz.h: bfz_vocab_loss, bfz_vocab_loss_grad).  The
 head's weight may be the row-major FP8 weight and scale grid that the step
 writes.
 """
-from . import _check, _dev, _stream, lib
-from ._tensors import BF16, E4M3, F32, id_vector, matrix, tile_grid, work_pointer
+from . import _check, lib
+from ._tensors import BF16, E4M3, F32, id_vector, matrix, raw_stream, tile_grid, vector, work_pointer
 
 
 def vocab_loss_workspace(n, vocab, dim, weight_dtype=None, grad=True, device="cuda"):
@@ -36,10 +36,9 @@ def vocab_loss(hidden, weight, targets, loss, lse, work, grid=None, stream=None)
     z = hidden weight^T; loss 0 for a target outside the vocabulary.  hidden:
     (n, dim) bfloat16; weight: (vocab, dim) bfloat16, or E4M3 codes (uint8) with
     their tile scales `grid`; targets: int64 or int32; loss, lse: float32 (n)."""
-    import torch
     args, n, vocab, dim, wcode = _operands(hidden, weight, targets, grid)
-    _check(lib().bfz_vocab_loss(*args, _dev(loss, torch.float32, "loss", n), _dev(lse, torch.float32, "lse", n),
-                                _work(work, n, vocab, dim, wcode, 0), _stream(stream)))
+    _check(lib().bfz_vocab_loss(*args, vector(loss, "loss", n), vector(lse, "lse", n),
+                                _work(work, n, vocab, dim, wcode, 0), raw_stream(stream)))
 
 
 def vocab_loss_grad(hidden, weight, targets, lse, dloss, dhidden, dweight, work, grid=None, accumulate=False,
@@ -47,7 +46,6 @@ def vocab_loss_grad(hidden, weight, targets, lse, dloss, dhidden, dweight, work,
     """Gradient of sum(dloss * loss): dhidden (n, dim) bfloat16 and dweight
     (vocab, dim) bfloat16 or float32, each may be None.  lse: as vocab_loss
     wrote it; dloss: float32 (n).  accumulate adds to dweight."""
-    import torch
     args, n, vocab, dim, wcode = _operands(hidden, weight, targets, grid)
     dh = dw = (None, 0, 0, 0, 0)
     if dhidden is not None:
@@ -58,6 +56,6 @@ def vocab_loss_grad(hidden, weight, targets, lse, dloss, dhidden, dweight, work,
         dw = matrix(dweight, "dweight")
         if dw[1] not in (BF16, F32) or dw[2:4] != (vocab, dim):
             raise ValueError(f"dweight: need bfloat16 or float32 {(vocab, dim)}")
-    _check(lib().bfz_vocab_loss_grad(*args, _dev(lse, torch.float32, "lse", n), _dev(dloss, torch.float32, "dloss", n),
+    _check(lib().bfz_vocab_loss_grad(*args, vector(lse, "lse", n), vector(dloss, "dloss", n),
                                      dh[0], dh[4], dw[0], dw[1], dw[4], int(bool(accumulate)),
-                                     _work(work, n, vocab, dim, wcode, 1), _stream(stream)))
+                                     _work(work, n, vocab, dim, wcode, 1), raw_stream(stream)))

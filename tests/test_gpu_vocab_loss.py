@@ -103,7 +103,8 @@ def _check(h, value, t, got, dloss=None, base=None):
 
 
 SIZES = [(1, 1, 1), (1, 300, 64), (5, 257, 100), (7, 1000, 16), (64, 256, 128), (65, 1000, 72), (128, 511, 192), (129, 700, 130),
-         (130, 513, 1000), (256, 1024, 256), (257, 3000, 320), (300, 9000, 64), (3, 40000, 48)]
+         (130, 513, 1000), (256, 1024, 256), (257, 3000, 320), (300, 9000, 64), (3, 40000, 48),
+         (16, 5000, 200), (17, 600, 136), (15, 127, 520), (600, 2500, 512)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])

@@ -6,7 +6,11 @@ import pytest
 import torch
 
 import blockwise_fp8_zero_amd as bfz
-from blockwise_fp8_zero_amd.norm import _Tensor
+
+
+class _Tensor(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32), ("reserved", C.c_int32)]
+
 
 P = C.c_void_p
 A, B, W = P(0x10000), P(0x20000), P(0x30000)
