@@ -107,9 +107,7 @@ def _check(rc):
 
 
 def _stream(stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    return C.c_void_p(raw_stream(stream))
 
 
 def _dev(t, dtype, name, numel=None):
@@ -448,6 +446,7 @@ def e4m3_encode(x, out, stream=None):
                                  _stream(stream)))
 
 
+from ._tensors import raw_stream  # noqa: E402
 from .norm import clip_coef, clip_grads, grad_norm, norm_workspace, shard_grad_norm  # noqa: E402
 from .embedding import embed, embed_grad, embed_grad_workspace  # noqa: E402
 from .vocab_loss import vocab_loss, vocab_loss_grad, vocab_loss_workspace  # noqa: E402

@@ -218,7 +218,7 @@ extern "C" int bfz_embed_grad(const void* ids, int32_t ids64, int64_t n, const v
     if (!rc && n > 0) rc = check_work(work, where);
     if (rc) return rc;
     // a launch counts its work-items in 32 bits: 2^24 workgroups of 256
-    if (((n + 7) / 8) * ((dim + 255) / 256) + (vocab + 15) / 16 >= (int64_t(1) << 24))
+    if (((n + 7) / 8) * ((dim + 255) / 256) + (vocab + 63) / 64 + 2048 >= (int64_t(1) << 24))
         return fail(BFZ_EINVAL, "%s: %lld tokens of width %lld are too many for one call", where, (long long)n, (long long)dim);
     const EmbedGradArgs a{ids, ids64, dout_dtype, dtable_dtype, dout, dtable, n, vocab, dim, dout_ld, dtable_ld, scale, accumulate};
     return launched(where, launch_embed_grad(a, work, stream));

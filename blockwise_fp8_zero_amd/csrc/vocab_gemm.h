@@ -20,6 +20,13 @@
 // instead a row's 16- or 32-byte pieces are permuted by an XOR with its row
 // number, chosen so that the lanes that read together touch all banks.
 //
+// 8192 x 32768 x 4096 runs at 1.20 to 1.39 PFLOP/s (epilogues included), the
+// library's product of two bf16 matrices at 1.31 to 1.49 there.  The matrix
+// cores are busy 64 to 70% of the cycles, at a clock that their load lowers
+// to 1.9 GHz; LDS 25%.  What is left is the barrier, where all eight waves
+// meet, and with E4M3 the conversions and rescaling.  Letting two groups of
+// four waves take turns at reading and multiplying measured 5-12% slower.
+//
 // E4M3 codes become bf16 exactly; their tile scales are applied to the
 // binary32 sums.  A wave's rows lie in one 128-row tile, so its scale
 // changes only with k: the sums are kept in units of the current tile's scale
@@ -28,6 +35,8 @@
 // 2^-60 of the unit in use, the tile's codes are multiplied by 2^-127
 // instead: what it adds is below 2^-60 of that unit.
 #pragma once
+
+#include <utility>
 
 #include "ops_device.h"
 #include "ops_internal.h"
@@ -61,6 +70,16 @@ struct GemmArgs {
     int64_t blocks_m, blocks_k;  // its sizes
     int32_t tiles_m, tiles_n, splits, group_m;
 };
+
+// f(0), f(1), ..., f(n - 1) with constant arguments.
+template <int... I, class F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int kCount, class F>
+__device__ __forceinline__ void each(F&& f) {
+    each_of(std::make_integer_sequence<int, kCount>{}, f);
+}
 
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // beyond every buffer: loads give zero
 constexpr uint32_t kBufferBytes = 0x80000000u;
@@ -161,16 +180,16 @@ struct FP8KC {
         return static_cast<const char*>(o.p) + row0 * o.ld + k0;
     }
     __device__ __forceinline__ static int64_t advance(const Operand&) { return kBK; }
-    __device__ __forceinline__ static int k_of(int, int, int lane) { return 16 * ((lane & 3) ^ ((lane >> 3) & 3)); }
+    __device__ __forceinline__ static int k_of(int, int, int lane) { return 16 * ((lane & 3) ^ ((lane >> 4) & 3)); }
     __device__ __forceinline__ static uint32_t offset(const Operand& o, int64_t row0, int j, int wave, int lane) {
         const int row = (j * kGemmWaves + wave) * 16 + (lane >> 2);
-        return row0 + row < o.extent ? (uint32_t)(row * o.ld) + 16u * ((lane & 3) ^ ((lane >> 3) & 3)) : kNowhere;
+        return row0 + row < o.extent ? (uint32_t)(row * o.ld) + 16u * ((lane & 3) ^ ((lane >> 4) & 3)) : kNowhere;
     }
     __device__ __forceinline__ FP8KC(uint32_t lds, int row0, int lane) {
         const int g = lane >> 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            at[h] = lds + (row0 + (lane & 15)) * 64 + (((2 * h + (g >> 1)) ^ ((lane >> 1) & 3)) << 4) + 8 * (g & 1);
+            at[h] = lds + (row0 + (lane & 15)) * 64 + (((2 * h + (g >> 1)) ^ ((lane >> 2) & 3)) << 4) + 8 * (g & 1);
     }
     __device__ __forceinline__ Frag read(uint32_t stage, int h, int t) const {
         return lds_read<u32x2>(at[h] + stage + t * 1024);
@@ -282,6 +301,7 @@ template <class A, class B, int kBN, int kWavesM, class Epilogue>
 __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilogue epilogue) {
     constexpr int kWavesN = kGemmWaves / kWavesM;
     constexpr int kTM = kBM / kWavesM / 16, kTN = kBN / kWavesN / 16;
+    static_assert(kTileDim % (kTM * 16) == 0, "a wave's rows share their tile scales");
     constexpr int kStage = A::kBytes + B::kBytes;
     constexpr uint32_t kOther = kStage;  // the second buffer; XOR with it toggles 0 and kStage
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -307,22 +327,29 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
     const int64_t adv_a = A::advance(g.a), adv_b = B::advance(g.b);
     const uint32_t lds_a = lds + wave * 1024, lds_b = lds_a + A::kBytes;
 
-    // loads of the next step into buffer `stage`; past the end of k they give
-    // zero (no branch: the lanes' offsets are selected)
+    // Loads of the next step into buffer `stage`, `parts` calls of which part
+    // p issues its share; past the end of k they give zero (no branch: the
+    // lanes' offsets are selected).
     int64_t left_a = g.a.k - k0, left_b = g.b.k - k0;
-    auto issue = [&](uint32_t stage) {
+    constexpr int kLoads = A::kLoads + B::kLoads;
+    auto issue = [&](uint32_t stage, auto part, auto of) {
+        constexpr int p = decltype(part)::value, parts = decltype(of)::value;
+        constexpr int from = p * kLoads / parts, to = (p + 1) * kLoads / parts;
         const i32x4 ra = buffer_of(base_a), rb = buffer_of(base_b);
+        const int la = (int)max((int64_t)0, min(left_a, (int64_t)kBK)), lb = (int)max((int64_t)0, min(left_b, (int64_t)kBK));
+        each<to - from>([&](auto i) {
+            constexpr int j = from + decltype(i)::value;
+            if constexpr (j < A::kLoads)
+                load_to_lds(ra, A::k_of(j, wave, lane) < la ? off_a[j] : kNowhere, lds_a + stage + j * (kGemmWaves * 1024));
+            else
+                load_to_lds(rb, B::k_of(j - A::kLoads, wave, lane) < lb ? off_b[j - A::kLoads] : kNowhere,
+                            lds_b + stage + (j - A::kLoads) * (kGemmWaves * 1024));
+        });
+        if constexpr (p + 1 < parts) return;
         base_a += adv_a;
         base_b += adv_b;
-        const int la = (int)max((int64_t)0, min(left_a, (int64_t)kBK)), lb = (int)max((int64_t)0, min(left_b, (int64_t)kBK));
         left_a -= kBK;
         left_b -= kBK;
-#pragma unroll
-        for (int j = 0; j < A::kLoads; ++j)
-            load_to_lds(ra, A::k_of(j, wave, lane) < la ? off_a[j] : kNowhere, lds_a + stage + j * (kGemmWaves * 1024));
-#pragma unroll
-        for (int j = 0; j < B::kLoads; ++j)
-            load_to_lds(rb, B::k_of(j, wave, lane) < lb ? off_b[j] : kNowhere, lds_b + stage + j * (kGemmWaves * 1024));
     };
 
     f32x4 acc[kTM][kTN];
@@ -345,48 +372,45 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
     if constexpr (A::kScaled) grid_row = g.grid + min((m0 + wm * kTM * 16) / kTileDim, g.blocks_m - 1) * g.grid_m;
     auto scale_at = [&](int64_t kb) { return grid_row[min(kb, g.blocks_k - 1) * g.grid_k]; };
     float next_scale = 1.0f;
-    if constexpr (A::kScaled) {
-        unit = next_scale = scale_at(k0 / kTileDim);
-    }
+    if constexpr (A::kScaled) unit = next_scale = scale_at(k0 / kTileDim);
 
-    auto multiply = [&](int h) {
-#pragma unroll
-        for (int t = 0; t < kTM; ++t) {
-            const bf16x8 av = A::value(a[h][t], keep);
+    // Half h of a step: its multiplications in kTM parts, with the reads of the
+    // other half (from buffer `from`) and, in the second half, the loads of the
+    // step after next (into buffer `into`) spread over them.  The order is fixed
+    // here: left to itself the compiler issues the reads, or the loads, in a row
+    // while the matrix cores wait (8192 x 32768 x 4096, bf16: 1254 TFLOP/s with
+    // its order, 1316 with this one; all reads in the first part 1298).
+    auto half = [&](auto which, uint32_t from, uint32_t into) {
+        constexpr int h = decltype(which)::value;
+        bf16x8 av = A::value(a[h][0], keep);
+        each<kTM>([&](auto part) {
+            constexpr int t = decltype(part)::value;
+            each<(t + 1) * kTN / kTM - t * kTN / kTM>([&](auto i) {
+                constexpr int u = t * kTN / kTM + decltype(i)::value;
+                b[1 - h][u] = fb.read(from, 1 - h, u);
+            });
+            a[1 - h][t] = fa.read(from, 1 - h, t);
+            if constexpr (h == 1) issue(into, part, std::integral_constant<int, kTM>{});
 #pragma unroll
             for (int u = 0; u < kTN; ++u)
-                acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, B::value(b[h][u], 1.0f), acc[t][u], 0, 0, 0);
-        }
+                acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b[h][u], acc[t][u], 0, 0, 0);
+            if constexpr (t + 1 < kTM) av = A::value(a[h][t + 1], keep);
+            __builtin_amdgcn_sched_barrier(0);
+        });
     };
-
-    // One step from buffer `stage`.  The reads of the other half come first in
-    // each half and are spread over its multiplications.
-    constexpr int kReads = A::kReads * kTM + B::kReads * kTN;
-    auto spread = [&] {
-#pragma unroll
-        for (int i = 0; i < kReads; ++i) {
-            if constexpr (A::kScaled) __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // conversions
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                            // an LDS read
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                            // a matrix instruction
-        }
-    };
+    constexpr std::integral_constant<int, 0> kNone{};
+    constexpr std::integral_constant<int, 1> kOnce{};
     auto step = [&](uint32_t stage) {
-        read_half(stage, 1);
-        multiply(0);
-        spread();
-        __builtin_amdgcn_sched_barrier(0);
+        half(kNone, stage, 0);
         wait_loads();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        issue(stage);
-        read_half(stage ^ kOther, 0);
-        multiply(1);
-        spread();
+        half(kOnce, stage ^ kOther, stage);
         __builtin_amdgcn_sched_barrier(0);
     };
     if (steps > 0) {
-        issue(0);
-        issue(kOther);
+        issue(0, kNone, kOnce);
+        issue(kOther, kNone, kOnce);
         wait_loads();
         __builtin_amdgcn_s_barrier();
         read_half(0, 0);
@@ -431,8 +455,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
 // its k in blocks of 128; a lane loads 32 k of one row of A and of one token
 // straight into registers, the four lanes of a row 64 bytes side by side, two
 // blocks ahead.  Which k a matrix instruction takes is free as long as A and B
-// agree.  The waves' sums meet in LDS.  Here a block's sums fit beside the total, so tile scales
-// are applied block by block.
+// agree.  The waves' sums meet in LDS.  Here a block's sums fit beside the
+// total, so tile scales are applied block by block.  One token on 32768 x 4096
+// codes: 33 us, 4.1 TB/s (64-wide tiles through LDS: 57 us).
 constexpr int kFewRows = 32, kFewTokens = 16, kFewWaves = 4;
 
 template <bool kFp8, class Epilogue>

@@ -276,10 +276,14 @@ __global__ __launch_bounds__(kJoinTokens* kJoinSlots) void join_stats_kernel(con
 
 // Rows with a width or alignment that 16-byte loads cannot take, copied into
 // rows of `width` elements with zeros at the end.
+// T: the widest unit that rows start on and are a multiple of.
 template <class T>
-__global__ void pad_rows_kernel(const T* __restrict__ src, int64_t ld, int64_t rows, int64_t dim, T* __restrict__ dst, int64_t width) {
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < width; c += blockDim.x) dst[r * width + c] = c < dim ? src[r * ld + c] : (T)0;
+__global__ __launch_bounds__(256) void pad_rows_kernel(const T* __restrict__ src, int64_t ld, int64_t rows, int64_t dim,
+                                                       T* __restrict__ dst, int64_t width) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * width; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / width, c = i - r * width;
+        dst[i] = c < dim ? src[r * ld + c] : (T)0;
+    }
 }
 
 // Largest |dloss| of the tokens that count; 1 where there is none.
@@ -323,25 +327,6 @@ __global__ __launch_bounds__(256) void finish_hidden_kernel(const float* __restr
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// Vocabulary rows of a piece: dz and a padded copy of the piece's weights
-// take at most 512 MiB each.
-int64_t piece_rows(int64_t n, int64_t vocab, int64_t dim) {
-    const int64_t most = int64_t(512) << 20;
-    const int64_t by_dz = most / (2 * std::max<int64_t>(n, 1)), by_copy = most / (2 * up(dim, 64));
-    const int64_t rows = std::max<int64_t>(1024, std::min(by_dz, by_copy) / 256 * 256);
-    return std::min(rows, up(vocab, 256));
-}
-
-struct Work {
-    float2* partial;
-    float* target_logit;
-    void *hidden, *weight;  // padded copies
-    bf16_t* dz;
-    float* sums;
-    float* unit;
-    int64_t bytes;
-};
-
 constexpr int waves_m_of(int bn) { return bn == 64 ? 8 : 4; }
 
 // Time of a product of `tiles` 256 x bn tiles and `steps` steps of k, in
@@ -379,16 +364,24 @@ int best_width(int64_t n, int64_t rows, int64_t dim, double* least) {
     }
     return best;
 }
-Rows logits_rows(int64_t n, int64_t rows, int64_t dim) {
+Rows logits_rows(int64_t n, int64_t rows, int64_t dim, double* us = nullptr) {
+    double whole = 0.0, rest;
     if (n <= kFewTokens) return Rows{0, kFewTokens};
-    double whole, rest;
     const int bn = best_width(n, rows, dim, &whole);
+    if (us) *us = whole;
     const int64_t across = up(n, 256) / 256, tiles = up(rows, kBM) / kBM * across;
     const int64_t full = tiles / 256 * 256 / across * kBM;
     if (full == 0 || full >= rows) return Rows{0, bn};
     const int rest_bn = best_width(n, rows - full, dim, &rest);
     const double both = product_us(full / kBM * across, 256, up(dim, kBK) / kBK) + rest;
-    return both < whole ? Rows{full, rest_bn} : Rows{0, bn};
+    if (both >= whole) return Rows{0, bn};
+    if (us) *us = both;
+    return Rows{full, rest_bn};
+}
+double logits_us(int64_t n, int64_t rows, int64_t dim) {
+    double us = double(rows) * double(dim) * 5e-7;  // few tokens: bound by the weights
+    logits_rows(n, rows, dim, &us);
+    return us;
 }
 
 // Of dh: few tiles and a long k (the piece's rows), so k is split too; each
@@ -400,15 +393,49 @@ Rows logits_rows(int64_t n, int64_t rows, int64_t dim) {
 struct HiddenShape {
     int bn, splits;
 };
-HiddenShape hidden_shape(int64_t n, int64_t dim, int64_t piece) {
+HiddenShape hidden_shape(int64_t n, int64_t dim, int64_t piece, double* product = nullptr) {
     HiddenShape best{0, 1};
     double least = 0.0;
     for (int bn : kWidths)
-        for (int s = 1; s <= 64 && (s == 1 || piece / s >= 256); s *= 2) {
+        for (int s = 1; s <= 64 && (s == 1 || piece / s >= 256); s += s < 16 ? 1 : 8) {
             const int64_t tiles = up(dim, kBM) / kBM * (up(n, bn) / bn);
-            const double us = product_us(tiles * s, bn, up(piece, kBK) / kBK / s) + 1.6e-6 * double(n) * double(dim) * s;
-            if (!best.bn || us < least) best = HiddenShape{bn, s}, least = us;
+            const double one = product_us(tiles * s, bn, up(piece, kBK) / kBK / s);
+            const double us = one + 1.6e-6 * double(n) * double(dim) * s;
+            if (!best.bn || us < least) {
+                best = HiddenShape{bn, s}, least = us;
+                if (product) *product = one;
+            }
         }
+    return best;
+}
+
+// Vocabulary rows of a piece.  Longer pieces have fewer half-filled rounds and
+// add to dh's sums less often; a dz of 128 MiB stays in the last-level cache,
+// where its products read it (8192 x 131072 x 4096: dz 7.34 ms in pieces of 8192
+// rows, 8.05 in pieces of 32768, the three products 20.6 and 21.2 ms; but 4000 x
+// 100000 x 2048: 4.96 ms in seven pieces, 4.26 in one of 128 MiB or 1 GiB of dz).
+// Chosen by the modelled time; a piece's dz and a padded copy of its weights
+// take 1 GiB each at most.
+double piece_us(int64_t n, int64_t rows, int64_t dim) {
+    double hidden;
+    hidden_shape(n, dim, rows, &hidden);
+    const double z = logits_us(n, rows, dim) * (2 * n * rows > (int64_t(128) << 20) ? 1.08 : 1.0);
+    const double weight = product_us(up(dim, kBM) / kBM * (up(rows, 256) / 256), 256, up(n, kBK) / kBK);
+    return z + hidden + weight + 15.0;
+}
+int64_t piece_rows(int64_t n, int64_t vocab, int64_t dim) {
+    int64_t best = 0;
+    double least = 0.0;
+    for (int shift = 27; shift <= 30; ++shift) {
+        const int64_t most = int64_t(1) << shift;
+        const int64_t by_dz = most / (2 * std::max<int64_t>(n, 1)), by_copy = (int64_t(1) << 30) / (2 * up(dim, 64));
+        const int64_t rows = std::min(std::max<int64_t>(1024, std::min(by_dz, by_copy) / 256 * 256), up(vocab, 256));
+        const int64_t full = vocab / rows, rest = vocab - full * rows;
+        const double us = double(full) * piece_us(n, rows, dim) + (rest ? piece_us(n, rest, dim) : 0.0) +
+                          3e-7 * double(full + (rest > 0) - 1) * double(n) * double(dim);
+        if (!best || us < least) best = rows, least = us;
+        if (rows >= vocab) break;
+    }
     return best;
 }
 
@@ -418,6 +445,16 @@ int64_t stat_slots(int64_t rows, int width) {
     return width == kFewTokens ? up(rows, kFewRows) / kFewRows : up(rows, kBM) / kBM * waves_m_of(width);
 }
 int64_t most_slots(int64_t vocab) { return up(vocab, kBM) / kBM * 8; }
+
+struct Work {
+    float2* partial;
+    float* target_logit;
+    void *hidden, *weight;  // padded copies
+    bf16_t* dz;
+    float* sums;
+    float* unit;
+    int64_t bytes;
+};
 
 Work work_of(void* work, int64_t n, int64_t vocab, int64_t dim, int fp8, int grad) {
     Work w{};
@@ -514,12 +551,21 @@ int hidden_grad(int fp8, int bn, const GemmArgs& g, const SumEpilogue& e, void* 
     }
 }
 
-template <class T>
+// All sizes in bytes.
 int pad_rows(const void* src, int64_t ld, int64_t rows, int64_t dim, void* dst, int64_t width, void* stream) {
-    const uint32_t wgs = (uint32_t)std::min<int64_t>(rows, 65536);
-    hipLaunchKernelGGL(pad_rows_kernel<T>, dim3(wgs), dim3(256), 0, (hipStream_t)stream, static_cast<const T*>(src), ld, rows, dim,
-                       static_cast<T*>(dst), width);
-    return hipGetLastError();
+    const uint64_t marks = reinterpret_cast<uintptr_t>(src) | (uint64_t)ld | (uint64_t)dim;
+    const auto launch = [&](auto unit) {
+        typedef decltype(unit) T;
+        const int64_t n = rows * width / (int64_t)sizeof(T);
+        hipLaunchKernelGGL(pad_rows_kernel<T>, dim3((uint32_t)std::min<int64_t>((n + 255) / 256, 1 << 20)), dim3(256), 0,
+                           (hipStream_t)stream, static_cast<const T*>(src), ld / (int64_t)sizeof(T), rows, dim / (int64_t)sizeof(T),
+                           static_cast<T*>(dst), width / (int64_t)sizeof(T));
+        return (int)hipGetLastError();
+    };
+    if (marks % 8 == 0) return launch(uint64_t{});
+    if (marks % 4 == 0) return launch(uint32_t{});
+    if (marks % 2 == 0) return launch(uint16_t{});
+    return launch(uint8_t{});
 }
 
 bool loadable(const void* p, int64_t ld, int64_t dim, int size) {
@@ -543,7 +589,7 @@ int source_of(const VocabLossArgs& a, const Work& w, Source* s, void* stream) {
         return hipSuccess;
     }
     s->hidden = Operand{w.hidden, s->width * 2, a.n, s->width};
-    return pad_rows<uint16_t>(a.hidden, a.hidden_ld, a.n, a.dim, w.hidden, s->width, stream);
+    return pad_rows(a.hidden, a.hidden_ld * 2, a.n, a.dim * 2, w.hidden, s->width * 2, stream);
 }
 
 // Rows [first, first + rows) of the weights, rows in extent and dim in k.
@@ -554,8 +600,7 @@ int weight_piece(const VocabLossArgs& a, const Work& w, const Source& s, int64_t
         return hipSuccess;
     }
     *o = Operand{w.weight, s.width * s.esize, rows, s.width};
-    return a.fp8 ? pad_rows<uint8_t>(p, a.weight_ld, rows, a.dim, w.weight, s.width, stream)
-                 : pad_rows<uint16_t>(p, a.weight_ld, rows, a.dim, w.weight, s.width, stream);
+    return pad_rows(p, a.weight_ld * s.esize, rows, a.dim * s.esize, w.weight, s.width * s.esize, stream);
 }
 
 // The tile scales of the piece that starts at vocabulary row `first`.
