@@ -189,7 +189,7 @@ class Plan:
         self.dims = [tuple(int(x) for x in d) for d in dims]
         arr = (C.c_int64 * (3 * max(1, len(self.dims))))(*[x for d in self.dims for x in d])
         h = C.c_void_p()
-        _check(lib().bfz_plan_create(C.cast(arr, C.c_void_p), len(self.dims), D, rank, C.byref(h)))
+        _check(lib().bfz_plan_create(arr, len(self.dims), D, rank, C.byref(h)))
         self._h = h
         self.D, self.rank = D, rank
         # elements of each weight, cells of its scale grid and of its transposed copy's
@@ -226,7 +226,7 @@ class Plan:
 
     def tile(self, slot):
         out = (C.c_int64 * 6)()
-        _check(lib().bfz_plan_tile(self._h, slot, C.cast(out, C.c_void_p)))
+        _check(lib().bfz_plan_tile(self._h, slot, out))
         return tuple(out)
 
     def close(self):
@@ -248,7 +248,7 @@ def paramwise_split(dims, D):
     flat = (C.c_int64 * (3 * max(1, len(dims))))(*[int(x) for d in dims for x in d])
     bop = np.empty(len(dims), dtype=np.int32)
     be = np.empty(D, dtype=np.int64)
-    _check(lib().bfz_paramwise_split(C.cast(flat, C.c_void_p), len(dims), D,
+    _check(lib().bfz_paramwise_split(flat, len(dims), D,
                                      bop.ctypes.data_as(C.c_void_p), be.ctypes.data_as(C.c_void_p)))
     return bop, be
 
@@ -298,9 +298,9 @@ def pack_shard(plan: Plan, srcs, dst, stream=None):
     arr = _ptr_array(srcs, torch.float32, "srcs", _weight_sizes(plan))
     d, stride = _tile_array(dst, plan.shard_tiles, "dst")
     if stride in (None, TILE_ELEMS):
-        _check(lib().pack_shard(plan.handle, C.cast(arr, C.c_void_p), d, _stream(stream)))
+        _check(lib().pack_shard(plan.handle, arr, d, _stream(stream)))
     else:
-        _check(lib().pack_shard_strided(plan.handle, C.cast(arr, C.c_void_p), d, stride,
+        _check(lib().pack_shard_strided(plan.handle, arr, d, stride,
                                         _stream(stream)))
 
 
@@ -313,7 +313,7 @@ def pack_shard_strided(plan: Plan, srcs, dst, dst_stride, stream=None):
     need = (q - 1) * int(dst_stride) + TILE_ELEMS if q else 0
     arr = _ptr_array(srcs, torch.float32, "srcs", _weight_sizes(plan))
     d = _dev(dst, torch.float32, "dst", need)
-    _check(lib().pack_shard_strided(plan.handle, C.cast(arr, C.c_void_p), d, int(dst_stride),
+    _check(lib().pack_shard_strided(plan.handle, arr, d, int(dst_stride),
                                     _stream(stream)))
 
 
@@ -362,7 +362,7 @@ def fold_adamw_fp8_step(plan: Plan, grads, master, m, v, codes, scale_inv, hp, s
     args = [p, mm, vv, _dev(codes, torch.uint8, "codes", n),
             _dev(scale_inv, torch.float32, "scale_inv", q)]
     name, scale = _clip("fold_adamw_fp8_step", grad_scale)
-    _check(getattr(lib(), name)(plan.handle, C.cast(arr, C.c_void_p), *args,
+    _check(getattr(lib(), name)(plan.handle, arr, *args,
                                 C.byref(_hparams(hp)), C.byref(opts), *scale, _stream(stream)))
 
 
@@ -383,8 +383,8 @@ def fold_adamw_fp8_step_unpack(plan: Plan, grads, master, m, v, codes, scale_inv
     (p, mm, vv), opts = _state(master, m, v, q, scale_pow2)
     name, scale = _clip("fold_adamw_fp8_step_unpack", grad_scale)
     _check(getattr(lib(), name)(
-        plan.handle, C.cast(g, C.c_void_p), p, mm, vv, c, sc, C.cast(a8, C.c_void_p),
-        C.cast(asc, C.c_void_p), C.byref(_hparams(hp)), C.byref(opts), *scale, _stream(stream)))
+        plan.handle, g, p, mm, vv, c, sc, a8,
+        asc, C.byref(_hparams(hp)), C.byref(opts), *scale, _stream(stream)))
 
 
 def fold_adamw_fp8_step_unpack_t(plan: Plan, grads, master, m, v, codes, scale_inv, dst_fp8,
@@ -408,8 +408,8 @@ def fold_adamw_fp8_step_unpack_t(plan: Plan, grads, master, m, v, codes, scale_i
     (p, mm, vv), opts = _state(master, m, v, q, True)
     name, scale = _clip("fold_adamw_fp8_step_unpack_t", grad_scale)
     _check(getattr(lib(), name)(
-        plan.handle, C.cast(g, C.c_void_p), p, mm, vv, c, sc, C.cast(a8, C.c_void_p),
-        C.cast(asc, C.c_void_p), C.cast(t8, C.c_void_p), C.cast(tsc, C.c_void_p),
+        plan.handle, g, p, mm, vv, c, sc, a8,
+        asc, t8, tsc,
         C.byref(_hparams(hp)), C.byref(opts), *scale, _stream(stream)))
 
 
@@ -422,7 +422,7 @@ def unpack_fp8(plan: Plan, codes, scale_inv, dst_fp8, dst_scale, stream=None):
     q = plan.shard_tiles
     _check(lib().unpack_fp8(plan.handle, _dev(codes, torch.uint8, "codes", q * TILE_ELEMS),
                             _dev(scale_inv, torch.float32, "scale_inv", q),
-                            C.cast(a8, C.c_void_p), C.cast(asc, C.c_void_p), _stream(stream)))
+                            a8, asc, _stream(stream)))
 
 
 def transpose_pow2(plan: Plan, codes, scale_inv, dst_t, dst_t_scale, stream=None):
@@ -434,7 +434,7 @@ def transpose_pow2(plan: Plan, codes, scale_inv, dst_t, dst_t_scale, stream=None
     asc = _ptr_array(dst_t_scale, torch.float32, "dst_t_scale", _t_grid_sizes(plan))
     _check(lib().bfz_transpose_pow2(plan.handle, _dev(codes, torch.uint8, "codes", q * TILE_ELEMS),
                                     _dev(scale_inv, torch.float32, "scale_inv", q),
-                                    C.cast(a8, C.c_void_p), C.cast(asc, C.c_void_p),
+                                    a8, asc,
                                     _stream(stream)))
 
 

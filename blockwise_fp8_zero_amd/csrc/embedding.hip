@@ -155,17 +155,23 @@ __device__ __forceinline__ int32_t count_before(const int32_t* run, int j0, int 
     return before;
 }
 
-// A workgroup ranks 64 tokens of a run: its waves share out the run's ids.
+// A workgroup ranks kGroup tokens of a run: its waves, and the 64 / kGroup
+// lanes of each that hold the same token, share out the run's ids.
+template <int kGroup>
 __global__ __launch_bounds__(kRankThreads) void rank_runs_kernel(const void* ids, int ids64, int64_t n, int64_t vocab,
                                                                  int32_t* keys, int32_t* pos) {
+    constexpr int kLanes = 64 / kGroup;
     __shared__ alignas(16) int32_t run[kRun];
     __shared__ int32_t count[kRankWaves][64];
-    const int64_t base = (int64_t)(blockIdx.x / (kRun / 64)) * kRun;
-    const int group = (int)(blockIdx.x % (kRun / 64)) * 64;
+    const int64_t base = (int64_t)(blockIdx.x / (kRun / kGroup)) * kRun;
+    const int group = (int)(blockIdx.x % (kRun / kGroup)) * kGroup;
     const int len = (int)(n - base < kRun ? n - base : kRun);
     if (group >= len) return;
-    const int share = (len + kRankWaves * 16 - 1) / (kRankWaves * 16) * 16;  // ids per wave
-    for (int j = threadIdx.x; j < share * kRankWaves; j += kRankThreads) {
+    constexpr int kUnit = kRankWaves * kLanes * 16;
+    const int share = (len + kUnit - 1) / kUnit * kLanes * 16;  // ids per wave
+#pragma unroll
+    for (int u = 0; u < kRun / kRankThreads; ++u) {
+        const int j = u * kRankThreads + threadIdx.x;
         int32_t k = 0x7FFFFFFF;  // past the end: after every key
         if (j < len) {
             const int64_t r = row_of(ids, ids64, base + j, vocab);
@@ -175,18 +181,22 @@ __global__ __launch_bounds__(kRankThreads) void rank_runs_kernel(const void* ids
     }
     __syncthreads();
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int i = group + lane;
+    const int i = group + lane % kGroup;
     const int32_t key = i < len ? run[i] : 0;
-    const int j0 = w * share, j1 = j0 + share;
+    const int w0 = w * share, w1 = w0 + share;
+    const int j0 = w0 + lane / kGroup * (share / kLanes), j1 = j0 + share / kLanes;
     int32_t before;
-    if (j1 <= group) before = count_before<1>(run, j0, j1, i, key);
-    else if (j0 >= group + 64) before = count_before<-1>(run, j0, j1, i, key);
+    if (w1 <= group) before = count_before<1>(run, j0, j1, i, key);
+    else if (w0 >= group + kGroup) before = count_before<-1>(run, j0, j1, i, key);
     else before = count_before<0>(run, j0, j1, i, key);
     count[w][lane] = before;
     __syncthreads();
-    if (w != 0 || i >= len) return;
+    if (w != 0 || lane >= kGroup || i >= len) return;
+    before = 0;
 #pragma unroll
-    for (int x = 1; x < kRankWaves; ++x) before += count[x][lane];
+    for (int x = 0; x < kRankWaves; ++x)
+#pragma unroll
+        for (int y = 0; y < kLanes; ++y) before += count[x][y * kGroup + lane];
     keys[base + before] = key;
     pos[base + before] = (int32_t)(base + i);
 }
@@ -214,7 +224,7 @@ struct FillArgs {
     int32_t rows, wgs;
 };
 
-template <class O, int kVec>
+template <class O>
 __device__ __forceinline__ void fill_absent(const FillArgs& f, int64_t wg, const int32_t* keys, int64_t n, int64_t len) {
     __shared__ int32_t present[kFillRows];
     const int64_t v0 = wg * f.rows;
@@ -228,13 +238,18 @@ __device__ __forceinline__ void fill_absent(const FillArgs& f, int64_t wg, const
         if (at < end && keys[at] == v) present[threadIdx.x & 63] = 1;
     }
     __syncthreads();
-    float zero[kVec];
-#pragma unroll
-    for (int l = 0; l < kVec; ++l) zero[l] = 0.0f;
     for (int r = 0; r < f.rows; ++r) {
         if (present[r]) continue;
-        O* dst = static_cast<O*>(f.dtable) + (v0 + r) * f.ld;
-        for (int64_t c = (int64_t)threadIdx.x * kVec; c < f.dim; c += kThreads * kVec) store_piece<O, kVec>(dst + c, zero);
+        // whole 16-byte blocks between the row's ends, whatever its alignment
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        constexpr int kPer = 16 / sizeof(O);
+        O* row = static_cast<O*>(f.dtable) + (v0 + r) * f.ld;
+        const int64_t skew = (16 - (reinterpret_cast<uintptr_t>(row) & 15u)) % 16 / sizeof(O);
+        const int64_t head = skew < f.dim ? skew : f.dim;
+        const int64_t blocks = (f.dim - head) / kPer, tail = head + blocks * kPer;
+        for (int64_t c = threadIdx.x; c < blocks; c += kThreads) reinterpret_cast<u32x4*>(row + head)[c] = u32x4{0u, 0u, 0u, 0u};
+        if ((int64_t)threadIdx.x < head) row[threadIdx.x] = (O)0.0f;
+        else if (tail + threadIdx.x - head < f.dim) row[tail + threadIdx.x - head] = (O)0.0f;
     }
 }
 
@@ -242,13 +257,13 @@ __device__ __forceinline__ void fill_absent(const FillArgs& f, int64_t wg, const
 // a token advance together, so their loads overlap.  Workgroups past the tokens
 // fill the absent rows meanwhile: the merge waits for its searches, the fill
 // for memory.
-template <int kRuns, class O, int kVec>
+template <int kRuns, class O>
 __global__ __launch_bounds__(kThreads) void merge_runs_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ pos,
                                                               int32_t* __restrict__ out_keys, int32_t* __restrict__ out_pos,
                                                               int64_t n, int64_t len, int steps, FillArgs fill) {
     const int64_t merges = (n + kThreads - 1) / kThreads;
     if (blockIdx.x >= merges) {
-        fill_absent<O, kVec>(fill, blockIdx.x - merges, keys, n, len);
+        fill_absent<O>(fill, blockIdx.x - merges, keys, n, len);
         return;
     }
     const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -283,10 +298,10 @@ __global__ __launch_bounds__(kThreads) void merge_runs_kernel(const int32_t* __r
     out_pos[at] = pos[t];
 }
 
-template <int kRuns, class O, int kVec>
+template <int kRuns, class O>
 void merge_runs(const int32_t* keys, const int32_t* pos, int32_t* out_keys, int32_t* out_pos, int64_t n, int64_t len, int steps,
                 const FillArgs& fill, void* stream) {
-    hipLaunchKernelGGL((merge_runs_kernel<kRuns, O, kVec>), dim3((uint32_t)((n + kThreads - 1) / kThreads + fill.wgs)), dim3(kThreads),
+    hipLaunchKernelGGL((merge_runs_kernel<kRuns, O>), dim3((uint32_t)((n + kThreads - 1) / kThreads + fill.wgs)), dim3(kThreads),
                        0, (hipStream_t)stream, keys, pos, out_keys, out_pos, n, len, steps, fill);
 }
 
@@ -352,7 +367,7 @@ __global__ __launch_bounds__(kThreads) void segment_kernel(const void* dout_p, v
     __shared__ int32_t key[kMaxPer + 2], row[kMaxPer];
     const int64_t sums = a.ranges * a.slabs;
     if (blockIdx.x >= sums) {
-        fill_absent<O, kVec>(fill, blockIdx.x - sums, a.keys, a.n, a.n > 0 ? a.n : 1);
+        fill_absent<O>(fill, blockIdx.x - sums, a.keys, a.n, a.n > 0 ? a.n : 1);
         return;
     }
     const int64_t range = blockIdx.x / a.slabs;
@@ -499,18 +514,21 @@ int segments(const EmbedGradArgs& a, const GradWork& g, void* stream) {
     int at = 0;
     if (a.n > 0) {
         const int64_t runs = (a.n + kRun - 1) / kRun;
-        hipLaunchKernelGGL(rank_runs_kernel, dim3((uint32_t)(runs * (kRun / 64))), dim3(kRankThreads), 0, (hipStream_t)stream,
-                           a.ids, a.ids64, a.n, a.vocab, g.keys[0], g.pos[0]);
+        // few tokens: 16 a workgroup, so that they reach the device's width
+        const bool few = a.n <= 8192;
+        const auto rank = few ? rank_runs_kernel<16> : rank_runs_kernel<64>;
+        hipLaunchKernelGGL(rank, dim3((uint32_t)(runs * (kRun / (few ? 16 : 64)))), dim3(kRankThreads), 0, (hipStream_t)stream, a.ids,
+                           a.ids64, a.n, a.vocab, g.keys[0], g.pos[0]);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
     for (int64_t len = kRun; len < a.n; len *= kMergeRuns) {
         int steps = 1;  // a search over m entries takes at most bits(m) steps
         while ((int64_t(1) << steps) <= len) ++steps;
-        const auto merge = a.n <= 2 * len   ? merge_runs<2, O, kVec>
-                           : a.n <= 4 * len ? merge_runs<4, O, kVec>
-                           : a.n <= 8 * len ? merge_runs<8, O, kVec>
-                                            : merge_runs<kMergeRuns, O, kVec>;
+        const auto merge = a.n <= 2 * len   ? merge_runs<2, O>
+                           : a.n <= 4 * len ? merge_runs<4, O>
+                           : a.n <= 8 * len ? merge_runs<8, O>
+                                            : merge_runs<kMergeRuns, O>;
         const FillArgs none{};
         const bool last = len * kMergeRuns >= a.n;
         merge(g.keys[at], g.pos[at], g.keys[at ^ 1], g.pos[at ^ 1], a.n, len, steps, last ? fill : none, stream);

@@ -232,8 +232,10 @@ int check_loss(const void* hidden, int64_t hidden_ld, int64_t n, const void* wei
     if (n < 0 || vocab < 1 || dim < 1 || n > (int64_t(1) << 24) || vocab > (int64_t(1) << 27) || dim > (int64_t(1) << 20))
         return fail(BFZ_EINVAL, "%s: need 0 <= n <= 2^24, 1 <= vocab <= 2^27, 1 <= dim <= 2^20", where);
     // a launch counts its work-items in 32 bits: under 2^23 tiles of 512
-    if (((vocab + 255) / 256) * ((n + 63) / 64) >= (int64_t(1) << 23))
-        return fail(BFZ_EINVAL, "%s: %lld tokens by %lld rows are too many for one call", where, (long long)n, (long long)vocab);
+    if (((vocab + 255) / 256) * ((n + 63) / 64) >= (int64_t(1) << 23) ||
+        ((dim + 255) / 256) * ((n + 63) / 64) >= (int64_t(1) << 23))
+        return fail(BFZ_EINVAL, "%s: %lld tokens by %lld rows of width %lld are too many for one call", where, (long long)n,
+                    (long long)vocab, (long long)dim);
     if (weight_dtype != kBF16 && weight_dtype != kE4M3)
         return fail(BFZ_EINVAL, "%s: the weight must be BFZ_BF16 or BFZ_E4M3", where);
     if ((weight_dtype == kE4M3) != (grid != nullptr))

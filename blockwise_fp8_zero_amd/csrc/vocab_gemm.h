@@ -507,6 +507,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_tokens_kernel(GemmArgs g, 
                 b[x][l] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, in ? (int)(row_b + (uint32_t)(k * 2)) : (int)kNowhere, 0, 0));
             }
         }
+        __builtin_amdgcn_sched_barrier(0);  // all of them before the first use
 #pragma unroll
         for (int x = 0; x < kAhead; ++x)
 #pragma unroll

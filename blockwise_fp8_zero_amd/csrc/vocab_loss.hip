@@ -198,32 +198,67 @@ struct WeightGradEpilogue {
             O* row = dw + v * ld + m0;
 #pragma unroll
             for (int r = 0; r < kTM; ++r) {
-                const f32x4 x = acc[r][u] * most;
-                O* p = row + 16 * r;
-                if (vec && m0 + 16 * r + 4 <= dim) {
-                    if constexpr (sizeof(O) == 4) {
-                        f32x4 y = x;
-                        if (add) y += *reinterpret_cast<const f32x4*>(p);
-                        *reinterpret_cast<f32x4*>(p) = y;
-                    } else {
-                        f32x4 y = x;
-                        if (add) {
-                            const u32x2 o = *reinterpret_cast<const u32x2*>(p);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) y[i] += __uint_as_float((i & 1) ? (o[i >> 1] & 0xFFFF0000u) : (o[i >> 1] << 16));
-                        }
-                        const u32x2 o = {pack2<bf16_t>(y[0], y[1]), pack2<bf16_t>(y[2], y[3])};
-                        *reinterpret_cast<u32x2*>(p) = o;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (m0 + 16 * r + i < dim) p[i] = Elem<O>::to(add ? Elem<O>::get(p[i]) + x[i] : x[i]);
-                }
+                put(row + 16 * r, m0 + 16 * r, acc[r][u] * most);
             }
         }
     }
+    // 4 elements of a row from column c on
+    __device__ __forceinline__ void put(O* p, int64_t c, f32x4 x) const {
+        if (vec && c + 4 <= dim) {
+            if constexpr (sizeof(O) == 4) {
+                if (add) x += *reinterpret_cast<const f32x4*>(p);
+                *reinterpret_cast<f32x4*>(p) = x;
+            } else {
+                if (add) {
+                    const u32x2 o = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] += __uint_as_float((i & 1) ? (o[i >> 1] & 0xFFFF0000u) : (o[i >> 1] << 16));
+                }
+                const u32x2 o = {pack2<bf16_t>(x[0], x[1]), pack2<bf16_t>(x[2], x[3])};
+                *reinterpret_cast<u32x2*>(p) = o;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c + i < dim) p[i] = Elem<O>::to(add ? Elem<O>::get(p[i]) + x[i] : x[i]);
+        }
+    }
 };
+
+// Rows of dW for few tokens, where a product of matrix tiles would be all
+// first loads and epilogue: a thread keeps its columns of every token's h in
+// registers and walks rows, whose dz the workgroup has read into LDS.  Bound
+// by writing dW (2 tokens of 83873 x 896: 51 us, 3.0 TB/s).
+constexpr int kFewGradRows = 64, kFewGradCols = 4;
+template <class O>
+__global__ __launch_bounds__(256) void few_weight_grad_kernel(const bf16_t* __restrict__ hidden, int64_t hidden_ld, int64_t dim,
+                                                              const bf16_t* __restrict__ dz, int64_t width, int64_t n, int64_t rows,
+                                                              WeightGradEpilogue<O> out) {
+    __shared__ float d[kFewGradRows][kFewTokens];
+    const int64_t v0 = (int64_t)blockIdx.x * kFewGradRows, c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * kFewGradCols;
+    const int count = (int)(rows - v0 < kFewGradRows ? rows - v0 : kFewGradRows);
+    const float most = *out.unit;
+    for (int i = threadIdx.x; i < kFewGradRows * kFewTokens; i += 256) {
+        const int t = i / kFewGradRows, r = i % kFewGradRows;
+        d[r][t] = t < n && r < count ? Elem<bf16_t>::get(dz[t * width + v0 + r]) * most : 0.0f;
+    }
+    float h[kFewTokens][kFewGradCols];
+#pragma unroll
+    for (int t = 0; t < kFewTokens; ++t)
+#pragma unroll
+        for (int l = 0; l < kFewGradCols; ++l)
+            h[t][l] = t < n && c + l < dim ? Elem<bf16_t>::get(hidden[t * hidden_ld + c + l]) : 0.0f;
+    __syncthreads();
+    if (c >= dim) return;
+    for (int r = 0; r < count; ++r) {
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int t = 0; t < kFewTokens; ++t)
+#pragma unroll
+            for (int l = 0; l < kFewGradCols; ++l) x[l] = __builtin_fmaf(d[r][t], h[t][l], x[l]);
+        out.put(out.dw + (out.first + v0 + r) * out.ld + c, c, x);
+    }
+}
 
 // lse and loss of a token from its partial statistics: 16 tokens a
 // workgroup, 16 slots at a time.
@@ -527,9 +562,8 @@ int launch_kr(const GemmArgs& g, const Epilogue& e, void* stream) {
 template <bool kFp8, class Epilogue>
 int launch_few(GemmArgs g, const Epilogue& e, void* stream) {
     g.tiles_m = (int32_t)(up(g.a.extent, kFewRows) / kFewRows);
-    g.tiles_n = (int32_t)(up(g.b.extent, kFewTokens) / kFewTokens);
-    hipLaunchKernelGGL((few_tokens_kernel<kFp8, Epilogue>), dim3((uint32_t)(g.tiles_m * g.tiles_n)), dim3(64 * kFewWaves), 0,
-                       (hipStream_t)stream, g, e);
+    g.tiles_n = 1;
+    hipLaunchKernelGGL((few_tokens_kernel<kFp8, Epilogue>), dim3((uint32_t)g.tiles_m), dim3(64 * kFewWaves), 0, (hipStream_t)stream, g, e);
     return hipGetLastError();
 }
 
@@ -637,6 +671,16 @@ int logits(const VocabLossArgs& a, const Source& s, const Operand& weight, int64
     return hipSuccess;
 }
 
+template <class O>
+int weight_grad_launch(const VocabLossArgs& a, const Work& w, const GemmArgs& d, int64_t rows, int64_t width, const WeightGradEpilogue<O>& e,
+                       void* stream) {
+    if (a.n > kFewTokens) return launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<O>>(d, e, stream);
+    const dim3 grid((uint32_t)((rows + kFewGradRows - 1) / kFewGradRows), (uint32_t)((a.dim + 256 * kFewGradCols - 1) / (256 * kFewGradCols)));
+    hipLaunchKernelGGL(few_weight_grad_kernel<O>, grid, dim3(256), 0, (hipStream_t)stream, static_cast<const bf16_t*>(a.hidden),
+                       a.hidden_ld, a.dim, w.dz, width, a.n, rows, e);
+    return hipGetLastError();
+}
+
 // Rows [first, first + rows) of dW = dz^T h: m is the hidden width, n the
 // vocabulary rows.
 int weight_grad(const VocabLossArgs& a, const Work& w, const Source& s, int64_t first, int64_t rows, int64_t width, void* stream) {
@@ -648,10 +692,10 @@ int weight_grad(const VocabLossArgs& a, const Work& w, const Source& s, int64_t 
     const int32_t vec = a.dweight_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % (f32 ? 16 : 8) == 0;
     if (f32) {
         const WeightGradEpilogue<float> e{static_cast<float*>(a.dweight), a.dweight_ld, a.dim, first, a.vocab, w.unit, a.accumulate, vec};
-        return launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<float>>(d, e, stream);
+        return weight_grad_launch<float>(a, w, d, rows, width, e, stream);
     }
     const WeightGradEpilogue<bf16_t> e{static_cast<bf16_t*>(a.dweight), a.dweight_ld, a.dim, first, a.vocab, w.unit, a.accumulate, vec};
-    return launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<bf16_t>>(d, e, stream);
+    return weight_grad_launch<bf16_t>(a, w, d, rows, width, e, stream);
 }
 
 }  // namespace

@@ -145,7 +145,7 @@ def _loss(grad=False, hidden=A, hld=8, n=4, weight=B, wt=1, wld=8, grid=None, V=
 @pytest.mark.parametrize("kw,rc", [
     (dict(hidden=None), EINVAL), (dict(weight=None), EINVAL), (dict(t=None), EINVAL), (dict(lse=None), EINVAL), (dict(work=None), EINVAL),
     (dict(n=-1), EINVAL), (dict(V=0), EINVAL), (dict(d=0), EINVAL), (dict(n=1 << 25), EINVAL), (dict(V=1 << 28), EINVAL),
-    (dict(d=1 << 21, hld=1 << 21, wld=1 << 21), EINVAL), (dict(n=1 << 24, V=1 << 27), EINVAL), (dict(wt=0), EINVAL), (dict(wt=3), EINVAL),
+    (dict(d=1 << 21, hld=1 << 21, wld=1 << 21), EINVAL), (dict(n=1 << 24, V=1 << 27), EINVAL), (dict(n=1 << 24, d=1 << 20, hld=1 << 20, wld=1 << 20), EINVAL), (dict(wt=0), EINVAL), (dict(wt=3), EINVAL),
     (dict(grid=A), EINVAL), (dict(wt=3, grid=P(0x1002)), EALIGN), (dict(hld=7), EINVAL), (dict(wld=7), EINVAL), (dict(wld=1 << 22), EINVAL),
     (dict(hidden=P(0x1001)), EALIGN), (dict(weight=P(0x1001)), EALIGN), (dict(t=P(0x1004)), EALIGN), (dict(t=P(0x1002), wide=0), EALIGN),
     (dict(lse=P(0x1002)), EALIGN), (dict(work=P(0x1010)), EALIGN),
