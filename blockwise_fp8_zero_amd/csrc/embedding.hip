@@ -238,18 +238,29 @@ __device__ __forceinline__ void fill_absent(const FillArgs& f, int64_t wg, const
         if (at < end && keys[at] == v) present[threadIdx.x & 63] = 1;
     }
     __syncthreads();
-    for (int r = 0; r < f.rows; ++r) {
-        if (present[r]) continue;
-        // whole 16-byte blocks between the row's ends, whatever its alignment
+    for (int r = 0; r < f.rows;) {
+        if (present[r]) {
+            ++r;
+            continue;
+        }
+        // absent rows that lie back to back are one range
+        int end = r + 1;
+        if (f.ld == f.dim)
+            while (end < f.rows && !present[end]) ++end;
+        const int64_t n_elems = (end - r) * f.dim;
+        // whole 16-byte blocks between the range's ends, whatever its alignment
         typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
         constexpr int kPer = 16 / sizeof(O);
         O* row = static_cast<O*>(f.dtable) + (v0 + r) * f.ld;
         const int64_t skew = (16 - (reinterpret_cast<uintptr_t>(row) & 15u)) % 16 / sizeof(O);
-        const int64_t head = skew < f.dim ? skew : f.dim;
-        const int64_t blocks = (f.dim - head) / kPer, tail = head + blocks * kPer;
-        for (int64_t c = threadIdx.x; c < blocks; c += kThreads) reinterpret_cast<u32x4*>(row + head)[c] = u32x4{0u, 0u, 0u, 0u};
+        const int64_t head = skew < n_elems ? skew : n_elems;
+        const int64_t blocks = (n_elems - head) / kPer, tail = head + blocks * kPer;
+        u32x4* block = reinterpret_cast<u32x4*>(row + head);
+#pragma unroll 4
+        for (int64_t c = threadIdx.x; c < blocks; c += kThreads) block[c] = u32x4{0u, 0u, 0u, 0u};
         if ((int64_t)threadIdx.x < head) row[threadIdx.x] = (O)0.0f;
-        else if (tail + threadIdx.x - head < f.dim) row[tail + threadIdx.x - head] = (O)0.0f;
+        else if (tail + threadIdx.x - head < n_elems) row[tail + threadIdx.x - head] = (O)0.0f;
+        r = end;
     }
 }
 
@@ -507,8 +518,8 @@ template <class I, class O, int kVec>
 int segments(const EmbedGradArgs& a, const GradWork& g, void* stream) {
     FillArgs fill{a.dtable, a.vocab, a.dim, a.dtable_ld, 0, 0};
     if (!a.accumulate) {
-        // as many rows as leave the device some 2048 workgroups
-        fill.rows = (int32_t)std::min<int64_t>(kFillRows, std::max<int64_t>(4, a.vocab / 2048));
+        // 128 KiB a workgroup (131072 x 4096: 492 us; 64 KiB 503, 512 KiB 499)
+        fill.rows = (int32_t)std::min<int64_t>(kFillRows, std::max<int64_t>(1, 128 * 1024 / (a.dim * (int64_t)sizeof(O))));
         fill.wgs = (int32_t)((a.vocab + fill.rows - 1) / fill.rows);
     }
     int at = 0;

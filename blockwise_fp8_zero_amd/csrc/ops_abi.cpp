@@ -217,9 +217,12 @@ extern "C" int bfz_embed_grad(const void* ids, int32_t ids64, int64_t n, const v
     if (!rc) rc = check_matrix(dtable, dtable_dtype, vocab, dim, dtable_ld, "dtable", where);
     if (!rc && n > 0) rc = check_work(work, where);
     if (rc) return rc;
-    // a launch counts its work-items in 32 bits: 2^24 workgroups of 256
-    if (((n + 7) / 8) * ((dim + 255) / 256) + (vocab + 63) / 64 + 2048 >= (int64_t(1) << 24))
-        return fail(BFZ_EINVAL, "%s: %lld tokens of width %lld are too many for one call", where, (long long)n, (long long)dim);
+    // a launch counts its work-items in 32 bits: 2^24 workgroups of 256.  A
+    // workgroup fills 64 rows or 128 KiB of them, one row at least.
+    const int64_t fill = dim * dtype_size(dtable_dtype) > 2048 ? vocab / (1 + (128 * 1024) / (dim * dtype_size(dtable_dtype))) * 2 : vocab / 64;
+    if (((n + 7) / 8) * ((dim + 255) / 256) + fill >= (int64_t(1) << 24) - 1)
+        return fail(BFZ_EINVAL, "%s: %lld tokens and %lld rows of width %lld are too many for one call", where, (long long)n,
+                    (long long)vocab, (long long)dim);
     const EmbedGradArgs a{ids, ids64, dout_dtype, dtable_dtype, dout, dtable, n, vocab, dim, dout_ld, dtable_ld, scale, accumulate};
     return launched(where, launch_embed_grad(a, work, stream));
 }
