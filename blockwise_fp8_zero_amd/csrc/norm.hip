@@ -8,6 +8,11 @@
 // relative error.  The sum's order is fixed by the sizes alone: each
 // workgroup takes a fixed share, adds its threads in a tree, and the last workgroup to finish adds the G partial sums in index order, so
 // two runs give the same bits.
+//
+// Bound by reading the gradients, at few of them by the launch: 40 ragged
+// tensors of 70.5M elements, half of them bf16, 46 us (4.6 TB/s), clipped into
+// f32 buffers in another 104 us (4.7 TB/s); the tiles of a 202M-element shard
+// 129 us (6.3 TB/s); one 256 x 384 tensor 5.7 us of a 7 us call.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

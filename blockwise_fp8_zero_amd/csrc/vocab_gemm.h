@@ -20,12 +20,15 @@
 // instead a row's 16- or 32-byte pieces are permuted by an XOR with its row
 // number, chosen so that the lanes that read together touch all banks.
 //
-// 8192 x 32768 x 4096 runs at 1.20 to 1.39 PFLOP/s (epilogues included), the
-// library's product of two bf16 matrices at 1.31 to 1.49 there.  The matrix
-// cores are busy 64 to 70% of the cycles, at a clock that their load lowers
-// to 1.9 GHz; LDS 25%.  What is left is the barrier, where all eight waves
-// meet, and with E4M3 the conversions and rescaling.  Letting two groups of
-// four waves take turns at reading and multiplying measured 5-12% slower.
+// 8192 x 32768 x 4096 runs at 1.13 to 1.39 PFLOP/s (epilogues included; boxes
+// differ by 8%), the library's product of two bf16 matrices at 1.31 to 1.49
+// there.  The matrix cores are busy 66 to 71% of the cycles with bf16 and 55 to
+// 58% with E4M3, at a clock that their load lowers to 1.9 GHz; LDS 17 to 27%.
+// What is left is the barrier, where all eight waves meet, and with E4M3 the
+// conversions and rescaling (2 vector instructions for each matrix one; 0.7
+// with bf16).  Letting two groups of four waves take turns at reading and
+// multiplying measured 5-12% slower, rescaling between the matrix instructions
+// no faster.
 //
 // E4M3 codes become bf16 exactly; their tile scales are applied to the
 // binary32 sums.  A wave's rows lie in one 128-row tile, so its scale
