@@ -428,11 +428,13 @@ double logits_us(int64_t n, int64_t rows, int64_t dim) {
 struct HiddenShape {
     int bn, splits;
 };
+constexpr int64_t kSplitTokens = 16384;  // splits times tokens, unless there are more tokens
+int64_t most_splits(int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(64, kSplitTokens / std::max<int64_t>(n, 1))); }
 HiddenShape hidden_shape(int64_t n, int64_t dim, int64_t piece, double* product = nullptr) {
     HiddenShape best{0, 1};
     double least = 0.0;
     for (int bn : kWidths)
-        for (int s = 1; s <= 64 && (s == 1 || piece / s >= 256); s += s < 16 ? 1 : 8) {
+        for (int s = 1; s <= most_splits(n) && (s == 1 || piece / s >= 256); s += s < 16 ? 1 : 8) {
             const int64_t tiles = up(dim, kBM) / kBM * (up(n, bn) / bn);
             const double one = product_us(tiles * s, bn, up(piece, kBK) / kBK / s);
             const double us = one + 1.6e-6 * double(n) * double(dim) * s;
@@ -449,8 +451,9 @@ HiddenShape hidden_shape(int64_t n, int64_t dim, int64_t piece, double* product 
 // where its products read it (8192 x 131072 x 4096: dz 7.34 ms in pieces of 8192
 // rows, 8.05 in pieces of 32768, the three products 20.6 and 21.2 ms; but 4000 x
 // 100000 x 2048: 4.96 ms in seven pieces, 4.26 in one of 128 MiB or 1 GiB of dz).
-// Chosen by the modelled time; a piece's dz and a padded copy of its weights
-// take 1 GiB each at most.
+// Chosen by the modelled time; a piece's dz and a padded bf16 copy of its
+// weights take 512 MiB each, or those of 1024 rows.
+constexpr int64_t kPieceBytes = int64_t(1) << 29, kLeastRows = 1024;
 double piece_us(int64_t n, int64_t rows, int64_t dim) {
     double hidden;
     hidden_shape(n, dim, rows, &hidden);
@@ -461,10 +464,9 @@ double piece_us(int64_t n, int64_t rows, int64_t dim) {
 int64_t piece_rows(int64_t n, int64_t vocab, int64_t dim) {
     int64_t best = 0;
     double least = 0.0;
-    for (int shift = 27; shift <= 30; ++shift) {
-        const int64_t most = int64_t(1) << shift;
-        const int64_t by_dz = most / (2 * std::max<int64_t>(n, 1)), by_copy = (int64_t(1) << 30) / (2 * up(dim, 64));
-        const int64_t rows = std::min(std::max<int64_t>(1024, std::min(by_dz, by_copy) / 256 * 256), up(vocab, 256));
+    for (int64_t most = kPieceBytes / 4; most <= kPieceBytes; most *= 2) {
+        const int64_t by_dz = most / (2 * std::max<int64_t>(n, 1)), by_copy = kPieceBytes / (2 * up(dim, 64));
+        const int64_t rows = std::min(std::max(kLeastRows, std::min(by_dz, by_copy) / 256 * 256), up(vocab, 256));
         const int64_t full = vocab / rows, rest = vocab - full * rows;
         const double us = double(full) * piece_us(n, rows, dim) + (rest ? piece_us(n, rest, dim) : 0.0) +
                           3e-7 * double(full + (rest > 0) - 1) * double(n) * double(dim);
@@ -491,6 +493,8 @@ struct Work {
     int64_t bytes;
 };
 
+// Each part is as large as any count of tokens up to n needs it (pieces and
+// splits change with n), so that a workspace serves the last, shorter batch too.
 Work work_of(void* work, int64_t n, int64_t vocab, int64_t dim, int fp8, int grad) {
     Work w{};
     char* p = static_cast<char*>(work);
@@ -500,9 +504,9 @@ Work work_of(void* work, int64_t n, int64_t vocab, int64_t dim, int fp8, int gra
         at += up(bytes, 256);
         return q;
     };
-    const int64_t piece = piece_rows(n, vocab, dim), width = up(dim, 64);
+    const int64_t width = up(dim, 64), rows = up(vocab, 256), esize = fp8 ? 1 : 2;
     w.hidden = take(n * width * 2);
-    w.weight = take(piece * width * (fp8 ? 1 : 2));
+    w.weight = take(std::min(std::max(kPieceBytes / 2, kLeastRows * width), rows * width) * esize);
     const int64_t mark = at;
     // the loss and its gradient run one after the other: one space for both
     w.partial = reinterpret_cast<float2*>(take(most_slots(vocab) * n * 8));
@@ -511,8 +515,8 @@ Work work_of(void* work, int64_t n, int64_t vocab, int64_t dim, int fp8, int gra
     if (grad) {
         at = mark;
         w.unit = reinterpret_cast<float*>(take(4));
-        w.dz = reinterpret_cast<bf16_t*>(take(n * piece * 2));
-        w.sums = reinterpret_cast<float*>(take(hidden_shape(n, dim, piece).splits * n * width * 4));
+        w.dz = reinterpret_cast<bf16_t*>(take(std::min(std::max(kPieceBytes, n * kLeastRows * 2), n * rows * 2)));
+        w.sums = reinterpret_cast<float*>(take(std::min(64 * n, std::max(kSplitTokens, n)) * width * 4));
         w.bytes = std::max(w.bytes, at);
     }
     return w;

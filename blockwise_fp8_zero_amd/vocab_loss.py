@@ -8,7 +8,7 @@ from ._tensors import BF16, E4M3, F32, id_vector, matrix, raw_stream, tile_grid,
 
 
 def vocab_loss_workspace(n, vocab, dim, weight_dtype=None, grad=True, device="cuda"):
-    """Workspace of vocab_loss and, with grad, vocab_loss_grad for n tokens.
+    """Workspace of vocab_loss and, with grad, vocab_loss_grad for up to n tokens.
     weight_dtype: torch.bfloat16, or torch.uint8 (the default) for E4M3 codes."""
     import torch
     code = BF16 if weight_dtype == torch.bfloat16 else E4M3

@@ -467,8 +467,9 @@ int bfz_embed(const void* ids, int32_t ids64, int64_t n, const void* table, int3
  * otherwise rows that occur are added to dtable and the others not touched.
  * The tokens are sorted first, so every sum has a fixed order: two runs give
  * the same bits.  dout: [n, dim]; dtable: [vocab, dim]; each BFZ_F32, BFZ_BF16
- * or BFZ_F16.  work: bfz_embed_grad_work_bytes(n, dim) of device memory,
- * 16-byte aligned, not shared by calls that may run at the same time.
+ * or BFZ_F16.  work: bfz_embed_grad_work_bytes(n, dim) of device memory (it
+ * serves every count of tokens up to n), 16-byte aligned, not shared by calls
+ * that may run at the same time.
  * At most 2^27 tokens and 2^27 rows.
  * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
  */
@@ -493,7 +494,8 @@ int bfz_embed_grad(const void* ids, int32_t ids64, int64_t n, const void* dout,
  * (targets64 != 0) or int32.  loss, lse: n floats.
  * work: bfz_vocab_loss_work_bytes(n, vocab, dim, weight_dtype, grad) of device
  * memory, 256-byte aligned, not shared by calls that may run at the same time
- * (grad != 0 covers both calls; 0: bad sizes).  At most 2^24 tokens, 2^27
+ * (grad != 0 covers both calls, and every count of tokens up to n; 0: bad
+ * sizes).  At most 2^24 tokens, 2^27
  * rows, dim 2^20, strides 2^21.
  * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
  */

@@ -182,6 +182,19 @@ def test_embed_grad_strides_and_empty():
     bfz.embed(ids[:0], dt, out)
 
 
+def test_embed_grad_workspace_serves_smaller_batches():
+    torch.manual_seed(11)
+    V, d = 400, 60
+    ids = torch.randint(0, V, (20000,), device="cuda")
+    dout = torch.randn(20000, d, device="cuda")
+    work = bfz.embed_grad_workspace(20000, d)
+    for n in (1, 500, 9000, 16383, 16384, 20000):
+        a, b = torch.empty(V, d, device="cuda"), torch.empty(V, d, device="cuda")
+        bfz.embed_grad(ids[:n], dout[:n], a, work)
+        bfz.embed_grad(ids[:n], dout[:n], b, bfz.embed_grad_workspace(n, d))
+        assert torch.equal(a, b), n
+
+
 def test_embed_past_32_bits():
     """Row offsets past 2^32 elements, both ways."""
     V, d = 1_100_000, 4096

@@ -225,6 +225,21 @@ def test_one_side_only_and_empty():
     assert bool((loss == 0).all()) and bool((dh == 0).all()) and bool((dw == 0).all())
 
 
+def test_a_workspace_serves_smaller_batches():
+    V, d = 5000, 128
+    h, w, grid, value, t = _case(2000, V, d, "fp8")
+    dloss = torch.rand(2000, device="cuda")
+    work = bfz.vocab_loss_workspace(2000, V, d)
+    for n in (1, 16, 17, 300, 1999):
+        want = _run(h[:n], w, grid, t[:n], dloss[:n])
+        work.fill_(0xFF)
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        dh, dw = torch.empty_like(h[:n]), torch.empty(V, d, device="cuda", dtype=torch.bfloat16)
+        bfz.vocab_loss(h[:n], w, t[:n], loss, lse, work, grid=grid)
+        bfz.vocab_loss_grad(h[:n], w, t[:n], lse, dloss[:n], dh, dw, work, grid=grid)
+        assert all(torch.equal(a, b) for a, b in zip(want, (loss, lse, dh, dw))), n
+
+
 def test_gradient_against_differences():
     """(L(h + e x) - L(h - e x)) / 2e along random bf16-exact directions, in
     64 bits from the formula, against <dh, x> of the kernel: off by the

@@ -171,5 +171,10 @@ def test_vocab_loss_work_sizes():
     f = bfz.lib().bfz_vocab_loss_work_bytes
     assert f(-1, 10, 8, 1, 0) == 0 and f(4, 0, 8, 1, 0) == 0 and f(4, 10, 8, 0, 0) == 0
     assert 0 < f(4, 10, 8, 1, 0) <= f(4, 10, 8, 1, 1)
+    # a workspace for n tokens serves every smaller batch
+    for V, d, t in ((131072, 4096, 3), (50001, 1000, 1), (300, 64, 3), (1 << 20, 512, 1)):
+        for grad in (0, 1):
+            sizes = [f(n, V, d, t, grad) for n in (0, 1, 16, 17, 100, 1000, 3000, 4000, 8192, 16384, 16385, 40000)]
+            assert sizes == sorted(sizes), (V, d, t, grad, sizes)
     # dz and the padded copy are bounded, whatever the vocabulary
     assert f(8192, 1 << 20, 4096, 3, 1) < 4 << 30
