@@ -100,7 +100,8 @@ __device__ __forceinline__ i32x4 buffer_of(const char* base) {
 // 16 bytes a lane from memory to LDS at lds + 16 * lane.  In assembly, so
 // that the compiler does not wait for it at the next LDS read: it has no
 // result register, and wait_loads() stands before the barrier that publishes
-// what it wrote.
+// what it wrote.  m0, the LDS address, is a register the compiler sets right
+// before each use of its own.
 __device__ __forceinline__ void load_to_lds(const i32x4& buf, uint32_t offset, uint32_t lds) {
     __asm__ volatile(
         "s_mov_b32 m0, %0\n\t"
