@@ -36,6 +36,11 @@ __device__ __forceinline__ int64_t target_of(const void* targets, int wide, int6
     return row_of(targets, wide, n, vocab);
 }
 
+// What exponentials are taken relative to: the maximum, or 0 where that is
+// infinite.  -inf logits, also where there is no other, then add 0, and a +inf
+// one makes the sum +inf.
+__device__ __forceinline__ float base_of(float top) { return fabsf(top) < INFINITY ? top : 0.0f; }
+
 // Softmax statistics of the tile's rows for each token: maximum and sum of
 // exponentials over the wave's rows, and the target's logit.
 struct StatsEpilogue {
@@ -70,17 +75,18 @@ struct StatsEpilogue {
             }
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float base = base_of(top);
             if (whole) {
 #pragma unroll
                 for (int r = 0; r < kTM; ++r)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f((acc[r][u][i] - top) * kLog2e);
+                    for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f((acc[r][u][i] - base) * kLog2e);
             } else {
 #pragma unroll
                 for (int r = 0; r < kTM; ++r)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (v0 + 16 * r + i < vocab) sum += __builtin_amdgcn_exp2f((acc[r][u][i] - top) * kLog2e);
+                        if (v0 + 16 * r + i < vocab) sum += __builtin_amdgcn_exp2f((acc[r][u][i] - base) * kLog2e);
             }
             sum += __shfl_xor(sum, 16, 64);
             sum += __shfl_xor(sum, 32, 64);
@@ -284,9 +290,10 @@ __global__ __launch_bounds__(kJoinTokens* kJoinSlots) void join_stats_kernel(con
             for (int u = 0; u < 8; ++u) t = fmaxf(t, p[u].x);
             // a slot beyond the vocabulary has maximum -inf and sum 0 (one of
             // NaN logits has sum NaN, which stays)
-            sum = sum == 0.0f ? 0.0f : sum * __builtin_amdgcn_exp2f((top - t) * kLog2e);
+            const float base = base_of(t);
+            sum = sum == 0.0f ? 0.0f : sum * __builtin_amdgcn_exp2f((base_of(top) - base) * kLog2e);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) sum += p[u].y == 0.0f ? 0.0f : p[u].y * __builtin_amdgcn_exp2f((p[u].x - t) * kLog2e);
+            for (int u = 0; u < 8; ++u) sum += p[u].y == 0.0f ? 0.0f : p[u].y * __builtin_amdgcn_exp2f((base_of(p[u].x) - base) * kLog2e);
             top = t;
         }
     tops[y][x] = top;
@@ -298,13 +305,13 @@ __global__ __launch_bounds__(kJoinTokens* kJoinSlots) void join_stats_kernel(con
             const float a = tops[y][x], b = tops[y + half][x], t = fmaxf(a, b);
             const float sa = sums[y][x], sb = sums[y + half][x];
             tops[y][x] = t;
-            sums[y][x] = (sa == 0.0f ? 0.0f : sa * __builtin_amdgcn_exp2f((a - t) * kLog2e)) +
-                         (sb == 0.0f ? 0.0f : sb * __builtin_amdgcn_exp2f((b - t) * kLog2e));
+            sums[y][x] = (sa == 0.0f ? 0.0f : sa * __builtin_amdgcn_exp2f((base_of(a) - base_of(t)) * kLog2e)) +
+                         (sb == 0.0f ? 0.0f : sb * __builtin_amdgcn_exp2f((base_of(b) - base_of(t)) * kLog2e));
         }
         __syncthreads();
     }
     if (y != 0 || token >= n) return;
-    const float l = tops[0][x] + logf(sums[0][x]);
+    const float l = base_of(tops[0][x]) + logf(sums[0][x]);
     lse[token] = l;
     loss[token] = target_of(targets, targets64, token, vocab) < 0 ? 0.0f : l - target_logit[token];
 }

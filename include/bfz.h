@@ -485,7 +485,9 @@ int bfz_embed_grad(const void* ids, int32_t ids64, int64_t n, const void* dout,
  * t = targets[k]:
  *   lse[k]  = log sum_v exp z[k][v]
  *   loss[k] = lse[k] - z[k][t], or 0 when t lies outside [0, vocab)
- * The logits are reduced as they are computed, never stored.
+ * The logits are reduced as they are computed, never stored.  A logit of -Inf
+ * adds nothing (lse is -Inf where there is no other), one of +Inf makes lse
+ * +Inf, a NaN one NaN, of its own token only.
  * hidden: bf16 [n, dim], rows hidden_ld elements apart.  weight: [vocab, dim],
  * BFZ_BF16 (grid NULL) or BFZ_E4M3 codes with their row-major scale grid
  * [ceil(vocab/128), ceil(dim/128)], as the step writes both.  Rows that start
