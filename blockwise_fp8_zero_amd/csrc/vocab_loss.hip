@@ -150,6 +150,13 @@ struct LogitGradEpilogue {
                     for (int i = 0; i < 4; ++i)
                         if (first + m0 + 16 * r + i >= vocab) x[r][i] = 0.0f;
             }
+            // a token without a target, whatever its logits are
+            if (__any(there && t < 0)) {
+#pragma unroll
+                for (int r = 0; r < kTM; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[r][i] = t < 0 ? 0.0f : x[r][i];
+            }
             if (!there) continue;
             bf16_t* row = dz + token * width + m0;
 #pragma unroll
@@ -239,7 +246,7 @@ constexpr int kFewGradRows = 64, kFewGradCols = 4;
 template <class O>
 __global__ __launch_bounds__(256) void few_weight_grad_kernel(const bf16_t* __restrict__ hidden, int64_t hidden_ld, int64_t dim,
                                                               const bf16_t* __restrict__ dz, int64_t width, int64_t n, int64_t rows,
-                                                              WeightGradEpilogue<O> out) {
+                                                              const void* targets, int32_t targets64, WeightGradEpilogue<O> out) {
     __shared__ float d[kFewGradRows][kFewTokens];
     const int64_t v0 = (int64_t)blockIdx.x * kFewGradRows, c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * kFewGradCols;
     const int count = (int)(rows - v0 < kFewGradRows ? rows - v0 : kFewGradRows);
@@ -250,10 +257,12 @@ __global__ __launch_bounds__(256) void few_weight_grad_kernel(const bf16_t* __re
     }
     float h[kFewTokens][kFewGradCols];
 #pragma unroll
-    for (int t = 0; t < kFewTokens; ++t)
+    for (int t = 0; t < kFewTokens; ++t) {
+        const bool counts = t < n && target_of(targets, targets64, t, out.vocab) >= 0;
 #pragma unroll
         for (int l = 0; l < kFewGradCols; ++l)
-            h[t][l] = t < n && c + l < dim ? Elem<bf16_t>::get(hidden[t * hidden_ld + c + l]) : 0.0f;
+            h[t][l] = counts && c + l < dim ? Elem<bf16_t>::get(hidden[t * hidden_ld + c + l]) : 0.0f;
+    }
     __syncthreads();
     if (c >= dim) return;
     for (int r = 0; r < count; ++r) {
@@ -328,12 +337,30 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const T* __restrict__ src
     }
 }
 
-// Largest |dloss| of the tokens that count; 1 where there is none.
-__global__ __launch_bounds__(1024) void upstream_unit_kernel(const float* __restrict__ dloss, const void* targets, int32_t targets64,
-                                                             int64_t vocab, int64_t n, float* unit) {
+// What the gradient starts from.  The first workgroup finds the largest |dloss|
+// of the tokens that count (1 where there is none).  The others copy the hidden
+// rows, where `dst` asks for that, into rows of `width` units with zeros at the
+// end, and zeros for a token without a target: in dW = dz^T h its dz of 0 would
+// not keep a NaN or infinity out.  T: the widest unit that rows start on and
+// are a multiple of.
+constexpr int kPrepareThreads = 1024, kPrepareRows = kPrepareThreads / 64;
+template <class T>
+__global__ __launch_bounds__(kPrepareThreads) void prepare_grad_kernel(const float* __restrict__ dloss, const void* targets,
+                                                                       int32_t targets64, int64_t vocab, int64_t n, float* unit,
+                                                                       const T* __restrict__ src, int64_t ld, int64_t dim,
+                                                                       T* __restrict__ dst, int64_t width) {
+    if (blockIdx.x > 0) {
+        const int lane = threadIdx.x & 63;
+        for (int64_t token = (int64_t)(blockIdx.x - 1) * kPrepareRows + (threadIdx.x >> 6); token < n;
+             token += (int64_t)(gridDim.x - 1) * kPrepareRows) {
+            const bool counts = target_of(targets, targets64, token, vocab) >= 0;
+            for (int64_t c = lane; c < width; c += 64) dst[token * width + c] = counts && c < dim ? src[token * ld + c] : T{};
+        }
+        return;
+    }
     __shared__ float tops[16];
     float top = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += 1024)
+    for (int64_t i = threadIdx.x; i < n; i += kPrepareThreads)
         if (target_of(targets, targets64, i, vocab) >= 0) top = fmaxf(top, fabsf(dloss[i]));
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
@@ -621,23 +648,38 @@ bool loadable(const void* p, int64_t ld, int64_t dim, int size) {
 }
 
 // The operands as the products read them: in place where rows suit 16-byte
-// loads, else padded copies (the weights' by pieces).
+// loads, else padded copies (the weights' by pieces).  dW reads a copy of h
+// always, in which tokens without a target are zero (8192 x 4096: 25 us with the
+// largest dloss, 8 without the copy, of a gradient of 20 ms).
 struct Source {
     Operand hidden;      // rows of tokens
     bool copy_weight;
     int64_t width, esize;
 };
 
-int source_of(const VocabLossArgs& a, const Work& w, Source* s, void* stream) {
-    s->width = up(a.dim, 64);
-    s->esize = a.fp8 ? 1 : 2;
-    s->copy_weight = !loadable(a.weight, a.weight_ld, a.dim, (int)s->esize);
-    if (loadable(a.hidden, a.hidden_ld, a.dim, 2)) {
-        s->hidden = Operand{a.hidden, a.hidden_ld * 2, a.n, a.dim};
-        return hipSuccess;
-    }
-    s->hidden = Operand{w.hidden, s->width * 2, a.n, s->width};
-    return pad_rows(a.hidden, a.hidden_ld * 2, a.n, a.dim * 2, w.hidden, s->width * 2, stream);
+Source source_of(const VocabLossArgs& a, const Work& w, bool copy_hidden) {
+    Source s;
+    s.width = up(a.dim, 64);
+    s.esize = a.fp8 ? 1 : 2;
+    s.copy_weight = !loadable(a.weight, a.weight_ld, a.dim, (int)s.esize);
+    s.hidden = copy_hidden ? Operand{w.hidden, s.width * 2, a.n, s.width} : Operand{a.hidden, a.hidden_ld * 2, a.n, a.dim};
+    return s;
+}
+
+int prepare_grad(const VocabLossArgs& a, const Work& w, int64_t width, bool copy_hidden, void* stream) {
+    const uint64_t marks = reinterpret_cast<uintptr_t>(a.hidden) | (uint64_t)(a.hidden_ld * 2) | (uint64_t)(a.dim * 2);
+    const auto launch = [&](auto unit) {
+        typedef decltype(unit) T;
+        constexpr int kPer = (int)sizeof(T) / 2;
+        const int64_t copies = copy_hidden ? std::min<int64_t>((a.n + kPrepareRows - 1) / kPrepareRows, 4096) : 0;
+        hipLaunchKernelGGL(prepare_grad_kernel<T>, dim3((uint32_t)(1 + copies)), dim3(kPrepareThreads), 0, (hipStream_t)stream,
+                           a.dloss, a.targets, a.targets64, a.vocab, a.n, w.unit, static_cast<const T*>(a.hidden),
+                           a.hidden_ld / kPer, a.dim / kPer, static_cast<T*>(w.hidden), width / kPer);
+        return (int)hipGetLastError();
+    };
+    if (marks % 16 == 0) return launch(u32x4{});
+    if (marks % 4 == 0) return launch(uint32_t{});
+    return launch(uint16_t{});
 }
 
 // Rows [first, first + rows) of the weights, rows in extent and dim in k.
@@ -691,7 +733,7 @@ int weight_grad_launch(const VocabLossArgs& a, const Work& w, const GemmArgs& d,
     if (a.n > kFewTokens) return launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<O>>(d, e, stream);
     const dim3 grid((uint32_t)((rows + kFewGradRows - 1) / kFewGradRows), (uint32_t)((a.dim + 256 * kFewGradCols - 1) / (256 * kFewGradCols)));
     hipLaunchKernelGGL(few_weight_grad_kernel<O>, grid, dim3(256), 0, (hipStream_t)stream, static_cast<const bf16_t*>(a.hidden),
-                       a.hidden_ld, a.dim, w.dz, width, a.n, rows, e);
+                       a.hidden_ld, a.dim, w.dz, width, a.n, rows, a.targets, a.targets64, e);
     return hipGetLastError();
 }
 
@@ -721,8 +763,9 @@ int64_t vocab_loss_work_bytes(int64_t n, int64_t vocab, int64_t dim, int fp8, in
 int launch_vocab_loss(const VocabLossArgs& a, void* work, void* stream) {
     if (a.n == 0) return hipSuccess;
     const Work w = work_of(work, a.n, a.vocab, a.dim, a.fp8, 0);
-    Source s;
-    int err = source_of(a, w, &s, stream);
+    const bool copy_hidden = !loadable(a.hidden, a.hidden_ld, a.dim, 2);
+    const Source s = source_of(a, w, copy_hidden);
+    int err = copy_hidden ? pad_rows(a.hidden, a.hidden_ld * 2, a.n, a.dim * 2, w.hidden, s.width * 2, stream) : hipSuccess;
     if (err) return err;
     const int64_t piece = s.copy_weight ? piece_rows(a.n, a.vocab, a.dim) : a.vocab;
     int64_t slots = 0;
@@ -746,13 +789,10 @@ int launch_vocab_loss(const VocabLossArgs& a, void* work, void* stream) {
 
 int launch_vocab_loss_grad(const VocabLossArgs& a, void* work, void* stream) {
     const Work w = work_of(work, a.n, a.vocab, a.dim, a.fp8, 1);
-    Source s{};
-    int err = hipSuccess;
-    if (a.n > 0) err = source_of(a, w, &s, stream);
-    if (err) return err;
-    hipLaunchKernelGGL(upstream_unit_kernel, dim3(1), dim3(1024), 0, (hipStream_t)stream, a.dloss, a.targets, a.targets64, a.vocab, a.n,
-                       w.unit);
-    err = hipGetLastError();
+    // dW of few tokens reads h itself
+    const bool copy_hidden = a.n > 0 && ((a.dweight && a.n > kFewTokens) || !loadable(a.hidden, a.hidden_ld, a.dim, 2));
+    const Source s = source_of(a, w, copy_hidden);
+    int err = prepare_grad(a, w, s.width, copy_hidden, stream);
     if (err) return err;
     const int64_t piece = piece_rows(a.n, a.vocab, a.dim);
     const HiddenShape shape = hidden_shape(a.n, a.dim, piece);

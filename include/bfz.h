@@ -512,6 +512,8 @@ int bfz_vocab_loss(const void* hidden, int64_t hidden_ld, int64_t n, const void*
  * Its gradient for the upstream gradient dloss[k] of each loss:
  *   dz[k][v] = dloss[k] (exp(z[k][v] - lse[k]) - [v = t]), 0 for a target
  *   outside [0, vocab);  dhidden = dz weight;  dweight = dz^T hidden.
+ * A token whose target lies outside has a zero row of dhidden and adds nothing
+ * to dweight, also where its hidden row, lse or dloss is NaN or infinite.
  * lse: as bfz_vocab_loss wrote it.  dz is rounded to bf16 before the two
  * products, which sum in binary32.  dhidden (bf16 [n, dim]) and dweight
  * (BFZ_BF16 or BFZ_F32 [vocab, dim]) are written whole, each may be NULL;
