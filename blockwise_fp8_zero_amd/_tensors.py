@@ -1,7 +1,7 @@
 """Argument marshalling shared by the operators around the step.  Pointers are
 plain integers here: at the smallest sizes a call costs what its arguments do.
 """
-F32, BF16, F16, E4M3 = 0, 1, 2, 3
+F32, BF16, F16, E4M3, F32_ROUNDED = 0, 1, 2, 3, 4
 
 _torch = _floats = _codes = _raw = _device = None
 

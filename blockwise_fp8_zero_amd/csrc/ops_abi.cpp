@@ -302,9 +302,11 @@ extern "C" int bfz_vocab_loss_grad(const void* hidden, int64_t hidden_ld, int64_
     if (!aligned(lse, 4) || !aligned(dloss, 4)) return fail(BFZ_EALIGN, "%s: lse and dloss must be 4-byte aligned", where);
     if (dhidden) rc = check_matrix(dhidden, kBF16, n, dim, dhidden_ld, "dhidden", where);
     if (rc) return rc;
+    const bool two_parts = dweight && dweight_dtype == kF32;
     if (dweight) {
+        if (dweight_dtype == BFZ_F32_ROUNDED) dweight_dtype = kF32;
         if (dweight_dtype != kBF16 && dweight_dtype != kF32)
-            return fail(BFZ_EINVAL, "%s: dweight must be BFZ_BF16 or BFZ_F32", where);
+            return fail(BFZ_EINVAL, "%s: dweight must be BFZ_BF16, BFZ_F32 or BFZ_F32_ROUNDED", where);
         rc = check_matrix(dweight, dweight_dtype, vocab, dim, dweight_ld, "dweight", where);
         if (rc) return rc;
     }
@@ -326,6 +328,7 @@ extern "C" int bfz_vocab_loss_grad(const void* hidden, int64_t hidden_ld, int64_
     a.dhidden_ld = dhidden_ld;
     a.dweight = dweight;
     a.dweight_type = dweight_dtype;
+    a.dz_parts = two_parts ? 2 : 1;
     a.dweight_ld = dweight_ld;
     a.accumulate = accumulate;
     return launched(where, launch_vocab_loss_grad(a, work, stream));

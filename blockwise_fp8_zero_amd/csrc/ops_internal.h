@@ -93,6 +93,7 @@ struct VocabLossArgs {
     void* dhidden;        // bf16, or null
     void* dweight;        // bf16 or f32, or null
     int32_t dweight_type, accumulate;
+    int32_t dz_parts;     // bf16 parts of dz that dweight is made of: 1 or 2
     int64_t dhidden_ld, dweight_ld;
 };
 int64_t vocab_loss_work_bytes(int64_t n, int64_t vocab, int64_t dim, int fp8, int grad);

@@ -15,6 +15,12 @@
 // dz, rounded to bf16 (the matrix cores' input type: each dz is off by at
 // most 2^-8 of itself, which the sums over v and n average out); then
 // dz W adds onto dh's binary32 sums and dz^T h gives the piece's rows of dW.
+// A float32 dW would show that rounding (1.4e-3 of it at 512 x 4000 x 128 with
+// a dloss of each token's own), so what bf16 left of dz follows as a second
+// bf16 part, 2^-16 off at most, and dW's product runs over the tokens twice:
+// dz's rows, and h's, stand one part below the other.  An f32 dW of 512 x 4000 x
+// 128 is then 2.2e-6 off.  The caller may waive it: loss and gradients of 8192 x
+// 131072 x 4096 E4M3 with an f32 dW take 35.2 ms, with dz rounded once 27.4.
 // dz is rounded in units of the largest dloss, by which the results are
 // multiplied in binary32: where dloss is the same for all tokens, as in a
 // mean, the target's p - 1 then rounds by what p holds, not by an error of
@@ -30,7 +36,7 @@
 namespace bfz {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ int64_t target_of(const void* targets, int wide, int64_t n, int64_t vocab) {
     return row_of(targets, wide, n, vocab);
@@ -104,9 +110,11 @@ struct StatsEpilogue {
     }
 };
 
-// dz of the piece, bf16 [token][width]; zero beyond the vocabulary.
+// dz of the piece, bf16 [token][width]; zero beyond the vocabulary.  rest, where
+// there is one: what the rounding left, in the same layout.
 struct LogitGradEpilogue {
     bf16_t* dz;
+    bf16_t* rest;
     int64_t width, first, vocab, n;
     const float* lse;
     const float* dloss;
@@ -127,8 +135,13 @@ struct LogitGradEpilogue {
             // p = 2^(z log2e - lse log2e), as 2^64 p and a factor, since the
             // instruction gives zero for subnormal results; a token without a
             // target gets p = 0
-            const float shift = t < 0 ? -INFINITY : 64.0f - lse[token] * kLog2e;
-            const float factor = up * 0x1p-64f;
+            const float turned = t < 0 ? INFINITY : lse[token] * kLog2e;
+            const float shift = 64.0f - turned;
+            // the roundings of both, which all the token's p share, go into the
+            // factor: of the product, and of the difference
+            const float back = shift - 64.0f;
+            const float lost = (64.0f - (shift - back)) + (-turned - back) - __builtin_fmaf(t < 0 ? 0.0f : lse[token], kLog2e, -turned);
+            const float factor = up * 0x1p-64f * (fabsf(lost) < 1.0f ? __builtin_fmaf(lost, kLn2, 1.0f) : 1.0f);
             const int64_t at = t - first - m0;
             float x[kTM][4];
 #pragma unroll
@@ -163,6 +176,12 @@ struct LogitGradEpilogue {
             for (int r = 0; r < kTM; ++r) {
                 const u32x2 y = {pack2<bf16_t>(x[r][0], x[r][1]), pack2<bf16_t>(x[r][2], x[r][3])};
                 *reinterpret_cast<u32x2*>(row + 16 * r) = y;
+                if (rest) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[r][i] -= __uint_as_float((i & 1) ? (y[i >> 1] & 0xFFFF0000u) : (y[i >> 1] << 16));
+                    *reinterpret_cast<u32x2*>(rest + token * width + m0 + 16 * r) =
+                        u32x2{pack2<bf16_t>(x[r][0], x[r][1]), pack2<bf16_t>(x[r][2], x[r][3])};
+                }
             }
         }
     }
@@ -245,15 +264,16 @@ struct WeightGradEpilogue {
 constexpr int kFewGradRows = 64, kFewGradCols = 4;
 template <class O>
 __global__ __launch_bounds__(256) void few_weight_grad_kernel(const bf16_t* __restrict__ hidden, int64_t hidden_ld, int64_t dim,
-                                                              const bf16_t* __restrict__ dz, int64_t width, int64_t n, int64_t rows,
-                                                              const void* targets, int32_t targets64, WeightGradEpilogue<O> out) {
+                                                              const bf16_t* __restrict__ dz, const bf16_t* __restrict__ rest, int64_t width,
+                                                              int64_t n, int64_t rows, const void* targets, int32_t targets64, WeightGradEpilogue<O> out) {
     __shared__ float d[kFewGradRows][kFewTokens];
     const int64_t v0 = (int64_t)blockIdx.x * kFewGradRows, c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * kFewGradCols;
     const int count = (int)(rows - v0 < kFewGradRows ? rows - v0 : kFewGradRows);
     const float most = *out.unit;
     for (int i = threadIdx.x; i < kFewGradRows * kFewTokens; i += 256) {
         const int t = i / kFewGradRows, r = i % kFewGradRows;
-        d[r][t] = t < n && r < count ? Elem<bf16_t>::get(dz[t * width + v0 + r]) * most : 0.0f;
+        const int64_t at = t * width + v0 + r;
+        d[r][t] = t < n && r < count ? (Elem<bf16_t>::get(dz[at]) + (rest ? Elem<bf16_t>::get(rest[at]) : 0.0f)) * most : 0.0f;
     }
     float h[kFewTokens][kFewGradCols];
 #pragma unroll
@@ -339,22 +359,25 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const T* __restrict__ src
 
 // What the gradient starts from.  The first workgroup finds the largest |dloss|
 // of the tokens that count (1 where there is none).  The others copy the hidden
-// rows, where `dst` asks for that, into rows of `width` units with zeros at the
-// end, and zeros for a token without a target: in dW = dz^T h its dz of 0 would
-// not keep a NaN or infinity out.  T: the widest unit that rows start on and
-// are a multiple of.
+// rows into rows of `width` units with zeros at the end, and zeros for a token
+// without a target: in dW = dz^T h its dz of 0 would not keep a NaN or infinity
+// out.  They stand there `parts` times, once for each part of dz.  T: the widest
+// unit that rows start on and are a multiple of.
 constexpr int kPrepareThreads = 1024, kPrepareRows = kPrepareThreads / 64;
 template <class T>
 __global__ __launch_bounds__(kPrepareThreads) void prepare_grad_kernel(const float* __restrict__ dloss, const void* targets,
                                                                        int32_t targets64, int64_t vocab, int64_t n, float* unit,
                                                                        const T* __restrict__ src, int64_t ld, int64_t dim,
-                                                                       T* __restrict__ dst, int64_t width) {
+                                                                       T* __restrict__ dst, int64_t width, int32_t parts) {
     if (blockIdx.x > 0) {
         const int lane = threadIdx.x & 63;
         for (int64_t token = (int64_t)(blockIdx.x - 1) * kPrepareRows + (threadIdx.x >> 6); token < n;
              token += (int64_t)(gridDim.x - 1) * kPrepareRows) {
             const bool counts = target_of(targets, targets64, token, vocab) >= 0;
-            for (int64_t c = lane; c < width; c += 64) dst[token * width + c] = counts && c < dim ? src[token * ld + c] : T{};
+            for (int64_t c = lane; c < width; c += 64) {
+                const T x = counts && c < dim ? src[token * ld + c] : T{};
+                for (int32_t k = 0; k < parts; ++k) dst[(k * n + token) * width + c] = x;
+            }
         }
         return;
     }
@@ -486,23 +509,24 @@ HiddenShape hidden_shape(int64_t n, int64_t dim, int64_t piece, double* product 
 // rows, 8.05 in pieces of 32768, the three products 20.6 and 21.2 ms; but 4000 x
 // 100000 x 2048: 4.96 ms in seven pieces, 4.26 in one of 128 MiB or 1 GiB of dz).
 // Chosen by the modelled time; a piece's dz and a padded bf16 copy of its
-// weights take 512 MiB each, or those of 1024 rows.
+// weights take 512 MiB each, or those of 1024 rows
+// (dz in two parts: half the rows).
 constexpr int64_t kPieceBytes = int64_t(1) << 29, kLeastRows = 1024;
-double piece_us(int64_t n, int64_t rows, int64_t dim) {
+double piece_us(int64_t n, int64_t rows, int64_t dim, int parts) {
     double hidden;
     hidden_shape(n, dim, rows, &hidden);
-    const double z = logits_us(n, rows, dim) * (2 * n * rows > (int64_t(128) << 20) ? 1.08 : 1.0);
-    const double weight = product_us(up(dim, kBM) / kBM * (up(rows, 256) / 256), 256, up(n, kBK) / kBK);
+    const double z = logits_us(n, rows, dim) * (2 * parts * n * rows > (int64_t(128) << 20) ? 1.08 : 1.0);
+    const double weight = product_us(up(dim, kBM) / kBM * (up(rows, 256) / 256), 256, up(parts * n, kBK) / kBK);
     return z + hidden + weight + 15.0;
 }
-int64_t piece_rows(int64_t n, int64_t vocab, int64_t dim) {
+int64_t piece_rows(int64_t n, int64_t vocab, int64_t dim, int parts) {
     int64_t best = 0;
     double least = 0.0;
     for (int64_t most = kPieceBytes / 4; most <= kPieceBytes; most *= 2) {
-        const int64_t by_dz = most / (2 * std::max<int64_t>(n, 1)), by_copy = kPieceBytes / (2 * up(dim, 64));
-        const int64_t rows = std::min(std::max(kLeastRows, std::min(by_dz, by_copy) / 256 * 256), up(vocab, 256));
+        const int64_t by_dz = most / (2 * parts * std::max<int64_t>(n, 1)), by_copy = kPieceBytes / (2 * up(dim, 64));
+        const int64_t rows = std::min(std::max(kLeastRows / parts, std::min(by_dz, by_copy) / 256 * 256), up(vocab, 256));
         const int64_t full = vocab / rows, rest = vocab - full * rows;
-        const double us = double(full) * piece_us(n, rows, dim) + (rest ? piece_us(n, rest, dim) : 0.0) +
+        const double us = double(full) * piece_us(n, rows, dim, parts) + (rest ? piece_us(n, rest, dim, parts) : 0.0) +
                           3e-7 * double(full + (rest > 0) - 1) * double(n) * double(dim);
         if (!best || us < least) best = rows, least = us;
         if (rows >= vocab) break;
@@ -539,7 +563,7 @@ Work work_of(void* work, int64_t n, int64_t vocab, int64_t dim, int fp8, int gra
         return q;
     };
     const int64_t width = up(dim, 64), rows = up(vocab, 256), esize = fp8 ? 1 : 2;
-    w.hidden = take(n * width * 2);
+    w.hidden = take(n * width * 2 * (grad ? 2 : 1));
     w.weight = take(std::min(std::max(kPieceBytes / 2, kLeastRows * width), rows * width) * esize);
     const int64_t mark = at;
     // the loss and its gradient run one after the other: one space for both
@@ -549,7 +573,7 @@ Work work_of(void* work, int64_t n, int64_t vocab, int64_t dim, int fp8, int gra
     if (grad) {
         at = mark;
         w.unit = reinterpret_cast<float*>(take(4));
-        w.dz = reinterpret_cast<bf16_t*>(take(std::min(std::max(kPieceBytes, n * kLeastRows * 2), n * rows * 2)));
+        w.dz = reinterpret_cast<bf16_t*>(take(std::min(std::max(kPieceBytes, n * kLeastRows * 2), n * rows * 4)));
         w.sums = reinterpret_cast<float*>(take(std::min(64 * n, std::max(kSplitTokens, n)) * width * 4));
         w.bytes = std::max(w.bytes, at);
     }
@@ -674,7 +698,7 @@ int prepare_grad(const VocabLossArgs& a, const Work& w, int64_t width, bool copy
         const int64_t copies = copy_hidden ? std::min<int64_t>((a.n + kPrepareRows - 1) / kPrepareRows, 4096) : 0;
         hipLaunchKernelGGL(prepare_grad_kernel<T>, dim3((uint32_t)(1 + copies)), dim3(kPrepareThreads), 0, (hipStream_t)stream,
                            a.dloss, a.targets, a.targets64, a.vocab, a.n, w.unit, static_cast<const T*>(a.hidden),
-                           a.hidden_ld / kPer, a.dim / kPer, static_cast<T*>(w.hidden), width / kPer);
+                           a.hidden_ld / kPer, a.dim / kPer, static_cast<T*>(w.hidden), width / kPer, a.dz_parts);
         return (int)hipGetLastError();
     };
     if (marks % 16 == 0) return launch(u32x4{});
@@ -733,7 +757,7 @@ int weight_grad_launch(const VocabLossArgs& a, const Work& w, const GemmArgs& d,
     if (a.n > kFewTokens) return launch_gemm<BF16KR<kBM, 8>, BF16KR<256, 4>, 256, 2, WeightGradEpilogue<O>>(d, e, stream);
     const dim3 grid((uint32_t)((rows + kFewGradRows - 1) / kFewGradRows), (uint32_t)((a.dim + 256 * kFewGradCols - 1) / (256 * kFewGradCols)));
     hipLaunchKernelGGL(few_weight_grad_kernel<O>, grid, dim3(256), 0, (hipStream_t)stream, static_cast<const bf16_t*>(a.hidden),
-                       a.hidden_ld, a.dim, w.dz, width, a.n, rows, a.targets, a.targets64, e);
+                       a.hidden_ld, a.dim, w.dz, a.dz_parts > 1 ? w.dz + a.n * width : nullptr, width, a.n, rows, a.targets, a.targets64, e);
     return hipGetLastError();
 }
 
@@ -741,9 +765,9 @@ int weight_grad_launch(const VocabLossArgs& a, const Work& w, const GemmArgs& d,
 // vocabulary rows.
 int weight_grad(const VocabLossArgs& a, const Work& w, const Source& s, int64_t first, int64_t rows, int64_t width, void* stream) {
     GemmArgs d{};
-    d.a = Operand{s.hidden.p, s.hidden.ld, a.n > 0 ? s.hidden.k : a.dim, a.n};
-    d.b = Operand{w.dz, width * 2, rows, a.n};
-    d.k = a.n;
+    d.k = a.dz_parts * a.n;
+    d.a = Operand{s.hidden.p, s.hidden.ld, s.hidden.k, d.k};
+    d.b = Operand{w.dz, width * 2, rows, d.k};
     const bool f32 = a.dweight_type == kF32;
     const int32_t vec = a.dweight_ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % (f32 ? 16 : 8) == 0;
     if (f32) {
@@ -767,7 +791,7 @@ int launch_vocab_loss(const VocabLossArgs& a, void* work, void* stream) {
     const Source s = source_of(a, w, copy_hidden);
     int err = copy_hidden ? pad_rows(a.hidden, a.hidden_ld * 2, a.n, a.dim * 2, w.hidden, s.width * 2, stream) : hipSuccess;
     if (err) return err;
-    const int64_t piece = s.copy_weight ? piece_rows(a.n, a.vocab, a.dim) : a.vocab;
+    const int64_t piece = s.copy_weight ? piece_rows(a.n, a.vocab, a.dim, 1) : a.vocab;
     int64_t slots = 0;
     for (int64_t first = 0; first < a.vocab; first += piece) {
         const int64_t rows = std::min(piece, a.vocab - first);
@@ -794,7 +818,7 @@ int launch_vocab_loss_grad(const VocabLossArgs& a, void* work, void* stream) {
     const Source s = source_of(a, w, copy_hidden);
     int err = prepare_grad(a, w, s.width, copy_hidden, stream);
     if (err) return err;
-    const int64_t piece = piece_rows(a.n, a.vocab, a.dim);
+    const int64_t piece = piece_rows(a.n, a.vocab, a.dim, a.dz_parts);
     const HiddenShape shape = hidden_shape(a.n, a.dim, piece);
     for (int64_t first = 0; first < a.vocab; first += piece) {
         const int64_t rows = std::min(piece, a.vocab - first);
@@ -804,7 +828,7 @@ int launch_vocab_loss_grad(const VocabLossArgs& a, void* work, void* stream) {
             err = weight_piece(a, w, s, first, rows, &weight, stream);
             if (err) return err;
             err = logits(a, s, weight, first, rows, [&](int64_t at, int64_t, int) {
-                return LogitGradEpilogue{w.dz + at, width, first + at, a.vocab, a.n, a.lse, a.dloss, w.unit, a.targets, a.targets64};
+                return LogitGradEpilogue{w.dz + at, a.dz_parts > 1 ? w.dz + a.n * width + at : nullptr, width, first + at, a.vocab, a.n, a.lse, a.dloss, w.unit, a.targets, a.targets64};
             }, stream);
             if (err) return err;
         }

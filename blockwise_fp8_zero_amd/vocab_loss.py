@@ -4,7 +4,7 @@ head's weight may be the row-major FP8 weight and scale grid that the step
 writes.
 """
 from . import _check, lib
-from ._tensors import BF16, E4M3, F32, id_vector, matrix, raw_stream, tile_grid, vector, work_pointer
+from ._tensors import BF16, E4M3, F32, F32_ROUNDED, id_vector, matrix, raw_stream, tile_grid, vector, work_pointer
 
 
 def vocab_loss_workspace(n, vocab, dim, weight_dtype=None, grad=True, device="cuda"):
@@ -42,10 +42,12 @@ def vocab_loss(hidden, weight, targets, loss, lse, work, grid=None, stream=None)
 
 
 def vocab_loss_grad(hidden, weight, targets, lse, dloss, dhidden, dweight, work, grid=None, accumulate=False,
-                    stream=None):
+                    stream=None, rounded=False):
     """Gradient of sum(dloss * loss): dhidden (n, dim) bfloat16 and dweight
     (vocab, dim) bfloat16 or float32, each may be None.  lse: as vocab_loss
-    wrote it; dloss: float32 (n).  accumulate adds to dweight."""
+    wrote it; dloss: float32 (n).  accumulate adds to dweight.  A float32 dweight
+    is made of the logits' gradients in two bfloat16 parts (2^-16 off at most);
+    rounded=True rounds them to bfloat16 once (2^-8), in less time."""
     args, n, vocab, dim, wcode = _operands(hidden, weight, targets, grid)
     dh = dw = (None, 0, 0, 0, 0)
     if dhidden is not None:
@@ -56,6 +58,11 @@ def vocab_loss_grad(hidden, weight, targets, lse, dloss, dhidden, dweight, work,
         dw = matrix(dweight, "dweight")
         if dw[1] not in (BF16, F32) or dw[2:4] != (vocab, dim):
             raise ValueError(f"dweight: need bfloat16 or float32 {(vocab, dim)}")
+    dtype = dw[1]
+    if rounded:
+        if dweight is None or dtype != F32:
+            raise ValueError("rounded: only of a float32 dweight")
+        dtype = F32_ROUNDED
     _check(lib().bfz_vocab_loss_grad(*args, vector(lse, "lse", n), vector(dloss, "dloss", n),
-                                     dh[0], dh[4], dw[0], dw[1], dw[4], int(bool(accumulate)),
+                                     dh[0], dh[4], dw[0], dtype, dw[4], int(bool(accumulate)),
                                      _work(work, n, vocab, dim, wcode, 1), raw_stream(stream)))

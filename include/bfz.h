@@ -392,6 +392,7 @@ int bfz_fold_adamw_fp8_step_unpack_t_clip(const bfz_plan* plan, const float* con
 #define BFZ_BF16 1
 #define BFZ_F16 2
 #define BFZ_E4M3 3 /* codes, with a grid of one float scale per 128x128 tile */
+#define BFZ_F32_ROUNDED 4 /* bfz_vocab_loss_grad's dweight only, see there */
 
 /* n elements back to back at any element alignment. */
 typedef struct {
@@ -514,9 +515,12 @@ int bfz_vocab_loss(const void* hidden, int64_t hidden_ld, int64_t n, const void*
  *   outside [0, vocab);  dhidden = dz weight;  dweight = dz^T hidden.
  * A token whose target lies outside has a zero row of dhidden and adds nothing
  * to dweight, also where its hidden row, lse or dloss is NaN or infinite.
- * lse: as bfz_vocab_loss wrote it.  dz is rounded to bf16 before the two
- * products, which sum in binary32.  dhidden (bf16 [n, dim]) and dweight
- * (BFZ_BF16 or BFZ_F32 [vocab, dim]) are written whole, each may be NULL;
+ * lse: as bfz_vocab_loss wrote it.  dz is rounded to bf16 (2^-8 of each at
+ * most) before the two products, which sum in binary32, but for a BFZ_F32
+ * dweight, whose product takes dz in two bf16 parts (2^-16).  BFZ_F32_ROUNDED is
+ * a float dweight made of dz rounded once, in less time.  dhidden (bf16
+ * [n, dim]) and dweight ([vocab, dim], BFZ_BF16, BFZ_F32 or BFZ_F32_ROUNDED)
+ * are written whole, each may be NULL;
  * accumulate != 0 adds to dweight instead.  Every sum has a fixed order:
  * two runs give the same bits.  Other arguments, limits and errors as above.
  */
