@@ -195,7 +195,18 @@ constexpr int kStepLdsBytes = 96 * 1024;                 // > half of the 160 Ki
 // padding slot) reads `spare` instead -- a 16-byte block of the same tile
 // that the wave reads anyway -- and finish() discards it: lane-divergent
 // branches around those loads would make the compiler wait for every
-// outstanding read where they join.
+// outstanding read where they join.  finish() also multiplies by the clipping
+// factor (kClip), before it puts zeros outside the weight's edge: the factor,
+// even a NaN, does not reach them.
+
+template <bool kClip>
+__device__ __forceinline__ f32x4 clipped(f32x4 x, float factor) {
+    if constexpr (kClip) {
+#pragma unroll
+        for (int l = 0; l < 4; ++l) x[l] *= factor;
+    }
+    return x;
+}
 
 // Gradient of a tile already folded into the tile-major shard.
 struct TileMajorGrad {
@@ -204,7 +215,10 @@ struct TileMajorGrad {
     __device__ __forceinline__ Raw load(int k, const f32x4*) const {
         return tile.load(k * kStepThreads + threadIdx.x);
     }
-    __device__ __forceinline__ f32x4 finish(int, const Raw& r) const { return r; }
+    template <bool kClip>
+    __device__ __forceinline__ f32x4 finish(int, const Raw& r, float factor) const {
+        return clipped<kClip>(r, factor);
+    }
 };
 
 // Gradient read straight from the weight's row-major tensor (the fold done
@@ -234,9 +248,10 @@ struct RowMajorGrad {
         const f32x4* q = reinterpret_cast<const f32x4*>(origin + (int64_t)r * ld + c);
         return load_stream(lane_ok(k, c) ? q : spare);
     }
-    __device__ __forceinline__ f32x4 finish(int k, const Raw& x) const {
+    template <bool kClip = false>
+    __device__ __forceinline__ f32x4 finish(int k, const Raw& x, float factor = 1.0f) const {
         const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-        return lane_ok(k, 4 * (threadIdx.x & 31)) ? x : zero;
+        return lane_ok(k, 4 * (threadIdx.x & 31)) ? clipped<kClip>(x, factor) : zero;
     }
 };
 
@@ -271,7 +286,8 @@ struct ShiftedRowMajorGrad {
         return x;
     }
     // Both rows of a wave run the shuffle unconditionally (32-lane segments).
-    __device__ __forceinline__ f32x4 finish(int k, const Raw& x) const {
+    template <bool kClip = false>
+    __device__ __forceinline__ f32x4 finish(int k, const Raw& x, float factor = 1.0f) const {
         const int r = k * 32 + (threadIdx.x >> 5), c = 4 * (threadIdx.x & 31);
         const bool row_ok = r < rows;
         const float* row = origin + (int64_t)(row_ok ? r : 0) * ld;
@@ -291,6 +307,7 @@ struct ShiftedRowMajorGrad {
         y[1] = a == 0 ? f[1] : a == 1 ? f[2] : a == 2 ? f[3] : n[0];
         y[2] = a == 0 ? f[2] : a == 1 ? f[3] : a == 2 ? n[0] : n[1];
         y[3] = a == 0 ? f[3] : a == 1 ? n[0] : a == 2 ? n[1] : n[2];
+        y = clipped<kClip>(y, factor);
 #pragma unroll
         for (int l = 0; l < 4; ++l)
             if (!row_ok || c + l >= cols) y[l] = 0.0f;
@@ -343,8 +360,8 @@ struct RowMajorCodes {
 };
 
 // kClip: the gradient is multiplied by *s.grad_scale (one binary32 product,
-// as a separate pass over it would) before the update sees it.  A template
-// flag, so that the steps without it are compiled as before.
+// as a separate pass over the weights' gradients would) before the update sees
+// it.  A template flag, so that the steps without it are compiled as before.
 template <bool kClip, class GradFn, class Out = RowMajorCodes>
 __device__ __forceinline__ float step_tile(int64_t tile, float* __restrict__ master,
                                            float* __restrict__ mom1, float* __restrict__ mom2,
@@ -371,15 +388,10 @@ __device__ __forceinline__ float step_tile(int64_t tile, float* __restrict__ mas
         m[k] = bM.load(i);
         v[k] = bV.load(i);
     }
+    float factor = 1.0f;
+    if constexpr (kClip) factor = *s.grad_scale;
 #pragma unroll
-    for (int k = 0; k < kStepVec; ++k) g[k] = grad_at.finish(k, graw[k]);
-    if constexpr (kClip) {
-        const float c = *s.grad_scale;
-#pragma unroll
-        for (int k = 0; k < kStepVec; ++k)
-#pragma unroll
-            for (int l = 0; l < 4; ++l) g[k][l] *= c;
-    }
+    for (int k = 0; k < kStepVec; ++k) g[k] = grad_at.template finish<kClip>(k, graw[k], factor);
     float amax = 0.0f;
 #pragma unroll
     for (int k = 0; k < kStepVec; ++k) {
