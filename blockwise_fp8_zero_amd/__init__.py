@@ -107,7 +107,7 @@ def _check(rc):
 
 
 def _stream(stream):
-    return C.c_void_p(raw_stream(stream))
+    return C.c_void_p(raw_stream(None) if stream is None else stream.cuda_stream)
 
 
 def _dev(t, dtype, name, numel=None):
@@ -143,6 +143,9 @@ def _scalar(t, name, dtype=None):
     """Pointer of a one-element device tensor (float32 unless dtype says)."""
     import torch
     p = _dev(t, dtype or torch.float32, name, 1)
+    home = home_device()
+    if t.get_device() != home:
+        elsewhere(t, name, home)
     if t.numel() != 1:
         raise ValueError(f"{name}: needs one element, has {t.numel()}")
     return p
@@ -446,7 +449,7 @@ def e4m3_encode(x, out, stream=None):
                                  _stream(stream)))
 
 
-from ._tensors import raw_stream  # noqa: E402
+from ._tensors import elsewhere, home_device, raw_stream  # noqa: E402
 from .norm import clip_coef, clip_grads, grad_norm, norm_workspace, shard_grad_norm  # noqa: E402
 from .embedding import embed, embed_grad, embed_grad_workspace  # noqa: E402
 from .vocab_loss import vocab_loss, vocab_loss_grad, vocab_loss_workspace  # noqa: E402

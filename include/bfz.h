@@ -383,7 +383,8 @@ int bfz_fold_adamw_fp8_step_unpack_t_clip(const bfz_plan* plan, const float* con
                                           void* stream);
 
 /* ---- operators around the step ------------------------------------------
- * Conventions as above: device pointers are the caller's, calls enqueue
+ * Conventions as above: device pointers are the caller's, of the current device
+ * as is the stream (the Python binding refuses others), calls enqueue
  * kernels on `stream` and neither allocate nor synchronize.  Strides count
  * elements; inner strides are 1. */
 
