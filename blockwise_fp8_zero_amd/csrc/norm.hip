@@ -111,8 +111,10 @@ __device__ __forceinline__ void write_coef(double sumsq, double max_norm, float*
 // launches' sum and, in the last launch, writes the results.  The partials
 // cross XCDs, whose L2s are separate: they are written, counted and read with
 // agent-scope atomics, which act beyond the L2s, and the wait puts a
-// workgroup's partial there before it is counted.  (An acquire-release ticket
-// writes back and invalidates caches once per workgroup.)
+// workgroup's partial there before it is counted.  That is this hardware's
+// promise, of device-scope stores and vmcnt, not the language's, whose release
+// would also write the XCD's L2 back once per workgroup: 215 us instead of 152
+// for the 40 ragged tensors and their clipping.
 __device__ __forceinline__ void finish_sum(double acc, const NormOut& out, void* work) {
     __shared__ double lds[kThreads / 64];
     __shared__ uint32_t arrived;

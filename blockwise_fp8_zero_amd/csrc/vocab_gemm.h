@@ -105,8 +105,9 @@ __device__ __forceinline__ i32x4 buffer_of(const char* base) {
 // 16 bytes a lane from memory to LDS at lds + 16 * lane.  In assembly, so
 // that the compiler does not wait for it at the next LDS read: it has no
 // result register, and wait_loads() stands before the barrier that publishes
-// what it wrote.  m0, the LDS address, is a register the compiler sets right
-// before each use of its own.
+// what it wrote.  m0, the LDS address, is a reserved register that the compiler
+// sets right before each use of its own (named as clobbered it draws a warning
+// and leaves the code as it is).
 __device__ __forceinline__ void load_to_lds(const i32x4& buf, uint32_t offset, uint32_t lds) {
     __asm__ volatile(
         "s_mov_b32 m0, %0\n\t"
@@ -464,7 +465,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
 }
 
 // ---- few tokens -------------------------------------------------------------------
-// The same product for up to 16 tokens a workgroup, bound by reading A once.
+// The same product for up to 16 tokens in all, bound by reading A once.
 // Nothing is staged: four waves of a workgroup take 32 rows of A and share out
 // its k in blocks of 128; a lane loads 32 k of one row of A and of one token
 // straight into registers, the four lanes of a row 64 bytes side by side, two
@@ -482,16 +483,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_tokens_kernel(GemmArgs g, 
     __shared__ f32x4 part[kFewWaves][2][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, r = lane & 15;
-    const int tm = blockIdx.x % g.tiles_m, tn = blockIdx.x / g.tiles_m;
-    const int64_t m0 = (int64_t)tm * kFewRows, n0 = (int64_t)tn * kFewTokens;
+    const int64_t m0 = (int64_t)blockIdx.x * kFewRows;
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(static_cast<const char*>(g.a.p) + m0 * g.a.ld), (short)0, (int)kBufferBytes, 0x00020000);
     const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(static_cast<const char*>(g.b.p) + n0 * g.b.ld), (short)0, (int)kBufferBytes, 0x00020000);
+        const_cast<char*>(static_cast<const char*>(g.b.p)), (short)0, (int)kBufferBytes, 0x00020000);
     uint32_t row_a[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) row_a[t] = m0 + 16 * t + r < g.a.extent ? (uint32_t)((16 * t + r) * g.a.ld) : kNowhere;
-    const uint32_t row_b = n0 + r < g.b.extent ? (uint32_t)(r * g.b.ld) : kNowhere;
+    const uint32_t row_b = r < g.b.extent ? (uint32_t)(r * g.b.ld) : kNowhere;
     const float* scales = kFp8 ? g.grid + m0 / kTileDim * g.grid_m : nullptr;
     const int blocks = (int)((g.k + 127) / 128);
 
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_tokens_kernel(GemmArgs g, 
 #pragma unroll
         for (int w = 1; w < kFewWaves; ++w) sums[t][0] += part[w][t][lane];
     }
-    const WaveTile w{m0, n0, tm, 0, 0, lane};
+    const WaveTile w{m0, 0, (int)blockIdx.x, 0, 0, lane};
     epilogue.template run<2, 1>(sums, w);
 }
 

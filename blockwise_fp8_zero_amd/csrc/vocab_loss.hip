@@ -5,10 +5,10 @@
 //   dz[n][v] = dloss[n] (exp(z[n][v] - lse[n]) - [v = t[n]])
 //   dh = dz W,  dW = dz^T h
 //
-// Forward: one product whose epilogue reduces every 256 logits of a token to
-// their maximum and sum of exponentials; a small kernel joins those.  The
-// work is 2 N V d operations, bound by the matrix cores once N is a few
-// hundred, by reading W below that.
+// Forward: one product whose epilogue reduces a wave's 64 (32 in narrow tiles)
+// logits of a token to their maximum and sum of exponentials; a small kernel
+// joins those.  The work is 2 N V d operations, bound by the matrix cores once
+// N is a few hundred, by reading W below that.
 //
 // Gradient: 6 N V d operations in three products over pieces of the
 // vocabulary.  A piece's logits are computed again and leave the product as
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(256) void few_weight_grad_kernel(const bf16_t* __re
 }
 
 // lse and loss of a token from its partial statistics: 16 tokens a
-// workgroup, 16 slots at a time.
+// workgroup, 64 threads to a token, 8 slots a thread at a time.
 constexpr int kJoinTokens = 16, kJoinSlots = 64;
 __global__ __launch_bounds__(kJoinTokens* kJoinSlots) void join_stats_kernel(const float2* __restrict__ partial, int64_t slots,
                                                                             const float* __restrict__ target_logit,
@@ -625,10 +625,9 @@ int launch_kr(const GemmArgs& g, const Epilogue& e, void* stream) {
 }
 
 template <bool kFp8, class Epilogue>
-int launch_few(GemmArgs g, const Epilogue& e, void* stream) {
-    g.tiles_m = (int32_t)(up(g.a.extent, kFewRows) / kFewRows);
-    g.tiles_n = 1;
-    hipLaunchKernelGGL((few_tokens_kernel<kFp8, Epilogue>), dim3((uint32_t)g.tiles_m), dim3(64 * kFewWaves), 0, (hipStream_t)stream, g, e);
+int launch_few(const GemmArgs& g, const Epilogue& e, void* stream) {
+    const uint32_t blocks = (uint32_t)(up(g.a.extent, kFewRows) / kFewRows);
+    hipLaunchKernelGGL((few_tokens_kernel<kFp8, Epilogue>), dim3(blocks), dim3(64 * kFewWaves), 0, (hipStream_t)stream, g, e);
     return hipGetLastError();
 }
 
