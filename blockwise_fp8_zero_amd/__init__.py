@@ -94,6 +94,7 @@ def lib():
         L.bfz_vocab_loss.argtypes = [P, i64, i64, P, i32, i64, P, i64, i64, P, i32, P, P, P, P]
         L.bfz_vocab_loss_grad.argtypes = [P, i64, i64, P, i32, i64, P, i64, i64, P, i32, P, P, P, i64, P, i32, i64, i32,
                                           P, P]
+        L.bfz_vocab_loss_shape.argtypes = [i64, i64, i64, i32, P]
         L.bfz_last_error.argtypes = []
         L.bfz_last_error.restype = C.c_char_p
         _lib = L

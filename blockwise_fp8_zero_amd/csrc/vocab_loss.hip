@@ -857,3 +857,16 @@ int launch_vocab_loss_grad(const VocabLossArgs& a, void* work, void* stream) {
 }
 
 }  // namespace bfz
+
+extern "C" int bfz_vocab_loss_shape(int64_t n, int64_t vocab, int64_t dim, int32_t dweight_dtype, int64_t* shape) {
+    using namespace bfz;
+    if (!shape || n < 1 || vocab < 1 || dim < 1 || n > (int64_t(1) << 24) || vocab > (int64_t(1) << 27) || dim > (int64_t(1) << 20))
+        return fail(BFZ_EINVAL, "bfz_vocab_loss_shape: null pointer or bad sizes");
+    const Rows loss = logits_rows(n, vocab, dim);
+    const int64_t piece = piece_rows(n, vocab, dim, dweight_dtype == kF32 ? 2 : 1);
+    const Rows grad = logits_rows(n, std::min(piece, vocab), dim);
+    const HiddenShape hidden = hidden_shape(n, dim, piece);
+    const int64_t out[7] = {loss.full, loss.bn, piece, grad.full, grad.bn, hidden.bn, hidden.splits};
+    std::copy(out, out + 7, shape);
+    return BFZ_OK;
+}

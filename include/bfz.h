@@ -532,6 +532,18 @@ int bfz_vocab_loss_grad(const void* hidden, int64_t hidden_ld, int64_t n, const 
                         int32_t dweight_dtype, int64_t dweight_ld, int32_t accumulate, void* work,
                         void* stream);
 
+/*
+ * How the two calls above cut products of these sizes into tiles of 256
+ * vocabulary rows (dhidden: columns) by 256, 128 or 64 tokens, 16 meaning a read
+ * without tiles; for tests and timing.  shape: 7 numbers,
+ *   the loss:      rows that go into 256-wide tiles first, width of the others;
+ *   the gradient:  rows of a piece, of a whole piece the same two,
+ *                  width of dhidden's tiles, splits of its sum.
+ * Host only.  Errors: BFZ_EINVAL.
+ */
+int bfz_vocab_loss_shape(int64_t n, int64_t vocab, int64_t dim, int32_t dweight_dtype,
+                         int64_t* shape);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char* bfz_last_error(void);
 

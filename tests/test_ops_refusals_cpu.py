@@ -82,3 +82,18 @@ def test_factor_and_stream_of_another_device(monkeypatch):
 
     with pytest.raises(ValueError, match="stream"):
         bfz.raw_stream(Stream())
+
+
+def test_vocab_loss_shape():
+    import ctypes as C
+    f, out = bfz.lib().bfz_vocab_loss_shape, (C.c_int64 * 7)()
+    assert f(100, 1000, 64, 1, None) == EINVAL and f(0, 1000, 64, 1, out) == EINVAL and f(100, 1 << 28, 64, 1, out) == EINVAL
+    for n, V, d in ((1, 300, 64), (16, 5000, 200), (17, 600, 136), (1013, 50001, 1000), (8192, 131072, 4096), (100000, 131072, 512)):
+        for dw in (0, 1, 4):
+            assert f(n, V, d, dw, out) == 0
+            full, width, piece, grad_full, grad_width, hidden, splits = out
+            assert 0 <= full < V and full % 256 == 0 and 0 <= grad_full < V and grad_full % 256 == 0 and piece % 256 == 0
+            assert {width, grad_width} <= ({16} if n <= 16 else {256, 128, 64}) and hidden in (256, 128, 64)
+            assert 1 <= splits <= 64 and splits * n <= max(16384, n)
+            # a piece's dz stays within what the workspace has for it
+            assert n * piece * (4 if dw == 0 else 2) <= max(1 << 29, n * 2048)
