@@ -109,10 +109,15 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(EmbedArgs a, int32_t pi
             for (int l = 0; l < kVec; ++l) x[l] = 0.0f;
             if (row >= 0) {
                 Piece<T, kVec>::load(table + row * a.table_ld + c, x);
-                float s = a.scale;
-                if constexpr (sizeof(T) == 1) s *= a.grid[(row / kTileDim) * wb + c / kTileDim];
+                // the value first: a code of 0 stays 0 where the two scales'
+                // product would overflow
+                if constexpr (sizeof(T) == 1) {
+                    const float g = a.grid[(row / kTileDim) * wb + c / kTileDim];
 #pragma unroll
-                for (int l = 0; l < kVec; ++l) x[l] *= s;
+                    for (int l = 0; l < kVec; ++l) x[l] *= g;
+                }
+#pragma unroll
+                for (int l = 0; l < kVec; ++l) x[l] *= a.scale;
             }
             store_piece<O, kVec>(dst + c, x);
         }

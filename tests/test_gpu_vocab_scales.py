@@ -75,3 +75,14 @@ def test_a_nan_scale_is_seen(n, at):
     grid[1, at] = float("nan")
     loss, lse = _run(h, codes, grid, t)
     assert bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("n", [16, 17, 300])
+@pytest.mark.parametrize("share", [0.5, 1.0])
+def test_zero_scales(n, share):
+    """A grid that nothing has been written to yet."""
+    V, d = 700, 900
+    h, codes, t = _case(n, V, d, n + 4)
+    grid = torch.full((-(-V // 128), -(-d // 128)), 0.001, device="cuda")
+    grid[torch.rand(grid.shape, device="cuda") < share] = 0.0
+    _both(h, codes, grid, t)
