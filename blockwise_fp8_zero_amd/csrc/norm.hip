@@ -12,7 +12,7 @@
 // Bound by reading the gradients, at few of them by the launch: 40 ragged
 // tensors of 70.5M elements, half of them bf16, 46 us (4.6 TB/s), clipped into
 // f32 buffers in another 104 us (4.7 TB/s); the tiles of a 202M-element shard
-// 129 us (6.3 TB/s); one 256 x 384 tensor 5.7 us of a 7 us call.
+// 131 us (6.2 TB/s); one 256 x 384 tensor 5.2 us of a 7 us call.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -231,7 +231,8 @@ __global__ void clip_coef_kernel(const double* sumsq, double max_norm, float* no
 }
 
 // out = in * coef over elements [e0, e1): 8 elements per thread and step
-// where both ends are 16-byte aligned, one otherwise.
+// where both ends are 16-byte aligned, one otherwise (64M elements, f32 99 and
+// 118 us, bf16 into f32 85 and 124).
 template <class I, class O>
 __device__ __forceinline__ void clip_range(const I* in, O* out, int64_t e0, int64_t e1, float coef) {
     const bool vec = ((reinterpret_cast<uintptr_t>(in + e0) | reinterpret_cast<uintptr_t>(out + e0)) & 15u) == 0;

@@ -22,7 +22,7 @@
 //
 // 8192 x 32768 x 4096 runs at 1.13 to 1.39 PFLOP/s (epilogues included; boxes
 // differ by 8%), the library's product of two bf16 matrices at 1.31 to 1.49
-// there.  The matrix cores are busy 66 to 71% of the cycles with bf16 and 55 to
+// there.  The matrix cores are busy 65 to 71% of the cycles with bf16 and 54 to
 // 58% with E4M3, at a clock that their load lowers to 1.9 GHz; LDS 17 to 27%.
 // What is left is the barrier, where all eight waves meet, and with E4M3 the
 // conversions and rescaling (2 vector instructions for each matrix one; 0.7
@@ -472,7 +472,9 @@ __global__ __launch_bounds__(kGemmThreads, 2) void gemm_kernel(GemmArgs g, Epilo
 // blocks ahead.  Which k a matrix instruction takes is free as long as A and B
 // agree.  The waves' sums meet in LDS.  Here a block's sums fit beside the
 // total, so tile scales are applied block by block.  One token on 32768 x 4096
-// codes: 33 us, 4.1 TB/s (64-wide tiles through LDS: 57 us).
+// codes: 30 us, 4.5 TB/s (64-wide tiles through LDS: 57 us).  17 tokens and more
+// do go through 64-wide tiles, which on a head of under 65536 rows leave CUs
+// idle: 17 to 64 tokens 62 to 64 us there, on 131072 rows 143 to 148.
 constexpr int kFewRows = 32, kFewTokens = 16, kFewWaves = 4;
 
 template <bool kFp8, class Epilogue>
