@@ -95,6 +95,17 @@ def lib():
         L.bfz_vocab_loss_grad.argtypes = [P, i64, i64, P, i32, i64, P, i64, i64, P, i32, P, P, P, i64, P, i32, i64, i32,
                                           P, P]
         L.bfz_vocab_loss_shape.argtypes = [i64, i64, i64, i32, P]
+        L.bfz_quantize.argtypes = [P, i32, i64, i64, i64, i32, i32, P, i64, P, i64, P]
+        L.bfz_linear_work_bytes.argtypes = [i64, i64, i64, i32, i32]
+        L.bfz_linear_work_bytes.restype = i64
+        L.bfz_linear.argtypes = [P, i32, i64, P, i64, i32, i64, P, i64, P, i64, i64, P, i32, i64, P, P]
+        L.bfz_linear_grad_input.argtypes = [P, i64, P, i64, i32, i64, P, i64, P, i64, i64, P, i32, i64, i32, P, P]
+        L.bfz_linear_grad_weight.argtypes = [P, i64, P, i64, P, i64, P, i64, i64, i64, i64, P, i32, i64, i32, P, P]
+        L.bfz_layer_norm.argtypes = [P, i32, i64, i64, i64, P, P, i32, f32, P, i32, i64, P, P, P]
+        L.bfz_layer_norm_work_bytes.argtypes = [i64, i64]
+        L.bfz_layer_norm_work_bytes.restype = i64
+        L.bfz_layer_norm_grad.argtypes = [P, i32, i64, P, i32, i64, i64, i64, P, i32, P, P, P, i32, i64, P, P, i32, i32, P, P]
+        L.bfz_adamw_list.argtypes = [P, i32, A, P, P]
         L.bfz_last_error.argtypes = []
         L.bfz_last_error.restype = C.c_char_p
         _lib = L
@@ -454,3 +465,7 @@ from ._tensors import elsewhere, home_device, raw_stream  # noqa: E402
 from .norm import clip_coef, clip_grads, grad_norm, norm_workspace, shard_grad_norm  # noqa: E402
 from .embedding import embed, embed_grad, embed_grad_workspace  # noqa: E402
 from .vocab_loss import vocab_loss, vocab_loss_grad, vocab_loss_workspace  # noqa: E402
+from .linear import (linear, linear_grad_input, linear_grad_weight, linear_workspace, quantize,  # noqa: E402
+                     quantize_buffers)
+from .layer_norm import layer_norm, layer_norm_grad, layer_norm_workspace  # noqa: E402
+from .adamw_list import AdamWList, adamw_states  # noqa: E402

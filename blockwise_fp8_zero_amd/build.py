@@ -8,7 +8,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbfz.so")
 SOURCES = ["plan.cpp", "abi.cpp", "kernels.hip", "ops_abi.cpp", "norm.hip", "embedding.hip",
-           "vocab_loss.hip"]
+           "vocab_loss.hip", "layer_abi.cpp", "linear.hip", "layer_norm.hip", "adamw_list.hip"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

@@ -143,15 +143,13 @@ extern "C" int unpack_fp8(const bfz_plan* plan, const uint8_t* codes, const floa
     return BFZ_OK;
 }
 
-namespace {
-
 // The step's scalars, formed in double and rounded to binary32 once each:
 // the bias corrections 1 - beta^t enter as lr / (1 - beta1^t) and
 // sqrt(1 - beta2^t), as in the Int8AdamW step (lpnh.cn essay, section 4.3).
 // opts may be NULL (every option 0).  eps must be positive: it keeps the
 // denominator of an all-zero slot (every padding slot) away from 0 / 0.
-int make_scalars(const bfz_adamw* hp, const bfz_step_options* opts, StepScalars* s,
-                 const char* where) {
+int bfz::make_scalars(const bfz_adamw* hp, const bfz_step_options* opts, StepScalars* s,
+                      const char* where) {
     const bfz_step_options none{};
     if (!opts) opts = &none;
     if (opts->reserved != 0) return fail(BFZ_EINVAL, "%s: bfz_step_options.reserved must be 0", where);
@@ -178,6 +176,8 @@ int make_scalars(const bfz_adamw* hp, const bfz_step_options* opts, StepScalars*
     s->grad_scale = nullptr;
     return BFZ_OK;
 }
+
+namespace {
 
 int check_state(float* master, float* m, float* v, uint8_t* codes, float* scale_inv,
                 const char* where) {

@@ -91,6 +91,9 @@ int fail(int code, const char* fmt, ...);
 int check_plan(const bfz_plan* plan, const char* where);
 int check_weights(const bfz_plan* plan, const void* const* ptrs, const char* where);
 
+// The step's scalars from its hyper-parameters and options (abi.cpp).
+int make_scalars(const bfz_adamw* hp, const bfz_step_options* opts, StepScalars* s, const char* where);
+
 }  // namespace bfz
 
 struct bfz_plan {

@@ -544,6 +544,159 @@ int bfz_vocab_loss_grad(const void* hidden, int64_t hidden_ld, int64_t n, const 
 int bfz_vocab_loss_shape(int64_t n, int64_t vocab, int64_t dim, int32_t dweight_dtype,
                          int64_t* shape);
 
+/* ---- a layer around the FP8 weights, and the tensors that are not such weights ----
+ * Conventions as for the operators above. */
+
+/*
+ * E4M3 quantizer of activations and of their gradients, one scale for each
+ * block of 128.  A group is 128 consecutive columns of one row (tiles == 0) or
+ * a 128x128 tile (tiles != 0), cut off at the matrix's edge:
+ *   scale = amax / 448  (1 if amax = 0; 2^-149 if it rounds to 0), or with
+ *           pow2 != 0 the smallest 2^T with 448 2^T >= amax, T >= -149
+ *   code  = E4M3(x / scale), quotient in binary32, then to the nearest value,
+ *           ties to even, saturating
+ * as the step quantizes a weight's tile.  A NaN stays alone (its code is a
+ * NaN); an infinity makes its group's scale infinite and the group NaN.
+ * x: [n, dim], BFZ_F32, BFZ_BF16 or BFZ_F16, rows x_ld elements apart, any
+ * element alignment.  codes: [n, dim], 16-byte aligned, rows codes_ld apart, a
+ * multiple of 16; columns dim to the next multiple of 16 are written with
+ * zeros, others of a row left alone.  scales: rows scales_ld floats apart, of
+ * [ceil(dim/128), n] for row groups, one row for each 128 columns, and of the
+ * row-major grid [ceil(n/128), ceil(dim/128)] for tiles.
+ * At most 2^24 rows, dim 2^20, codes_ld 2^21.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int bfz_quantize(const void* x, int32_t x_dtype, int64_t x_ld, int64_t n, int64_t dim,
+                 int32_t tiles, int32_t pow2, uint8_t* codes, int64_t codes_ld, float* scales,
+                 int64_t scales_ld, void* stream);
+
+/*
+ * Linear layer on a FP8 weight: out = X W^T, with X the value (code * scale) of
+ * x and W that of weight, products on the matrix cores in E4M3:
+ *   out[t][o] = sum over blocks k of 128 columns of
+ *               scale_x(t, k) grid(o / 128, k) sum_i x[t][i] weight[o][i]
+ * Sums of a block and over blocks are binary32, each in an order that the
+ * sizes fix; the products of two scales are binary32 and must not overflow.
+ * The result is rounded once to out's type.
+ * x: [n, cols], E4M3 codes as bfz_quantize leaves them (zeros up to the next
+ * multiple of 16 columns) with their scales in its row (tiles == 0) or tile
+ * form; or BFZ_F32, BFZ_BF16 or BFZ_F16 values with scales NULL and tiles 0,
+ * quantized here by rows.  weight: codes [rows, cols], any alignment, with
+ * their row-major scale grid [ceil(rows/128), ceil(cols/128)], as the step
+ * writes both; one expert of a (E, rows, cols) weight is one call.  Rows that
+ * start on 16-byte boundaries and are a multiple of 16 wide are read in place,
+ * others first copied into the workspace.  out: [n, rows], BFZ_F32, BFZ_BF16 or
+ * BFZ_F16, rows out_ld apart, any element alignment.
+ * work: bfz_linear_work_bytes(n, rows, cols, x_dtype, copy) of device memory,
+ * 256-byte aligned, not shared by calls that may run at the same time; copy != 0
+ * where the weight's pointer or weight_ld is not a multiple of 16.  It serves
+ * every smaller n, and with x_dtype BFZ_E4M3 both gradients.
+ * At most 2^24 tokens, 2^20 rows and columns, strides of codes 2^21.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int64_t bfz_linear_work_bytes(int64_t n, int64_t rows, int64_t cols, int32_t x_dtype, int32_t copy);
+int bfz_linear(const void* x, int32_t x_dtype, int64_t x_ld, const float* scales,
+               int64_t scales_ld, int32_t tiles, int64_t n, const uint8_t* weight,
+               int64_t weight_ld, const float* grid, int64_t rows, int64_t cols, void* out,
+               int32_t out_dtype, int64_t out_ld, void* work, void* stream);
+
+/*
+ * Its gradients from quantized gradients of the output, dout [n, rows] (codes
+ * and scales as bfz_quantize leaves them):
+ *   bfz_linear_grad_input:   dx = dOut W       [n, cols], written or with
+ *                            accumulate != 0 added to dx
+ *   bfz_linear_grad_weight:  dweight = dOut^T X  [rows, cols], likewise
+ * The first takes dout's scales in either form, the second both operands' in
+ * the tile form, whose scales hold whichever way a tile is read: the codes that
+ * the forward product read serve here, and no transposed copy is made.
+ * accumulate adds in binary32 before the one rounding.  dweight with n = 0 is
+ * zero.  Other arguments, limits and errors as above.
+ */
+int bfz_linear_grad_input(const uint8_t* dout, int64_t dout_ld, const float* scales,
+                          int64_t scales_ld, int32_t tiles, int64_t n, const uint8_t* weight,
+                          int64_t weight_ld, const float* grid, int64_t rows, int64_t cols,
+                          void* dx, int32_t dx_dtype, int64_t dx_ld, int32_t accumulate,
+                          void* work, void* stream);
+int bfz_linear_grad_weight(const uint8_t* dout, int64_t dout_ld, const float* dout_grid,
+                           int64_t dout_grid_ld, const uint8_t* x, int64_t x_ld,
+                           const float* x_grid, int64_t x_grid_ld, int64_t n, int64_t rows,
+                           int64_t cols, void* dweight, int32_t dweight_dtype,
+                           int64_t dweight_ld, int32_t accumulate, void* work, void* stream);
+
+/*
+ * Layer norm of rows:
+ *   mean = sum x / dim,  rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps)
+ *   out  = (x - mean) rstd weight + bias
+ * in binary32, rounded once to out's type.  weight and bias: dim elements of
+ * param_dtype, each may be NULL (ones, zeros).  mean, rstd: n floats, for the
+ * gradient, each may be NULL.  x, out: [n, dim], BFZ_F32, BFZ_BF16 or BFZ_F16,
+ * any element alignment; out may be x itself when type and stride are equal.
+ * A row's non-finite values stay in that row.  eps > 0.  At most 2^24 rows,
+ * dim 32768.  Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int bfz_layer_norm(const void* x, int32_t x_dtype, int64_t x_ld, int64_t n, int64_t dim,
+                   const void* weight, const void* bias, int32_t param_dtype, float eps,
+                   void* out, int32_t out_dtype, int64_t out_ld, float* mean, float* rstd,
+                   void* stream);
+
+/*
+ * Its gradient.  With h = (x - mean) rstd and g = dout weight:
+ *   dx = rstd (g - sum g / dim - h sum(g h) / dim)
+ *   dweight = sum over rows of dout h,  dbias = sum over rows of dout
+ * mean, rstd: as bfz_layer_norm wrote them.  dx (its own type; it may be dout
+ * itself when type and stride are equal), dweight and dbias (dim elements of
+ * dparam_dtype) may each be NULL; accumulate != 0 adds to dweight and dbias, in
+ * binary32 before one rounding.  Every sum has an order that the sizes fix: two
+ * runs give the same bits.  work: bfz_layer_norm_work_bytes(n, dim) of device
+ * memory (it serves every smaller n), 256-byte aligned, not shared by calls
+ * that may run at the same time, NULL allowed where dweight and dbias are.
+ * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int64_t bfz_layer_norm_work_bytes(int64_t n, int64_t dim);
+int bfz_layer_norm_grad(const void* dout, int32_t dout_dtype, int64_t dout_ld, const void* x,
+                        int32_t x_dtype, int64_t x_ld, int64_t n, int64_t dim, const void* weight,
+                        int32_t param_dtype, const float* mean, const float* rstd, void* dx,
+                        int32_t dx_dtype, int64_t dx_ld, void* dweight, void* dbias,
+                        int32_t dparam_dtype, int32_t accumulate, void* work, void* stream);
+
+/* A tensor of bfz_adamw_list: n elements back to back, each array aligned to
+ * its elements.  State blocks are 256 consecutive elements, the last one cut
+ * off. */
+#define BFZ_STATE_BLOCK 256
+typedef struct {
+    void* param;        /* BFZ_F32, BFZ_BF16 or BFZ_F16 */
+    const void* grad;   /* likewise */
+    void* m;            /* floats, or BFZ_E4M3 codes */
+    void* v;
+    float* m_scale;     /* of E4M3 states: ceil(n/256) block scales; else NULL */
+    float* v_scale;
+    int64_t n;
+    int32_t param_dtype, grad_dtype, state_dtype;
+    int32_t reserved;   /* 0 */
+} bfz_adamw_tensor;
+
+/*
+ * AdamW over many tensors, the update of adamw_fp8_step, every operation one
+ * binary32 rounding in this order:
+ *   g = grad * *grad_scale (NULL: grad)
+ *   m' = beta1 m + (1-beta1) g;  v' = beta2 v + (1-beta2) (g g)
+ *   param' = param - lr/(1-beta1^t) (m' / (sqrt(v') / sqrt(1-beta2^t) + eps))
+ *   param' = param' - lr weight_decay param'
+ * param' is rounded once to its type.  E4M3 states hold m and r = sqrt(v), so
+ * that v is the square of a code times its block's scale:
+ *   m = m_code m_scale,  v = (v_code v_scale)^2, of binary32 products
+ *   afterwards scale = amax / 448 and code = E4M3(value / scale) of each
+ *   block's m' and sqrt(v'), by the rules of bfz_quantize, but that a positive
+ *   sqrt(v') never gets code 0 (eps alone would be left to divide by).
+ * Zeroed codes with any finite scales are zero states.  A NaN stays in its
+ * element, an infinity makes its block NaN.  Tensors must not overlap, but for
+ * a gradient that several of them share; n = 0 is allowed.  grad_scale: a
+ * device float, read when the kernel runs.  One launch for 56 tensors, one more
+ * for each further 56.  Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
+ */
+int bfz_adamw_list(const bfz_adamw_tensor* tensors, int32_t n_tensors, const bfz_adamw* hp,
+                   const float* grad_scale, void* stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char* bfz_last_error(void);
 
