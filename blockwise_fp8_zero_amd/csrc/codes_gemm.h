@@ -1,0 +1,302 @@
+// The matrix product of E4M3 codes with a scale for each block of 128 k:
+//
+//   D[n][m] = sum over blocks kb of scale_b(n, kb) scale_a(m / 128, kb) P(n, m, kb)
+//   P(n, m, kb) = sum over the block's k of A[m][k] B[n][k]
+//
+// A block's sum P is one matrix instruction of 128 k (or four of 32, below), its
+// scaling one fused operation for each result: while a row of tiles is
+// multiplied, the sums of the row before are scaled and added.
+//
+// A workgroup owns a kBM x kBN tile of D and walks k a block at a time.  A
+// block's operands go from memory straight into LDS (16 bytes a lane), into one
+// of two buffers.  When a wave has read the last of a block it meets the others;
+// the loads of the block after next then go into the buffer just read, and the
+// last row of tiles is multiplied while the next block's first fragments are
+// read.
+//
+// Operands come in two layouts, so that no operand is ever transposed in memory:
+// KC, k contiguous, and KR, m or n contiguous (rows of k), read with the LDS
+// transpose instruction.  Which k of a block a lane holds is free as long as both
+// operands agree: lane group g = lane / 16 holds k 16 g to 16 g + 15 and 64 + 16 g
+// on.  LDS rows have no padding (the direct loads write lanes back to back);
+// their 16-byte pieces are permuted by an XOR with the row, chosen so that the
+// lanes that read together touch all banks.
+//
+// kExact: the E4M3 matrix instructions align 8 products to the largest and keep
+// 13 bits below its exponent, which a bfloat16 or float16 result does not show
+// (5e-5 of it against 1.7e-3 for its own rounding) but a float32 one does.  Those
+// take bf16 instructions on the codes' values, whose products are exact and whose
+// sums are binary32, at half the rate.
+#pragma once
+
+#include "vocab_gemm.h"
+
+namespace bfz {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// Where B's scales lie: [k / 128][n], or by 128x128 tile [n / 128][k / 128] or
+// [k / 128][n / 128], rows scales_ld apart.
+constexpr int kEachOfN = 0, kTilesOfN = 1, kTilesOfK = 2;
+
+struct ProductArgs : GemmArgs {  // grid: scale of (m / 128, k / 128) at grid_m, grid_k; k_per_split a multiple of 128
+    const float* scales;
+    int64_t scales_ld;
+    int32_t tiles;
+};
+
+// ---- operand layouts ----------------------------------------------------------
+
+template <int kRows, int kWaves>
+struct CodesKC {
+    static constexpr int kBytes = kRows * 128;
+    static constexpr int kLoads = kBytes / 1024 / kWaves;
+    static_assert(kLoads >= 1 && kBytes % (1024 * kWaves) == 0, "whole loads for each wave");
+    uint32_t at[2];  // LDS offset of tile 0's fragment, by half
+    __device__ __forceinline__ static const char* base(const Operand& o, int64_t row0, int64_t k0) {
+        return static_cast<const char*>(o.p) + row0 * o.ld + k0;
+    }
+    __device__ __forceinline__ static int64_t advance(const Operand&) { return 128; }
+    // k that lane `lane` of load j covers from; the same for every load
+    __device__ __forceinline__ static int k_of(int, int, int lane) { return 16 * ((lane & 7) ^ (lane >> 3)); }
+    __device__ __forceinline__ static uint32_t offset(const Operand& o, int64_t row0, int j, int wave, int lane) {
+        const int row = (j * kWaves + wave) * 8 + (lane >> 3);
+        return row0 + row < o.extent ? (uint32_t)(row * o.ld) + 16u * ((lane & 7) ^ (lane >> 3)) : kNowhere;
+    }
+    __device__ __forceinline__ CodesKC(uint32_t lds, int row0, int lane) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) at[h] = lds + (row0 + (lane & 15)) * 128 + (((4 * h + (lane >> 4)) ^ (lane & 7)) << 4);
+    }
+    __device__ __forceinline__ i32x8 read(uint32_t stage, int t) const {
+        const i32x4 lo = lds_read<i32x4>(at[0] + stage + t * 2048), hi = lds_read<i32x4>(at[1] + stage + t * 2048);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// kTiles: the 16-wide tiles a wave reads.
+template <int kRows, int kWaves, int kTiles>
+struct CodesKR {
+    static constexpr int kBytes = kRows * 128;
+    static constexpr int kLoads = kBytes / 1024 / kWaves;
+    static_assert(kLoads >= 1 && kBytes % (1024 * kWaves) == 0, "whole loads for each wave");
+    static_assert(kRows == 256 || kRows == 128, "the permutation spans 256 bytes");
+    static constexpr int kPieces = kRows / 16, kRowsOfLoad = 64 / kPieces;
+    uint32_t at[kTiles];
+    // by which a row's pieces are permuted: 8 rows that one transpose reads, of
+    // two lane groups, fall on 16 different pieces of 256 bytes
+    __device__ __forceinline__ static int mix(int k) {
+        return kRows == 256 ? (k & 7) | ((k >> 1) & 8) : ((k >> 1) & 3) | ((k >> 2) & 4);
+    }
+    __device__ __forceinline__ static const char* base(const Operand& o, int64_t row0, int64_t k0) {
+        return static_cast<const char*>(o.p) + k0 * o.ld + row0;
+    }
+    __device__ __forceinline__ static int64_t advance(const Operand& o) { return 128 * o.ld; }
+    __device__ __forceinline__ static int k_of(int j, int wave, int lane) { return (j * kWaves + wave) * kRowsOfLoad + lane / kPieces; }
+    __device__ __forceinline__ static uint32_t offset(const Operand& o, int64_t row0, int j, int wave, int lane) {
+        const int k = k_of(j, wave, lane);
+        const int piece = (lane & (kPieces - 1)) ^ mix(k);
+        return row0 + 16 * piece < o.extent ? (uint32_t)(k * o.ld) + 16u * piece : kNowhere;
+    }
+    __device__ __forceinline__ CodesKR(uint32_t lds, int row0, int lane) {
+        const int k = 16 * (lane >> 4) + ((lane & 15) >> 1);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) at[t] = lds + k * kRows + (((row0 / 16 + t) ^ mix(k)) << 4) + 8 * (lane & 1);
+    }
+    __device__ __forceinline__ i32x8 read(uint32_t stage, int t) const {
+        typedef int i32x2 __attribute__((ext_vector_type(2)));
+        typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+        const uint32_t p = at[t] + stage;
+        i32x8 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // k 8 on has another permutation than k: bit 3 of k leaves mix alone at 256, and 128, bytes
+            const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(uintptr_t)(p + (64 * (j >> 1) + 8 * (j & 1)) * kRows));
+            r[2 * j] = x[0];
+            r[2 * j + 1] = x[1];
+        }
+        return r;
+    }
+};
+
+// ---- the kernel -----------------------------------------------------------------
+
+template <bool kExact>
+struct Multiply;
+
+template <>
+struct Multiply<false> {
+    typedef i32x8 Value;
+    __device__ __forceinline__ static Value value(const i32x8& f) { return f; }
+    __device__ __forceinline__ static f32x4 run(const Value& a, const Value& b) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+    }
+};
+
+template <>
+struct Multiply<true> {
+    struct Value {
+        bf16x8 v[4];
+    };
+    __device__ __forceinline__ static Value value(const i32x8& f) {
+        Value r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.v[j] = codes_to_bf16(u32x2{(uint32_t)f[2 * j], (uint32_t)f[2 * j + 1]}, 1.0f);
+        return r;
+    }
+    __device__ __forceinline__ static f32x4 run(const Value& a, const Value& b) {
+        f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[j], b.v[j], r, 0, 0, 0);
+        return r;
+    }
+};
+
+template <class A, class B, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact, class Epilogue>
+__global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(ProductArgs g, Epilogue epilogue) {
+    constexpr int kTM = kTileM / kWavesM / 16, kTN = kTileN / kWavesN / 16;
+    static_assert(kTileDim % (kTM * 16) == 0 && kTileDim % (kTN * 16) == 0, "a wave's rows and tokens lie in one tile each");
+    constexpr uint32_t kStage = A::kBytes + B::kBytes;
+    constexpr uint32_t kOther = kStage;
+    typedef Multiply<kExact> Mul;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / kWavesN, wn = wave % kWavesN;
+    int tm, tn, split;
+    tile_of(g, tm, tn, split);
+    const int64_t m0 = (int64_t)tm * kTileM, n0 = (int64_t)tn * kTileN;
+    const int64_t k0 = split * g.k_per_split;
+    const int64_t k1 = min(g.k, k0 + g.k_per_split);
+    const int steps = (int)((max(k1 - k0, (int64_t)0) + kTileDim - 1) / kTileDim);
+
+    const uint32_t lds = lds_address(smem);
+    const A fa(lds, wm * kTM * 16, lane);
+    const B fb(lds + A::kBytes, wn * kTN * 16, lane);
+    uint32_t off_a[A::kLoads], off_b[B::kLoads];
+#pragma unroll
+    for (int j = 0; j < A::kLoads; ++j) off_a[j] = A::offset(g.a, m0, j, wave, lane);
+#pragma unroll
+    for (int j = 0; j < B::kLoads; ++j) off_b[j] = B::offset(g.b, n0, j, wave, lane);
+    const char* base_a = A::base(g.a, m0, k0);
+    const char* base_b = B::base(g.b, n0, k0);
+    const int64_t adv_a = A::advance(g.a), adv_b = B::advance(g.b);
+    const uint32_t lds_a = lds + wave * 1024, lds_b = lds_a + A::kBytes;
+    constexpr int kWaves = kWavesM * kWavesN;
+
+    // Loads of the next block into buffer `stage`; past the end of k they give
+    // zero (no branch: the lanes' offsets are selected).
+    int64_t left_a = g.a.k - k0, left_b = g.b.k - k0;
+    auto issue = [&](uint32_t stage) {
+        const i32x4 ra = buffer_of(base_a), rb = buffer_of(base_b);
+        const int la = (int)max((int64_t)0, min(left_a, (int64_t)kTileDim)), lb = (int)max((int64_t)0, min(left_b, (int64_t)kTileDim));
+        each<A::kLoads>([&](auto i) {
+            constexpr int j = decltype(i)::value;
+            load_to_lds(ra, A::k_of(j, wave, lane) < la ? off_a[j] : kNowhere, lds_a + stage + j * (kWaves * 1024));
+        });
+        each<B::kLoads>([&](auto i) {
+            constexpr int j = decltype(i)::value;
+            load_to_lds(rb, B::k_of(j, wave, lane) < lb ? off_b[j] : kNowhere, lds_b + stage + j * (kWaves * 1024));
+        });
+        base_a += adv_a;
+        base_b += adv_b;
+        left_a -= kTileDim;
+        left_b -= kTileDim;
+    };
+
+    // scales of this wave's rows and of the lane's tokens in a block, beyond the
+    // edges those of the last
+    const int64_t mw = m0 + wm * kTM * 16, nw = n0 + wn * kTN * 16;
+    const float* scale_a = g.grid + min(mw / kTileDim, g.blocks_m - 1) * g.grid_m + k0 / kTileDim * g.grid_k;
+    const int64_t nlast = g.b.extent - 1;
+    const int64_t tile_b = min(nw, nlast) / kTileDim;
+    const float* scale_b = g.tiles == kTilesOfN ? g.scales + tile_b * g.scales_ld + k0 / kTileDim
+                                                : g.scales + k0 / kTileDim * g.scales_ld + (g.tiles ? tile_b : 0);
+    const int64_t step_b = g.tiles == kTilesOfN ? 1 : g.scales_ld;
+    int32_t token[kTN];
+#pragma unroll
+    for (int u = 0; u < kTN; ++u) token[u] = g.tiles ? 0 : (int32_t)min(nw + 16 * u + (lane & 15), nlast);
+    float next[kTN], next_a, now[kTN], by[kTN];
+    auto load_scales = [&](bool there) {
+        if (!there) return;
+        next_a = *scale_a;
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) next[u] = scale_b[token[u]];
+        scale_a += g.grid_k;
+        scale_b += step_b;
+    };
+    // Here, so that the wait which the compiler puts before their use does not
+    // catch the loads issued after it.
+    auto take_scales = [&]() {
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) {
+            now[u] = next[u] * next_a;
+            __asm__ volatile("" : "+v"(now[u]));
+        }
+    };
+
+    f32x4 acc[kTM][kTN];
+#pragma unroll
+    for (int t = 0; t < kTM; ++t)
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    if (steps > 0) {
+        load_scales(true);
+        take_scales();
+        issue(0);
+        issue(kOther);
+        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(A::kLoads + B::kLoads) : "memory");
+        __builtin_amdgcn_s_barrier();
+        i32x8 a[2], raw[kTN];
+        typename Mul::Value b[kTN];
+        f32x4 part[kTN];
+        a[0] = fa.read(0, 0);
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) raw[u] = fb.read(0, u);
+        auto scale_row = [&](auto row, auto col) {
+            constexpr int t = decltype(row)::value, u = decltype(col)::value;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(part[u][i], by[u], acc[t][u][i]);
+        };
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) {
+            part[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            by[u] = 0.0f;
+        }
+        uint32_t cur = 0;
+        for (int s = 0; s < steps; ++s) {
+            load_scales(s + 1 < steps);
+            each<kTM>([&](auto row) {
+                constexpr int t = decltype(row)::value;
+                if constexpr (t == kTM - 1) {
+                    // every fragment of this block is read; the next block has arrived
+                    wait_loads();
+                    __builtin_amdgcn_s_barrier();
+                    __builtin_amdgcn_sched_barrier(0);
+                    take_scales();
+                    issue(cur);
+                    cur = kOther - cur;
+                    a[(t + 1) & 1] = fa.read(cur, 0);
+                } else {
+                    a[(t + 1) & 1] = fa.read(cur, t + 1);
+                }
+                const typename Mul::Value av = Mul::value(a[t & 1]);
+                each<kTN>([&](auto col) {
+                    constexpr int u = decltype(col)::value;
+                    if constexpr (t == 0) b[u] = Mul::value(raw[u]);
+                    const f32x4 p = Mul::run(av, b[u]);
+                    if constexpr (t == kTM - 1) raw[u] = fb.read(cur, u);
+                    scale_row(std::integral_constant<int, (t + kTM - 1) % kTM>{}, col);
+                    part[u] = p;
+                    if constexpr (t == 0) by[u] = now[u];
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        }
+        each<kTN>([&](auto col) { scale_row(std::integral_constant<int, kTM - 1>{}, col); });
+        wait_loads();  // the loads issued past the end
+    }
+    const WaveTile w{mw, nw, tm, wm, split, lane};
+    epilogue.template run<kTM, kTN>(acc, w);
+}
+
+}  // namespace bfz

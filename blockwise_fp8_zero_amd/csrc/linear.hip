@@ -2,17 +2,18 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
+#include "codes_gemm.h"
 #include "layer_internal.h"
 #include "quant_device.h"
 
 namespace bfz {
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kThreads = 256;
+constexpr int64_t kMostSums = int64_t(1) << 23;  // floats that the splits of a product may take
 
 // ---- quantizer ------------------------------------------------------------------
 
@@ -90,110 +91,157 @@ int quantize(const QuantizeArgs& a, hipStream_t stream) {
 
 // ---- products -------------------------------------------------------------------
 
-// D[t][m] = sum_k scale_b(t, k) scale_a(m, k) B[t][k] A[m][k], one wave for 16 by
-// 16 of D, operands read byte by byte: right for every stride and size.
-struct SimpleArgs {
-    const uint8_t* a;
-    const uint8_t* b;
-    int64_t a_m, a_k, b_n, b_k;  // strides, bytes
-    const float* sa;
-    const float* sb;
-    int64_t sa_m, sa_k, sb_n, sb_k;  // of scales, by 128 m and 128 k; n by tile or each
-    int32_t sb_shift;
-    int64_t m, n, k;
+// Results of a product, rounded to their type, or a split's binary32 sums.  Two
+// tiles of 16 rows are exchanged between the halves of lane pairs, so that a lane
+// holds 8 consecutive m of a token.
+struct StoreEpilogue {
     void* out;
-    int32_t out_type, accumulate;
-    int64_t out_ld;
+    int64_t ld, slab;  // slab: from split to split
+    int64_t m, n;      // extents
+    int32_t type, add, vec;
+    template <int kTM, int kTN>
+    __device__ __forceinline__ void run(const f32x4 (&acc)[kTM][kTN], const WaveTile& w) const {
+        const int g = w.lane >> 4;
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) {
+            const int64_t token = w.n0 + 16 * u + (w.lane & 15);
+#pragma unroll
+            for (int t = 0; t < kTM; t += 2) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[t][u][i]), __float_as_uint(acc[t + 1][u][i]), false, false);
+                    x[i] = __uint_as_float(r[0]);
+                    x[4 + i] = __uint_as_float(r[1]);
+                }
+                const int64_t c = w.m0 + 16 * (t + (g & 1)) + 8 * (g >> 1);
+                if (token >= n || c >= m) continue;
+                const int64_t at = w.split * slab + token * ld + c;
+                if (type == kF32) put(static_cast<float*>(out) + at, c, x);
+                else if (type == kBF16) put(static_cast<bf16_t*>(out) + at, c, x);
+                else put(static_cast<f16_t*>(out) + at, c, x);
+            }
+        }
+    }
+    template <class O>
+    __device__ __forceinline__ void put(O* p, int64_t c, float (&x)[8]) const {
+        if (vec && c + 8 <= m) {
+            if (add) {
+                float y[8];
+                load8(p, y);
+#pragma unroll
+                for (int l = 0; l < 8; ++l) x[l] += y[l];
+            }
+            store8(p, x);
+        } else {
+#pragma unroll
+            for (int l = 0; l < 8; ++l)
+                if (c + l < m) p[l] = Elem<O>::to(add ? Elem<O>::get(p[l]) + x[l] : x[l]);
+        }
+    }
 };
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// 8 codes as bf16, which holds them exactly.
-__device__ __forceinline__ bf16x8 codes_to_bf16(int w0, int w1) {
-    bf16x8 r;
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
-    r[0] = a[0];
-    r[1] = a[1];
-    r[2] = b[0];
-    r[3] = b[1];
-    r[4] = c[0];
-    r[5] = c[1];
-    r[6] = d[0];
-    r[7] = d[1];
-    return r;
-}
-
-__device__ __forceinline__ i32x8 gather(const uint8_t* p, int64_t stride, bool there, int64_t k0, int64_t k, int g) {
-    i32x8 r;
+// The sums of a split product: out = slabs added in their order.
+template <class O>
+__global__ __launch_bounds__(kThreads) void join_splits_kernel(const float* __restrict__ sums, int32_t splits, StoreEpilogue s) {
+    const int64_t pieces = (s.m + 7) / 8;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= s.n * pieces) return;
+    const int64_t token = i / pieces, c = 8 * (i - token * pieces);
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int32_t k = 0; k < splits; ++k) {
+        float y[8];
+        load8(sums + k * s.slab + token * (pieces * 8) + c, y);
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int l = 0; l < 4; ++l) {
-            const int64_t at = k0 + (w < 4 ? 16 * g + 4 * w : 64 + 16 * g + 4 * (w - 4)) + l;
-            if (there && at < k) x |= (uint32_t)p[at * stride] << (8 * l);
-        }
-        r[w] = (int)x;
+        for (int l = 0; l < 8; ++l) x[l] += y[l];
     }
-    return r;
+    s.put(static_cast<O*>(s.out) + token * s.ld + c, c, x);
 }
 
-__device__ __forceinline__ float get_any(const void* p, int type, int64_t i) {
-    return type == kF32 ? static_cast<const float*>(p)[i]
-                        : type == kBF16 ? Elem<bf16_t>::get(static_cast<const bf16_t*>(p)[i]) : Elem<f16_t>::get(static_cast<const f16_t*>(p)[i]);
-}
-
-__device__ __forceinline__ void put_any(void* p, int type, int64_t i, float x) {
-    if (type == kF32) static_cast<float*>(p)[i] = x;
-    else if (type == kBF16) static_cast<bf16_t*>(p)[i] = Elem<bf16_t>::to(x);
-    else static_cast<f16_t*>(p)[i] = Elem<f16_t>::to(x);
-}
-
-__global__ __launch_bounds__(64) void simple_product_kernel(SimpleArgs s, int32_t m_tiles) {
-    const int lane = threadIdx.x, g = lane >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x % m_tiles) * 16, n0 = (int64_t)(blockIdx.x / m_tiles) * 16;
-    const int64_t m = m0 + (lane & 15), n = n0 + (lane & 15);
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t k0 = 0; k0 < s.k; k0 += kTileDim) {
-        const i32x8 a = gather(s.a + min(m, s.m - 1) * s.a_m, s.a_k, m < s.m, k0, s.k, g);
-        const i32x8 b = gather(s.b + min(n, s.n - 1) * s.b_n, s.b_k, n < s.n, k0, s.k, g);
-        f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (s.out_type == kF32) {
+// A weight whose rows the products cannot read in place, copied into rows of
+// `width` bytes with zeros at the end.
+__global__ __launch_bounds__(kThreads) void copy_weight_kernel(const uint8_t* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
+                                                               uint8_t* __restrict__ dst, int64_t width) {
+    const int64_t words = width / 4;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows * words; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t r = i / words, c = 4 * (i - r * words);
+        uint32_t w = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(a[2 * j], a[2 * j + 1]), codes_to_bf16(b[2 * j], b[2 * j + 1]), part, 0, 0, 0);
-        } else {
-            part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, part, 0, 0, 0, 0, 0, 0);
-        }
-        const float scale = s.sa[m0 / kTileDim * s.sa_m + k0 / kTileDim * s.sa_k] *
-                            s.sb[(min(n, s.n - 1) >> s.sb_shift) * s.sb_n + k0 / kTileDim * s.sb_k];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(part[i], scale, acc[i]);
-    }
-    if (n >= s.n) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t at = m0 + 4 * g + i;
-        if (at >= s.m) continue;
-        const int64_t e = n * s.out_ld + at;
-        put_any(s.out, s.out_type, e, s.accumulate ? get_any(s.out, s.out_type, e) + acc[i] : acc[i]);
+        for (int l = 0; l < 4; ++l)
+            if (c + l < cols) w |= (uint32_t)src[r * ld + c + l] << (8 * l);
+        reinterpret_cast<uint32_t*>(dst)[i] = w;
     }
 }
 
-int simple_product(const SimpleArgs& s, void* stream) {
-    const int64_t m_tiles = (s.m + 15) / 16, n_tiles = (s.n + 15) / 16;
-    hipLaunchKernelGGL(simple_product_kernel, dim3((uint32_t)(m_tiles * n_tiles)), dim3(64), 0, (hipStream_t)stream, s, (int32_t)m_tiles);
+// ---- host -------------------------------------------------------------------------
+
+template <class A, class B, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact>
+int launch_tiles(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
+    constexpr int kLds = 2 * (A::kBytes + B::kBytes);
+    const auto kernel = codes_gemm_kernel<A, B, kTileM, kTileN, kWavesM, kWavesN, kExact, StoreEpilogue>;
+    static std::atomic<bool> ready{false};
+    if (!ready.load(std::memory_order_relaxed)) {
+        const hipError_t rc = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        if (rc != hipSuccess) return rc;
+        ready.store(true, std::memory_order_relaxed);
+    }
+    g.tiles_m = (int32_t)((g.a.extent + kTileM - 1) / kTileM);
+    g.tiles_n = (int32_t)((g.b.extent + kTileN - 1) / kTileN);
+    g.group_m = std::min(g.tiles_m, 4);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(g.tiles_m * g.tiles_n * g.splits)), dim3(64 * kWavesM * kWavesN), kLds, stream, g, e);
     return hipGetLastError();
 }
 
-void token_scales(SimpleArgs& s, const Codes& c) {
-    s.sb = c.scales;
-    s.sb_n = c.tiles ? c.scales_ld : 1;
-    s.sb_k = c.tiles ? 1 : c.scales_ld;
-    s.sb_shift = c.tiles ? 7 : 0;
+template <bool kAKR, int kRows, int kWaves, int kTiles>
+using Layout = std::conditional_t<kAKR, CodesKR<kRows, kWaves, kTiles>, CodesKC<kRows, kWaves>>;
+
+// Splits of k until there are tiles for every CU.
+int32_t splits_for(int64_t tiles, int64_t k, int64_t m, int64_t n) {
+    const int64_t blocks = (k + kTileDim - 1) / kTileDim;
+    int64_t s = std::min<int64_t>(std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), blocks / 4), 16);
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(s, kMostSums / std::max<int64_t>(1, m * n)));
+}
+
+bool wide_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256) >= 192; }
+
+template <bool kAKR, bool kBKR, bool kExact>
+int launch_product(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
+    if constexpr (kExact) {
+        if (wide_tiles(g.a.extent, g.b.extent))
+            return launch_tiles<Layout<kAKR, 256, 8, 4>, Layout<kBKR, 128, 8, 4>, 256, 128, 4, 2, true>(g, e, stream);
+    } else {
+        if (wide_tiles(g.a.extent, g.b.extent))
+            return launch_tiles<Layout<kAKR, 256, 8, 8>, Layout<kBKR, 256, 8, 4>, 256, 256, 2, 4, false>(g, e, stream);
+    }
+    return launch_tiles<Layout<kAKR, 128, 4, 4>, Layout<kBKR, 128, 4, 4>, 128, 128, 2, 2, kExact>(g, e, stream);
+}
+
+template <bool kAKR, bool kBKR>
+int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* sums, hipStream_t stream) {
+    const bool exact = a.out_type == kF32;
+    const int size = dtype_size(a.out_type);
+    StoreEpilogue e{a.out, a.out_ld, 0, m, n, a.out_type, a.accumulate, 0};
+    e.vec = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_ld * size)) & 15u) == 0;
+    const int64_t blocks = std::max<int64_t>(1, (g.k + kTileDim - 1) / kTileDim);
+    g.splits = wide_tiles(m, n) ? 1 : splits_for(((m + 127) / 128) * ((n + 127) / 128), g.k, m, n);
+    g.k_per_split = (blocks + g.splits - 1) / g.splits * kTileDim;
+    if (g.splits == 1) return exact ? launch_product<kAKR, kBKR, true>(g, e, stream) : launch_product<kAKR, kBKR, false>(g, e, stream);
+    const int64_t pieces = (m + 7) / 8;
+    e.slab = pieces * 8 * n;
+    const StoreEpilogue part{sums, pieces * 8, e.slab, pieces * 8, n, kF32, 0, 1};
+    const int rc = exact ? launch_product<kAKR, kBKR, true>(g, part, stream) : launch_product<kAKR, kBKR, false>(g, part, stream);
+    if (rc) return rc;
+    const dim3 wgs((uint32_t)((n * pieces + kThreads - 1) / kThreads));
+    if (a.out_type == kF32) hipLaunchKernelGGL((join_splits_kernel<float>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);
+    else if (a.out_type == kBF16) hipLaunchKernelGGL((join_splits_kernel<bf16_t>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);
+    else hipLaunchKernelGGL((join_splits_kernel<f16_t>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);
+    return hipGetLastError();
+}
+
+void token_scales(ProductArgs& g, const Codes& c) {
+    g.scales = c.scales;
+    g.scales_ld = c.scales_ld;
+    g.tiles = c.tiles ? kTilesOfN : kEachOfN;
 }
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
@@ -205,83 +253,92 @@ int launch_quantize(const QuantizeArgs& a, void* stream) {
     return a.x_type == kF32 ? quantize<float>(a, s) : a.x_type == kBF16 ? quantize<bf16_t>(a, s) : quantize<f16_t>(a, s);
 }
 
+// The workspace: codes and scales of inputs, the copy of a weight, the sums of
+// splits.
+namespace {
+int64_t codes_bytes(int64_t n, int64_t cols) { return round_up(n * round_up(cols, 16), 256) + round_up((cols + 127) / 128 * n * 4, 256); }
+int64_t copy_bytes(int64_t rows, int64_t cols) { return round_up(rows * round_up(cols, 16), 256); }
+}  // namespace
+
 int64_t linear_work_bytes(int64_t n, int64_t rows, int64_t cols, int copy, int quantize) {
-    return 256 + (quantize ? round_up(n * round_up(cols, 16), 256) + round_up((cols + 127) / 128 * n * 4, 256) : 0);
+    return 4 * kMostSums + (copy ? copy_bytes(rows, cols) : 0) + (quantize ? codes_bytes(n, cols) : 0);
 }
 
 void linear_work_codes(void* work, int64_t n, int64_t cols, uint8_t** codes, int64_t* ld, float** scales) {
     *ld = round_up(cols, 16);
-    *codes = static_cast<uint8_t*>(work);
+    *codes = static_cast<uint8_t*>(work) + 4 * kMostSums;
     *scales = reinterpret_cast<float*>(*codes + round_up(n * *ld, 256));
 }
 
-int launch_linear(const LinearArgs& a, void*, void* stream) {
-    SimpleArgs s{};
-    s.a = a.weight;
-    s.a_m = a.weight_ld;
-    s.a_k = 1;
-    s.b = a.x.p;
-    s.b_n = a.x.ld;
-    s.b_k = 1;
-    s.sa = a.grid;
-    s.sa_m = (a.cols + 127) / 128;
-    s.sa_k = 1;
-    token_scales(s, a.x);
-    s.m = a.rows;
-    s.n = a.n;
-    s.k = a.cols;
-    s.out = a.out;
-    s.out_type = a.out_type;
-    s.out_ld = a.out_ld;
-    s.accumulate = a.accumulate;
-    return simple_product(s, stream);
+namespace {
+
+// The weight as an operand, copied where its rows cannot be read in place.
+int weight_operand(const LinearArgs& a, void* work, bool quantized, hipStream_t stream, Operand* o) {
+    o->p = a.weight;
+    o->ld = a.weight_ld;
+    if (in_place(a.weight, a.weight_ld, a.cols)) return hipSuccess;
+    uint8_t* copy = static_cast<uint8_t*>(work) + 4 * kMostSums + (quantized ? codes_bytes(a.n, a.cols) : 0);
+    o->p = copy;
+    o->ld = round_up(a.cols, 16);
+    const int64_t wgs = std::min<int64_t>((a.rows * (o->ld / 4) + kThreads - 1) / kThreads, 16384);
+    hipLaunchKernelGGL(copy_weight_kernel, dim3((uint32_t)wgs), dim3(kThreads), 0, stream, a.weight, a.weight_ld, a.rows, a.cols, copy, o->ld);
+    return hipGetLastError();
 }
 
-int launch_linear_grad_input(const LinearArgs& a, void*, void* stream) {
-    SimpleArgs s{};
-    s.a = a.weight;
-    s.a_m = 1;
-    s.a_k = a.weight_ld;
-    s.b = a.x.p;
-    s.b_n = a.x.ld;
-    s.b_k = 1;
-    s.sa = a.grid;
-    s.sa_m = 1;
-    s.sa_k = (a.cols + 127) / 128;
-    token_scales(s, a.x);
-    s.m = a.cols;
-    s.n = a.n;
-    s.k = a.rows;
-    s.out = a.out;
-    s.out_type = a.out_type;
-    s.out_ld = a.out_ld;
-    s.accumulate = a.accumulate;
-    return simple_product(s, stream);
+}  // namespace
+
+int launch_linear(const LinearArgs& a, void* work, void* stream) {
+    ProductArgs g{};
+    const bool quantized = a.x.p == static_cast<uint8_t*>(work) + 4 * kMostSums;
+    const int rc = weight_operand(a, work, quantized, (hipStream_t)stream, &g.a);
+    if (rc) return rc;
+    const int64_t wide = (a.cols + kTileDim - 1) / kTileDim;
+    g.a.extent = a.rows;
+    g.a.k = round_up(a.cols, 16);
+    g.b = Operand{a.x.p, a.x.ld, a.n, round_up(a.cols, 16)};
+    g.k = a.cols;
+    g.grid = a.grid;
+    g.grid_m = wide;
+    g.grid_k = 1;
+    g.blocks_m = (a.rows + kTileDim - 1) / kTileDim;
+    g.blocks_k = wide;
+    token_scales(g, a.x);
+    return product<false, false>(g, a, a.rows, a.n, static_cast<float*>(work), (hipStream_t)stream);
 }
 
-int launch_linear_grad_weight(const LinearArgs& a, void*, void* stream) {
-    SimpleArgs s{};
-    s.a = a.other.p;
-    s.a_m = 1;
-    s.a_k = a.other.ld;
-    s.b = a.x.p;
-    s.b_n = 1;
-    s.b_k = a.x.ld;
-    s.sa = a.other.scales;
-    s.sa_m = 1;
-    s.sa_k = a.other.scales_ld;
-    s.sb = a.x.scales;
-    s.sb_n = 1;
-    s.sb_k = a.x.scales_ld;
-    s.sb_shift = 7;
-    s.m = a.cols;
-    s.n = a.rows;
-    s.k = a.n;
-    s.out = a.out;
-    s.out_type = a.out_type;
-    s.out_ld = a.out_ld;
-    s.accumulate = a.accumulate;
-    return simple_product(s, stream);
+int launch_linear_grad_input(const LinearArgs& a, void* work, void* stream) {
+    ProductArgs g{};
+    const int rc = weight_operand(a, work, false, (hipStream_t)stream, &g.a);
+    if (rc) return rc;
+    const int64_t wide = (a.cols + kTileDim - 1) / kTileDim;
+    g.a.extent = a.cols;
+    g.a.k = a.rows;
+    g.b = Operand{a.x.p, a.x.ld, a.n, round_up(a.rows, 16)};
+    g.k = a.rows;
+    g.grid = a.grid;
+    g.grid_m = 1;
+    g.grid_k = wide;
+    g.blocks_m = wide;
+    g.blocks_k = (a.rows + kTileDim - 1) / kTileDim;
+    token_scales(g, a.x);
+    return product<true, false>(g, a, a.cols, a.n, static_cast<float*>(work), (hipStream_t)stream);
+}
+
+int launch_linear_grad_weight(const LinearArgs& a, void* work, void* stream) {
+    ProductArgs g{};
+    g.a = Operand{a.other.p, a.other.ld, a.cols, a.n};
+    g.b = Operand{a.x.p, a.x.ld, a.rows, a.n};
+    g.k = a.n;
+    g.grid = a.other.scales;
+    g.grid_m = 1;
+    g.grid_k = a.other.scales_ld;
+    g.blocks_m = (a.cols + kTileDim - 1) / kTileDim;
+    g.blocks_k = (a.n + kTileDim - 1) / kTileDim;
+    // tokens of D are rows of dweight here, whose tiles' scales lie side by side
+    g.scales = a.x.scales;
+    g.scales_ld = a.x.scales_ld;
+    g.tiles = kTilesOfK;
+    return product<true, true>(g, a, a.cols, a.rows, static_cast<float*>(work), (hipStream_t)stream);
 }
 
 }  // namespace bfz

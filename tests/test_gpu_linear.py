@@ -197,7 +197,8 @@ def test_quantize_strides_and_padding():
 
 
 SIZES = [(1, 1, 1), (1, 128, 128), (2, 16, 2000), (3, 5, 7), (17, 130, 200), (16, 700, 1024), (33, 257, 640), (64, 256, 384), (65, 300, 1001), (129, 1000, 136),
-         (300, 513, 640), (257, 1544, 1001), (520, 768, 2048), (1030, 1300, 912)]
+         (300, 513, 640), (257, 1544, 1001), (520, 768, 2048), (1030, 1300, 912), (3333, 3701, 400),
+         (3590, 1700, 3600)]
 
 
 @pytest.mark.parametrize("n,rows,cols", SIZES)
