@@ -1,4 +1,16 @@
 // Layer norm and its gradient.
+//
+//   h = (x - mean) rstd,  out = h weight + bias,  g = dout weight
+//   dx = rstd (g - mean(g) - h mean(g h)),  dweight = sum dout h,  dbias = sum dout
+//
+// Bound by memory: a row is read once, kept in registers while its sums are made
+// (the variance as the mean of (x - mean)^2, in two steps, so that a large common
+// offset costs nothing), and written once.  A row belongs to 64 to 1024 threads
+// with 8 or 16 (32 beyond 16384 columns) of its elements each; workgroups walk
+// rows, the next row's loads under way while one is summed, and keep weight and
+// bias, and in the gradient their columns' sums for dweight and dbias, in
+// registers.  Those leave as one partial row a workgroup, which a second kernel
+// adds: sums in an order that the sizes fix.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -9,7 +21,7 @@
 namespace bfz {
 namespace {
 
-constexpr int kThreads = 256;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float get_any(const void* p, int type, int64_t i) {
     return type == kF32 ? static_cast<const float*>(p)[i]
@@ -28,89 +40,399 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x;
 }
 
-__device__ __forceinline__ float block_sum(float x, float* lds) {
-    x = wave_sum(x);
+// A thread's elements of a row.  kVec: pieces of 8 side by side, at 16-byte
+// boundaries; else 8 elements kLanes apart, which any alignment can load.  Either
+// way those within the row are the first of a piece.  kWide: an array may hold
+// 4-byte elements.
+template <int kLanes, int kPieces, bool kVec, bool kWide>
+struct Row {
+    static constexpr int kWords = kVec && !kWide ? 4 : 8;
+    struct Raw {
+        uint32_t w[kPieces][kWords];
+    };
+    int lane, count[kPieces];
+    __device__ __forceinline__ Row(int lane, int dim) : lane(lane) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int left = kVec ? dim - (j * kLanes + lane) * 8 : (dim - j * 8 * kLanes - lane + kLanes - 1) / kLanes;
+            count[j] = left < 0 ? 0 : left > 8 ? 8 : left;
+        }
+    }
+    __device__ __forceinline__ int column(int j, int l) const { return kVec ? (j * kLanes + lane) * 8 + l : (j * 8 + l) * kLanes + lane; }
+    // loads only: what is loaded is converted when it is used
+    __device__ __forceinline__ void load(const void* row, int type, Raw& r) const {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            if constexpr (kVec) {
+                if (count[j] == 8) {
+                    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(row) + (int64_t)column(j, 0) * (kWide && type == kF32 ? 4 : 2));
+                    const u32x4 a = *p;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r.w[j][i] = a[i];
+                    if constexpr (kWide) {
+                        if (type == kF32) {
+                            const u32x4 b = p[1];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) r.w[j][4 + i] = b[i];
+                        }
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) r.w[j][i] = 0;
+            }
+#pragma unroll
+            for (int l = 0; l < 8; ++l) {
+                const int c = column(j, l);
+                uint32_t x = 0;
+                if (l < count[j]) {
+                    if (kWide && type == kF32) x = static_cast<const uint32_t*>(row)[c];
+                    else x = static_cast<const uint16_t*>(row)[c];
+                }
+                if constexpr (!kVec) r.w[j][l] = x;
+                else if (kWide && type == kF32) r.w[j][l & (kWords - 1)] = x;
+                else r.w[j][l >> 1] |= x << (16 * (l & 1));
+            }
+        }
+    }
+    __device__ __forceinline__ void values(const Raw& r, int type, float (&x)[kPieces][8]) const {
+        if (kWide && type == kF32) {
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+                for (int l = 0; l < 8; ++l) x[j][l] = __uint_as_float(r.w[j][l & (kWords - 1)]);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+            for (int l = 0; l < 8; ++l) {
+                const uint32_t h = kVec ? r.w[j][l >> 1] >> (16 * (l & 1)) : r.w[j][l];
+                if (type == kBF16) x[j][l] = __uint_as_float(h << 16);
+                else x[j][l] = (float)__builtin_bit_cast(f16_t, (uint16_t)h);
+            }
+    }
+    __device__ __forceinline__ void store(void* row, int type, const float (&x)[kPieces][8]) const {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int c = column(j, 0);
+            if (kVec && count[j] == 8) {
+                if (type == kF32) store8(static_cast<float*>(row) + c, x[j]);
+                else if (type == kBF16) store8(static_cast<bf16_t*>(row) + c, x[j]);
+                else store8(static_cast<f16_t*>(row) + c, x[j]);
+            } else {
+#pragma unroll
+                for (int l = 0; l < 8; ++l)
+                    if (l < count[j]) put_any(row, type, column(j, l), x[j][l]);
+            }
+        }
+    }
+    // elements of a vector of parameters, `none` where there is none, from piece
+    // j0 on
+    template <int kMany>
+    __device__ __forceinline__ void params(const void* p, int type, float none, float (&x)[kMany][8], int j0 = 0) const {
+#pragma unroll
+        for (int j = 0; j < kMany; ++j)
+#pragma unroll
+            for (int l = 0; l < 8; ++l) x[j][l] = p && l < count[j0 + j] ? get_any(p, type, column(j0 + j, l)) : none;
+    }
+};
+
+// Sums over the kLanes threads of a row, the same in all of them; slot: LDS of
+// the row, kLanes / 64 floats for each of the sums.
+template <int kLanes, int kSums>
+__device__ __forceinline__ void row_sums(float (&s)[kSums], float* slot, int lane) {
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) s[k] = wave_sum(s[k]);
+    if constexpr (kLanes > 64) {
+        constexpr int kWaves = kLanes / 64;
+        if ((lane & 63) == 0) {
+#pragma unroll
+            for (int k = 0; k < kSums; ++k) slot[k * kWaves + (lane >> 6)] = s[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) {
+            s[k] = slot[k * kWaves];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) s[k] += slot[k * kWaves + w];
+        }
+    }
+}
+
+__device__ __forceinline__ const char* row_of(const void* p, int type, int64_t r, int64_t ld) {
+    return static_cast<const char*>(p) + r * ld * (type == kF32 ? 4 : 2);
+}
+
+constexpr int most(int a, int b) { return a > b ? a : b; }
+
+template <int kLanes, int kPieces, bool kVec, bool kWide>
+__global__ __launch_bounds__(most(kLanes, 256)) void layer_norm_kernel(LayerNormArgs a) {
+    constexpr int kRows = most(kLanes, 256) / kLanes;
+    __shared__ float lds[2][kRows][kLanes / 64];
+    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    typedef Row<kLanes, kPieces, kVec, kWide> Mine;
+    const Mine row(lane, (int)a.dim);
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    const float scale = 1.0f / (float)a.dim;
+    int64_t r = (int64_t)blockIdx.x * kRows + group;
+    constexpr bool kKeep = kPieces <= 2;  // parameters, and the next row's loads, in registers
+    typename Mine::Raw raw;
+    if constexpr (kKeep) row.load(row_of(a.x, a.x_type, min(r, a.n - 1), a.x_ld), a.x_type, raw);
+    float w[kKeep ? kPieces : 1][8], b[kKeep ? kPieces : 1][8];
+    if constexpr (kKeep) {
+        row.params(a.weight, a.param_type, 1.0f, w);
+        row.params(a.bias, a.param_type, 0.0f, b);
+    }
+    // the same number of turns for all rows of a workgroup, which share barriers
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.n; r0 += step, r += step) {
+        float x[kPieces][8];
+        if constexpr (!kKeep) row.load(row_of(a.x, a.x_type, min(r, a.n - 1), a.x_ld), a.x_type, raw);
+        row.values(raw, a.x_type, x);
+        if constexpr (kKeep) {
+            if (r0 + step < a.n) row.load(row_of(a.x, a.x_type, min(r + step, a.n - 1), a.x_ld), a.x_type, raw);
+        }
+        float sum[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+            for (int l = 0; l < 8; ++l) sum[0] += x[j][l];
+        row_sums<kLanes>(sum, lds[0][group], lane);
+        const float mean = sum[0] * scale;
+        float square[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+            for (int l = 0; l < 8; ++l) {
+                x[j][l] -= mean;
+                square[0] = __builtin_fmaf(l < row.count[j] ? x[j][l] : 0.0f, x[j][l], square[0]);
+            }
+        row_sums<kLanes>(square, lds[1][group], lane);
+        const float rstd = 1.0f / sqrtf(__builtin_fmaf(square[0], scale, a.eps));
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            if constexpr (!kKeep) {
+                row.params(a.weight, a.param_type, 1.0f, w, j);
+                row.params(a.bias, a.param_type, 0.0f, b, j);
+            }
+#pragma unroll
+            for (int l = 0; l < 8; ++l) x[j][l] = __builtin_fmaf(x[j][l] * rstd, w[kKeep ? j : 0][l], b[kKeep ? j : 0][l]);
+        }
+        if (r < a.n) {
+            row.store(const_cast<char*>(row_of(a.out, a.out_type, r, a.out_ld)), a.out_type, x);
+            if (lane == 0) {
+                if (a.mean) a.mean[r] = mean;
+                if (a.rstd) a.rstd[r] = rstd;
+            }
+        }
+    }
+}
+
+// Threads of a workgroup of the gradient: as many rows at a time as fit, so that
+// few partial rows leave.
+constexpr int kGradThreads = 1024;
+
+template <int kLanes, int kPieces, bool kVec, bool kWide>
+__global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(LayerNormGradArgs a, float* partial) {
+    constexpr int kRows = kGradThreads / kLanes, kWaves = kLanes / 64;
+    constexpr bool kAhead = kPieces == 1 || (kPieces == 2 && !kWide);  // the next row's loads under way: where registers allow
+    __shared__ float lds[2][kRows][2 * kWaves];
+    __shared__ float sums[kLanes][8];
+    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    typedef Row<kLanes, kPieces, kVec, kWide> Mine;
+    const Mine row(lane, (int)a.dim);
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    const float scale = 1.0f / (float)a.dim;
+    int64_t r = (int64_t)blockIdx.x * kRows + group;
+    typename Mine::Raw raw_x, raw_d;
+    float mean = 0.0f, rstd = 0.0f;
+    auto load = [&](int64_t at) {
+        at = min(at, a.n - 1);
+        row.load(row_of(a.x, a.x_type, at, a.x_ld), a.x_type, raw_x);
+        row.load(row_of(a.dout, a.dout_type, at, a.dout_ld), a.dout_type, raw_d);
+        mean = a.mean[at];
+        rstd = a.rstd[at];
+    };
+    constexpr bool kKeep = kPieces <= 2;
+    float dw[kPieces][8] = {}, db[kPieces][8] = {}, w[kKeep ? kPieces : 1][8];
+    if constexpr (kAhead) {
+        if ((int64_t)blockIdx.x * kRows < a.n) load(r);
+    }
+    if constexpr (kKeep) row.params(a.weight, a.param_type, 1.0f, w);
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.n; r0 += step, r += step, turn ^= 1) {
+        if constexpr (!kAhead) load(r);
+        float h[kPieces][8], d[kPieces][8];
+        const float m = mean, q = rstd;
+        row.values(raw_x, a.x_type, h);
+        row.values(raw_d, a.dout_type, d);
+        if constexpr (kAhead) {
+            if (r0 + step < a.n) load(r + step);
+        }
+        const bool there = r < a.n;
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            if constexpr (!kKeep) row.params(a.weight, a.param_type, 1.0f, w, j);
+#pragma unroll
+            for (int l = 0; l < 8; ++l) {
+                // beyond the row's end d is zero; h there does not count (0 times it
+                // may be NaN)
+                h[j][l] = l < row.count[j] ? (h[j][l] - m) * q : 0.0f;
+                const float g = d[j][l] * w[kKeep ? j : 0][l];
+                s[0] += g;
+                s[1] = __builtin_fmaf(g, h[j][l], s[1]);
+                if (there) {
+                    dw[j][l] = __builtin_fmaf(d[j][l], h[j][l], dw[j][l]);
+                    db[j][l] += d[j][l];
+                }
+            }
+        }
+        if (a.dx) {
+            row_sums<kLanes>(s, lds[turn][group], lane);
+            const float m1 = s[0] * scale, m2 = s[1] * scale;
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                if constexpr (!kKeep) row.params(a.weight, a.param_type, 1.0f, w, j);
+#pragma unroll
+                for (int l = 0; l < 8; ++l) d[j][l] = q * (__builtin_fmaf(d[j][l], w[kKeep ? j : 0][l], -m1) - h[j][l] * m2);
+            }
+            if (there) row.store(const_cast<char*>(row_of(a.dx, a.dx_type, r, a.dx_ld)), a.dx_type, d);
+        }
+    }
+    if (!partial) return;
+    // the workgroup's rows added, in their order
+    float* out = partial + (int64_t)blockIdx.x * 2 * a.dim;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            float(&x)[8] = k ? db[j] : dw[j];
+            if constexpr (kRows > 1) {
+                for (int g = 1; g < kRows; ++g) {
+                    __syncthreads();
+                    if (group == g) {
+#pragma unroll
+                        for (int l = 0; l < 8; ++l) sums[lane][l] = x[l];
+                    }
+                    __syncthreads();
+                    if (group == 0) {
+#pragma unroll
+                        for (int l = 0; l < 8; ++l) x[l] += sums[lane][l];
+                    }
+                }
+            }
+            if (group == 0) {
+#pragma unroll
+                for (int l = 0; l < 8; ++l)
+                    if (l < row.count[j]) out[k * a.dim + row.column(j, l)] = x[l];
+            }
+        }
+}
+
+// dweight and dbias from the workgroups' partial rows: 32 columns a workgroup, 8
+// threads to a column.
+constexpr int kJoinColumns = 32, kJoinSlices = 8;
+__global__ __launch_bounds__(kJoinColumns* kJoinSlices) void join_params_kernel(const float* __restrict__ partial, int64_t rows, LayerNormGradArgs a) {
+    __shared__ float lds[kJoinSlices][kJoinColumns];
+    const int x = threadIdx.x % kJoinColumns, y = threadIdx.x / kJoinColumns;
+    const int64_t c = (int64_t)blockIdx.x * kJoinColumns + x;
+    float sum = 0.0f;
+    if (c < 2 * a.dim) {
+        int64_t r = y;
+        for (; r + 7 * kJoinSlices < rows; r += 8 * kJoinSlices) {
+            float p[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) p[u] = partial[(r + u * kJoinSlices) * 2 * a.dim + c];
+            sum += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+        }
+        for (; r < rows; r += kJoinSlices) sum += partial[r * 2 * a.dim + c];
+    }
+    lds[y][x] = sum;
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    if (y != 0 || c >= 2 * a.dim) return;
+#pragma unroll
+    for (int k = 1; k < kJoinSlices; ++k) sum += lds[k][x];
+    void* out = c < a.dim ? a.dweight : a.dbias;
+    const int64_t at = c < a.dim ? c : c - a.dim;
+    if (out) put_any(out, a.dparam_type, at, a.accumulate ? get_any(out, a.dparam_type, at) + sum : sum);
 }
 
-__global__ __launch_bounds__(kThreads) void layer_norm_kernel(LayerNormArgs a) {
-    __shared__ float lds[4];
-    for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
-        float sum = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.dim; c += kThreads) sum += get_any(a.x, a.x_type, r * a.x_ld + c);
-        const float mean = block_sum(sum, lds) / (float)a.dim;
-        float square = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.dim; c += kThreads) {
-            const float d = get_any(a.x, a.x_type, r * a.x_ld + c) - mean;
-            square += d * d;
-        }
-        const float rstd = 1.0f / sqrtf(block_sum(square, lds) / (float)a.dim + a.eps);
-        for (int64_t c = threadIdx.x; c < a.dim; c += kThreads) {
-            const float h = (get_any(a.x, a.x_type, r * a.x_ld + c) - mean) * rstd;
-            const float w = a.weight ? get_any(a.weight, a.param_type, c) : 1.0f;
-            const float b = a.bias ? get_any(a.bias, a.param_type, c) : 0.0f;
-            put_any(a.out, a.out_type, r * a.out_ld + c, __builtin_fmaf(h, w, b));
-        }
-        if (threadIdx.x == 0) {
-            if (a.mean) a.mean[r] = mean;
-            if (a.rstd) a.rstd[r] = rstd;
-        }
-    }
+// ---- host -------------------------------------------------------------------------
+
+bool aligned16(const void* p, int64_t ld, int type) {
+    return ((reinterpret_cast<uintptr_t>(p) | (uint64_t)(ld * dtype_size(type))) & 15u) == 0;
 }
 
-__global__ __launch_bounds__(kThreads) void layer_norm_dx_kernel(LayerNormGradArgs a) {
-    __shared__ float lds[4];
-    for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
-        const float mean = a.mean[r], rstd = a.rstd[r];
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.dim; c += kThreads) {
-            const float h = (get_any(a.x, a.x_type, r * a.x_ld + c) - mean) * rstd;
-            const float g = get_any(a.dout, a.dout_type, r * a.dout_ld + c) * (a.weight ? get_any(a.weight, a.param_type, c) : 1.0f);
-            s1 += g;
-            s2 += g * h;
-        }
-        s1 = block_sum(s1, lds) / (float)a.dim;
-        s2 = block_sum(s2, lds) / (float)a.dim;
-        for (int64_t c = threadIdx.x; c < a.dim; c += kThreads) {
-            const float h = (get_any(a.x, a.x_type, r * a.x_ld + c) - mean) * rstd;
-            const float g = get_any(a.dout, a.dout_type, r * a.dout_ld + c) * (a.weight ? get_any(a.weight, a.param_type, c) : 1.0f);
-            put_any(a.dx, a.dx_type, r * a.dx_ld + c, rstd * (g - s1 - h * s2));
-        }
-    }
+// Calls f(threads of a row, pieces of 8 elements a thread) with the first of
+// these that hold dim columns.
+template <class F>
+int with_shape(int64_t dim, F&& f) {
+    using std::integral_constant;
+    if (dim <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if (dim <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    if (dim <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    if (dim <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    if (dim <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    if (dim <= 16384) return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
-// A thread a column.
-__global__ __launch_bounds__(64) void layer_norm_dw_kernel(LayerNormGradArgs a) {
-    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (c >= a.dim) return;
-    float dw = 0.0f, db = 0.0f;
-    for (int64_t r = 0; r < a.n; ++r) {
-        const float d = get_any(a.dout, a.dout_type, r * a.dout_ld + c);
-        dw += d * ((get_any(a.x, a.x_type, r * a.x_ld + c) - a.mean[r]) * a.rstd[r]);
-        db += d;
-    }
-    if (a.dweight) put_any(a.dweight, a.dparam_type, c, a.accumulate ? get_any(a.dweight, a.dparam_type, c) + dw : dw);
-    if (a.dbias) put_any(a.dbias, a.dparam_type, c, a.accumulate ? get_any(a.dbias, a.dparam_type, c) + db : db);
+template <class F>
+int with_flags(bool vec, bool wide, F&& f) {
+    using std::bool_constant;
+    if (vec) return wide ? f(bool_constant<true>{}, bool_constant<true>{}) : f(bool_constant<true>{}, bool_constant<false>{});
+    return wide ? f(bool_constant<false>{}, bool_constant<true>{}) : f(bool_constant<false>{}, bool_constant<false>{});
 }
+
+// Workgroups of the gradient: one a CU, or one for every two rows of each
+// thread group where there are fewer.
+constexpr int64_t kGradWgs = 256;
+int64_t grad_wgs(int64_t n, int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(kGradWgs, (n + rows - 1) / rows)); }
 
 }  // namespace
 
 int launch_layer_norm(const LayerNormArgs& a, void* stream) {
-    hipLaunchKernelGGL(layer_norm_kernel, dim3((uint32_t)std::min<int64_t>(a.n, 65536)), dim3(kThreads), 0, (hipStream_t)stream, a);
-    return hipGetLastError();
+    const bool vec = aligned16(a.x, a.x_ld, a.x_type) && aligned16(a.out, a.out_ld, a.out_type);
+    return with_shape(a.dim, [&](auto lanes, auto pieces) {
+        return with_flags(vec, a.x_type == kF32, [&](auto v, auto wide) {
+            constexpr int kLanes = decltype(lanes)::value, kPieces = decltype(pieces)::value, kThreads = most(kLanes, 256);
+            constexpr int64_t kRows = kThreads / kLanes;
+            const int64_t wgs = std::min<int64_t>((a.n + kRows - 1) / kRows, 256 * 2048 / kThreads);
+            hipLaunchKernelGGL((layer_norm_kernel<kLanes, kPieces, decltype(v)::value, decltype(wide)::value>), dim3((uint32_t)wgs),
+                               dim3(kThreads), 0, (hipStream_t)stream, a);
+            return (int)hipGetLastError();
+        });
+    });
 }
 
-int64_t layer_norm_work_bytes(int64_t, int64_t) { return 256; }
+int64_t layer_norm_work_bytes(int64_t n, int64_t dim) {
+    int64_t wgs = 0;
+    with_shape(dim, [&](auto lanes, auto) {
+        wgs = grad_wgs(n, kGradThreads / decltype(lanes)::value);
+        return 0;
+    });
+    return wgs * 2 * dim * 4;
+}
 
-int launch_layer_norm_grad(const LayerNormGradArgs& a, void*, void* stream) {
-    // the columns first: dx may be dout itself
-    if (a.dweight || a.dbias)
-        hipLaunchKernelGGL(layer_norm_dw_kernel, dim3((uint32_t)((a.dim + 63) / 64)), dim3(64), 0, (hipStream_t)stream, a);
-    if (a.dx && a.n > 0)
-        hipLaunchKernelGGL(layer_norm_dx_kernel, dim3((uint32_t)std::min<int64_t>(a.n, 65536)), dim3(kThreads), 0, (hipStream_t)stream, a);
+int launch_layer_norm_grad(const LayerNormGradArgs& a, void* work, void* stream) {
+    const bool vec = aligned16(a.x, a.x_ld, a.x_type) && aligned16(a.dout, a.dout_ld, a.dout_type) &&
+                     (!a.dx || aligned16(a.dx, a.dx_ld, a.dx_type));
+    float* partial = a.dweight || a.dbias ? static_cast<float*>(work) : nullptr;
+    if (!partial && !a.dx) return hipSuccess;
+    int64_t wgs = 0;
+    const int rc = with_shape(a.dim, [&](auto lanes, auto pieces) {
+        return with_flags(vec, a.x_type == kF32 || a.dout_type == kF32, [&](auto v, auto wide) {
+            constexpr int kLanes = decltype(lanes)::value, kPieces = decltype(pieces)::value;
+            wgs = grad_wgs(a.n, kGradThreads / kLanes);
+            hipLaunchKernelGGL((layer_norm_grad_kernel<kLanes, kPieces, decltype(v)::value, decltype(wide)::value>), dim3((uint32_t)wgs),
+                               dim3(kGradThreads), 0, (hipStream_t)stream, a, partial);
+            return (int)hipGetLastError();
+        });
+    });
+    if (rc || !partial) return rc;
+    hipLaunchKernelGGL(join_params_kernel, dim3((uint32_t)((2 * a.dim + kJoinColumns - 1) / kJoinColumns)), dim3(kJoinColumns * kJoinSlices), 0,
+                       (hipStream_t)stream, partial, wgs, a);
     return hipGetLastError();
 }
 
