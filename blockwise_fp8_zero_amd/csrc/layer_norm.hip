@@ -132,9 +132,17 @@ struct Row {
     template <int kMany>
     __device__ __forceinline__ void params(const void* p, int type, float none, float (&x)[kMany][8], int j0 = 0) const {
 #pragma unroll
-        for (int j = 0; j < kMany; ++j)
+        for (int j = 0; j < kMany; ++j) {
+            const int c = column(j0 + j, 0);
+            if (kVec && p && count[j0 + j] == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+                if (type == kF32) load8(static_cast<const float*>(p) + c, x[j]);
+                else if (type == kBF16) load8(static_cast<const bf16_t*>(p) + c, x[j]);
+                else load8(static_cast<const f16_t*>(p) + c, x[j]);
+                continue;
+            }
 #pragma unroll
             for (int l = 0; l < 8; ++l) x[j][l] = p && l < count[j0 + j] ? get_any(p, type, column(j0 + j, l)) : none;
+        }
     }
 };
 
@@ -228,6 +236,12 @@ __global__ __launch_bounds__(most(kLanes, 256)) void layer_norm_kernel(LayerNorm
     }
 }
 
+// dweight (k = 0) or dbias of column c.
+__device__ __forceinline__ void put_param(const LayerNormGradArgs& a, int k, int64_t c, float sum) {
+    void* out = k ? a.dbias : a.dweight;
+    if (out) put_any(out, a.dparam_type, c, a.accumulate ? get_any(out, a.dparam_type, c) + sum : sum);
+}
+
 // Threads of a workgroup of the gradient: as many rows at a time as fit, so that
 // few partial rows leave.
 constexpr int kGradThreads = 1024;
@@ -237,7 +251,7 @@ __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(LayerNorm
     constexpr int kRows = kGradThreads / kLanes, kWaves = kLanes / 64;
     constexpr bool kAhead = kPieces == 1 || (kPieces == 2 && !kWide);  // the next row's loads under way: where registers allow
     __shared__ float lds[2][kRows][2 * kWaves];
-    __shared__ float sums[kLanes][8];
+    __shared__ float sums[kRows][8][kLanes];
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
     typedef Row<kLanes, kPieces, kVec, kWide> Mine;
     const Mine row(lane, (int)a.dim);
@@ -300,32 +314,27 @@ __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(LayerNorm
             if (there) row.store(const_cast<char*>(row_of(a.dx, a.dx_type, r, a.dx_ld)), a.dx_type, d);
         }
     }
-    if (!partial) return;
-    // the workgroup's rows added, in their order
-    float* out = partial + (int64_t)blockIdx.x * 2 * a.dim;
+    if (!a.dweight && !a.dbias) return;
+    // the workgroup's rows added, in their order, 8 columns of each thread at a time
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            float(&x)[8] = k ? db[j] : dw[j];
-            if constexpr (kRows > 1) {
-                for (int g = 1; g < kRows; ++g) {
-                    __syncthreads();
-                    if (group == g) {
+            const float(&x)[8] = k ? db[j] : dw[j];
+            __syncthreads();
 #pragma unroll
-                        for (int l = 0; l < 8; ++l) sums[lane][l] = x[l];
-                    }
-                    __syncthreads();
-                    if (group == 0) {
+            for (int l = 0; l < 8; ++l) sums[group][l][lane] = x[l];
+            __syncthreads();
+            for (int i = threadIdx.x; i < 8 * kLanes; i += kGradThreads) {
+                // neighbours write side by side where a thread's columns do
+                const int of = kVec ? i >> 3 : i % kLanes, l = kVec ? i & 7 : i / kLanes;
+                float sum = 0.0f;
 #pragma unroll
-                        for (int l = 0; l < 8; ++l) x[l] += sums[lane][l];
-                    }
-                }
-            }
-            if (group == 0) {
-#pragma unroll
-                for (int l = 0; l < 8; ++l)
-                    if (l < row.count[j]) out[k * a.dim + row.column(j, l)] = x[l];
+                for (int g = 0; g < kRows; ++g) sum += sums[g][l][of];
+                const int64_t c = kVec ? (j * kLanes + of) * 8 + l : (j * 8 + l) * kLanes + of;
+                if (c >= a.dim) continue;
+                if (gridDim.x == 1) put_param(a, k, c, sum);
+                else partial[(int64_t)blockIdx.x * 2 * a.dim + k * a.dim + c] = sum;
             }
         }
 }
@@ -353,9 +362,7 @@ __global__ __launch_bounds__(kJoinColumns* kJoinSlices) void join_params_kernel(
     if (y != 0 || c >= 2 * a.dim) return;
 #pragma unroll
     for (int k = 1; k < kJoinSlices; ++k) sum += lds[k][x];
-    void* out = c < a.dim ? a.dweight : a.dbias;
-    const int64_t at = c < a.dim ? c : c - a.dim;
-    if (out) put_any(out, a.dparam_type, at, a.accumulate ? get_any(out, a.dparam_type, at) + sum : sum);
+    put_param(a, c >= a.dim, c < a.dim ? c : c - a.dim, sum);
 }
 
 // ---- host -------------------------------------------------------------------------
@@ -374,6 +381,19 @@ int with_shape(int64_t dim, F&& f) {
     if (dim <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     if (dim <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
     if (dim <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    if (dim <= 16384) return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+}
+
+// The same for the gradient, which has 16 waves' registers for twice the arrays.
+template <class F>
+int with_grad_shape(int64_t dim, F&& f) {
+    using std::integral_constant;
+    if (dim <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if (dim <= 1024) return f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+    if (dim <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    if (dim <= 4096) return f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
+    if (dim <= 8192) return f(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
     if (dim <= 16384) return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
     return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
@@ -408,7 +428,7 @@ int launch_layer_norm(const LayerNormArgs& a, void* stream) {
 
 int64_t layer_norm_work_bytes(int64_t n, int64_t dim) {
     int64_t wgs = 0;
-    with_shape(dim, [&](auto lanes, auto) {
+    with_grad_shape(dim, [&](auto lanes, auto) {
         wgs = grad_wgs(n, kGradThreads / decltype(lanes)::value);
         return 0;
     });
@@ -421,7 +441,7 @@ int launch_layer_norm_grad(const LayerNormGradArgs& a, void* work, void* stream)
     float* partial = a.dweight || a.dbias ? static_cast<float*>(work) : nullptr;
     if (!partial && !a.dx) return hipSuccess;
     int64_t wgs = 0;
-    const int rc = with_shape(a.dim, [&](auto lanes, auto pieces) {
+    const int rc = with_grad_shape(a.dim, [&](auto lanes, auto pieces) {
         return with_flags(vec, a.x_type == kF32 || a.dout_type == kF32, [&](auto v, auto wide) {
             constexpr int kLanes = decltype(lanes)::value, kPieces = decltype(pieces)::value;
             wgs = grad_wgs(a.n, kGradThreads / kLanes);
@@ -430,7 +450,7 @@ int launch_layer_norm_grad(const LayerNormGradArgs& a, void* work, void* stream)
             return (int)hipGetLastError();
         });
     });
-    if (rc || !partial) return rc;
+    if (rc || !partial || wgs == 1) return rc;
     hipLaunchKernelGGL(join_params_kernel, dim3((uint32_t)((2 * a.dim + kJoinColumns - 1) / kJoinColumns)), dim3(kJoinColumns * kJoinSlices), 0,
                        (hipStream_t)stream, partial, wgs, a);
     return hipGetLastError();
