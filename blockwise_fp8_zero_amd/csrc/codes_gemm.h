@@ -182,25 +182,31 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
     const uint32_t lds_a = lds + wave * 1024, lds_b = lds_a + A::kBytes;
     constexpr int kWaves = kWavesM * kWavesN;
 
-    // Loads of the next block into buffer `stage`; past the end of k they give
-    // zero (no branch: the lanes' offsets are selected).
-    int64_t left_a = g.a.k - k0, left_b = g.b.k - k0;
-    auto issue = [&](uint32_t stage) {
+    // Loads of the next block into buffer `stage`, `parts` calls of which part p
+    // issues its share; past the end of k they give zero (no branch: the lanes'
+    // offsets are selected).
+    int left_a = (int)(g.a.k - k0), left_b = (int)(g.b.k - k0);
+    constexpr int kLoads = A::kLoads + B::kLoads;
+    auto issue = [&](uint32_t stage, auto part, auto of) {
+        constexpr int p = decltype(part)::value, parts = decltype(of)::value;
+        constexpr int from = p * kLoads / parts, to = (p + 1) * kLoads / parts;
         const i32x4 ra = buffer_of(base_a), rb = buffer_of(base_b);
-        const int la = (int)max((int64_t)0, min(left_a, (int64_t)kTileDim)), lb = (int)max((int64_t)0, min(left_b, (int64_t)kTileDim));
-        each<A::kLoads>([&](auto i) {
-            constexpr int j = decltype(i)::value;
-            load_to_lds(ra, A::k_of(j, wave, lane) < la ? off_a[j] : kNowhere, lds_a + stage + j * (kWaves * 1024));
+        each<to - from>([&](auto i) {
+            constexpr int j = from + decltype(i)::value;
+            if constexpr (j < A::kLoads)
+                load_to_lds(ra, A::k_of(j, wave, lane) < left_a ? off_a[j] : kNowhere, lds_a + stage + j * (kWaves * 1024));
+            else
+                load_to_lds(rb, B::k_of(j - A::kLoads, wave, lane) < left_b ? off_b[j - A::kLoads] : kNowhere,
+                            lds_b + stage + (j - A::kLoads) * (kWaves * 1024));
         });
-        each<B::kLoads>([&](auto i) {
-            constexpr int j = decltype(i)::value;
-            load_to_lds(rb, B::k_of(j, wave, lane) < lb ? off_b[j] : kNowhere, lds_b + stage + j * (kWaves * 1024));
-        });
+        if constexpr (p + 1 < parts) return;
         base_a += adv_a;
         base_b += adv_b;
         left_a -= kTileDim;
         left_b -= kTileDim;
     };
+    constexpr std::integral_constant<int, 0> kNone{};
+    constexpr std::integral_constant<int, 1> kOnce{};
 
     // scales of this wave's rows and of the lane's tokens in a block, beyond the
     // edges those of the last
@@ -242,8 +248,8 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
     if (steps > 0) {
         load_scales(true);
         take_scales();
-        issue(0);
-        issue(kOther);
+        issue(0, kNone, kOnce);
+        issue(kOther, kNone, kOnce);
         __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(A::kLoads + B::kLoads) : "memory");
         __builtin_amdgcn_s_barrier();
         i32x8 a[2], raw[kTN];
@@ -267,29 +273,32 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
             load_scales(s + 1 < steps);
             each<kTM>([&](auto row) {
                 constexpr int t = decltype(row)::value;
-                if constexpr (t == kTM - 1) {
+                constexpr bool kLast = t == kTM - 1;
+                const uint32_t done = cur;
+                if constexpr (kLast) {
                     // every fragment of this block is read; the next block has arrived
                     wait_loads();
                     __builtin_amdgcn_s_barrier();
                     __builtin_amdgcn_sched_barrier(0);
                     take_scales();
-                    issue(cur);
                     cur = kOther - cur;
-                    a[(t + 1) & 1] = fa.read(cur, 0);
-                } else {
-                    a[(t + 1) & 1] = fa.read(cur, t + 1);
                 }
+                a[(t + 1) & 1] = fa.read(cur, kLast ? 0 : t + 1);
+                __builtin_amdgcn_sched_barrier(0);
                 const typename Mul::Value av = Mul::value(a[t & 1]);
                 each<kTN>([&](auto col) {
                     constexpr int u = decltype(col)::value;
                     if constexpr (t == 0) b[u] = Mul::value(raw[u]);
                     const f32x4 p = Mul::run(av, b[u]);
-                    if constexpr (t == kTM - 1) raw[u] = fb.read(cur, u);
+                    if constexpr (kLast) {
+                        raw[u] = fb.read(cur, u);
+                        issue(done, col, std::integral_constant<int, kTN>{});
+                    }
                     scale_row(std::integral_constant<int, (t + kTM - 1) % kTM>{}, col);
                     part[u] = p;
                     if constexpr (t == 0) by[u] = now[u];
+                    __builtin_amdgcn_sched_barrier(0);
                 });
-                __builtin_amdgcn_sched_barrier(0);
             });
         }
         each<kTN>([&](auto col) { scale_row(std::integral_constant<int, kTM - 1>{}, col); });
