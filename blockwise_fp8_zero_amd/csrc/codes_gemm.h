@@ -120,34 +120,29 @@ struct CodesKR {
 
 // ---- the kernel -----------------------------------------------------------------
 
+// A fragment's values in kParts parts, whose products add up to the block's.
 template <bool kExact>
 struct Multiply;
 
 template <>
 struct Multiply<false> {
+    static constexpr int kParts = 1;
     typedef i32x8 Value;
-    __device__ __forceinline__ static Value value(const i32x8& f) { return f; }
-    __device__ __forceinline__ static f32x4 run(const Value& a, const Value& b) {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+    __device__ __forceinline__ static Value value(const i32x8& f, int) { return f; }
+    __device__ __forceinline__ static f32x4 run(const Value& a, const Value& b, const f32x4& c) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
     }
 };
 
 template <>
 struct Multiply<true> {
-    struct Value {
-        bf16x8 v[4];
-    };
-    __device__ __forceinline__ static Value value(const i32x8& f) {
-        Value r;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r.v[j] = codes_to_bf16(u32x2{(uint32_t)f[2 * j], (uint32_t)f[2 * j + 1]}, 1.0f);
-        return r;
+    static constexpr int kParts = 4;
+    typedef bf16x8 Value;
+    __device__ __forceinline__ static Value value(const i32x8& f, int j) {
+        return codes_to_bf16(u32x2{(uint32_t)f[2 * j], (uint32_t)f[2 * j + 1]}, 1.0f);
     }
-    __device__ __forceinline__ static f32x4 run(const Value& a, const Value& b) {
-        f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[j], b.v[j], r, 0, 0, 0);
-        return r;
+    __device__ __forceinline__ static f32x4 run(const Value& a, const Value& b, const f32x4& c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
 };
 
@@ -252,12 +247,19 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
         issue(kOther, kNone, kOnce);
         __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(A::kLoads + B::kLoads) : "memory");
         __builtin_amdgcn_s_barrier();
+        constexpr int kParts = Mul::kParts;
+        // Rows of A are read kAhead rows before their use: two where they are converted
+        // during the row before.
+        constexpr int kAhead = kExact ? 2 : 1;
         i32x8 a[2], raw[kTN];
-        typename Mul::Value b[kTN];
+        typename Mul::Value av[kParts], b[kTN][kParts];
         f32x4 part[kTN];
         a[0] = fa.read(0, 0);
+        if constexpr (kAhead == 2) a[1] = fa.read(0, 1);
 #pragma unroll
         for (int u = 0; u < kTN; ++u) raw[u] = fb.read(0, u);
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) av[j] = Mul::value(a[0], j);
         auto scale_row = [&](auto row, auto col) {
             constexpr int t = decltype(row)::value, u = decltype(col)::value;
 #pragma unroll
@@ -283,22 +285,37 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
                     take_scales();
                     cur = kOther - cur;
                 }
-                a[(t + 1) & 1] = fa.read(cur, kLast ? 0 : t + 1);
+                if constexpr (kAhead == 1) {
+                    a[(t + 1) & 1] = fa.read(cur, kLast ? 0 : t + 1);
+                } else if constexpr (kLast) {
+                    a[(t + 1) & 1] = fa.read(cur, 0);
+                    a[t & 1] = fa.read(cur, 1);
+                } else if constexpr (t + 2 < kTM) {
+                    a[t & 1] = fa.read(cur, t + 2);
+                }
                 __builtin_amdgcn_sched_barrier(0);
-                const typename Mul::Value av = Mul::value(a[t & 1]);
-                each<kTN>([&](auto col) {
-                    constexpr int u = decltype(col)::value;
-                    if constexpr (t == 0) b[u] = Mul::value(raw[u]);
-                    const f32x4 p = Mul::run(av, b[u]);
-                    if constexpr (kLast) {
-                        raw[u] = fb.read(cur, u);
-                        issue(done, col, std::integral_constant<int, kTN>{});
+                f32x4 p[kTN];
+                each<kParts * kTN>([&](auto both) {
+                    constexpr int j = decltype(both)::value / kTN, u = decltype(both)::value % kTN;
+                    constexpr std::integral_constant<int, u> col{};
+                    if constexpr (t == 0) b[u][j] = Mul::value(raw[u], j);
+                    p[u] = Mul::run(av[j], b[u][j], j == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p[u]);
+                    if constexpr (kLast && j == kParts - 1) raw[u] = fb.read(cur, u);
+                    if constexpr (kLast && j == 0) issue(done, col, std::integral_constant<int, kTN>{});
+                    if constexpr (j == 0) {
+                        scale_row(std::integral_constant<int, (t + kTM - 1) % kTM>{}, col);
+                        if constexpr (t == 0) by[u] = now[u];
                     }
-                    scale_row(std::integral_constant<int, (t + kTM - 1) % kTM>{}, col);
-                    part[u] = p;
-                    if constexpr (t == 0) by[u] = now[u];
+                    // the next row's values, a part at a time, once this row's are used
+                    if constexpr (u == kTN - 1 && !(kLast && kAhead == 2)) av[j] = Mul::value(a[(t + 1) & 1], j);
                     __builtin_amdgcn_sched_barrier(0);
                 });
+                if constexpr (kLast && kAhead == 2) {
+#pragma unroll
+                    for (int j = 0; j < kParts; ++j) av[j] = Mul::value(a[(t + 1) & 1], j);
+                }
+#pragma unroll
+                for (int u = 0; u < kTN; ++u) part[u] = p[u];
             });
         }
         each<kTN>([&](auto col) { scale_row(std::integral_constant<int, kTM - 1>{}, col); });
