@@ -243,9 +243,14 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
     if (steps > 0) {
         load_scales(true);
         take_scales();
+        // A block's loads go out over kSpread rows of tiles, from the last row of the
+        // block before on: all at once they fill the queue, and a wave that waits
+        // there cannot multiply.
+        constexpr int kSpread = kTM / 2;
+        constexpr std::integral_constant<int, kSpread> kParted{};
         issue(0, kNone, kOnce);
-        issue(kOther, kNone, kOnce);
-        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(A::kLoads + B::kLoads) : "memory");
+        issue(kOther, kNone, kParted);
+        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads / kSpread) : "memory");
         __builtin_amdgcn_s_barrier();
         constexpr int kParts = Mul::kParts;
         // Rows of A are read kAhead rows before their use: two where they are converted
@@ -276,7 +281,6 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
             each<kTM>([&](auto row) {
                 constexpr int t = decltype(row)::value;
                 constexpr bool kLast = t == kTM - 1;
-                const uint32_t done = cur;
                 if constexpr (kLast) {
                     // every fragment of this block is read; the next block has arrived
                     wait_loads();
@@ -301,7 +305,8 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
                     if constexpr (t == 0) b[u][j] = Mul::value(raw[u], j);
                     p[u] = Mul::run(av[j], b[u][j], j == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p[u]);
                     if constexpr (kLast && j == kParts - 1) raw[u] = fb.read(cur, u);
-                    if constexpr (kLast && j == 0) issue(done, col, std::integral_constant<int, kTN>{});
+                    if constexpr (j == 0 && u == 1 && kLast) issue(kOther - cur, kNone, kParted);
+                    if constexpr (j == 0 && u == 1 && t + 1 < kSpread) issue(kOther - cur, std::integral_constant<int, t + 1>{}, kParted);
                     if constexpr (j == 0) {
                         scale_row(std::integral_constant<int, (t + kTM - 1) % kTM>{}, col);
                         if constexpr (t == 0) by[u] = now[u];
