@@ -29,6 +29,8 @@
 // sums are binary32, at half the rate.
 #pragma once
 
+#include <type_traits>
+
 #include "vocab_gemm.h"
 
 namespace bfz {
@@ -43,6 +45,7 @@ struct ProductArgs : GemmArgs {  // grid: scale of (m / 128, k / 128) at grid_m,
     const float* scales;
     int64_t scales_ld;
     int32_t tiles;
+    int32_t half_tiles_n;  // columns of tiles half as wide, after the tiles_n others
 };
 
 // ---- operand layouts ----------------------------------------------------------
@@ -79,13 +82,13 @@ struct CodesKR {
     static constexpr int kBytes = kRows * 128;
     static constexpr int kLoads = kBytes / 1024 / kWaves;
     static_assert(kLoads >= 1 && kBytes % (1024 * kWaves) == 0, "whole loads for each wave");
-    static_assert(kRows == 256 || kRows == 128, "the permutation spans 256 bytes");
+    static_assert(kRows == 256 || kRows == 128 || kRows == 64, "the permutation spans 256 bytes");
     static constexpr int kPieces = kRows / 16, kRowsOfLoad = 64 / kPieces;
     uint32_t at[kTiles];
     // by which a row's pieces are permuted: 8 rows that one transpose reads, of
     // two lane groups, fall on 16 different pieces of 256 bytes
     __device__ __forceinline__ static int mix(int k) {
-        return kRows == 256 ? (k & 7) | ((k >> 1) & 8) : ((k >> 1) & 3) | ((k >> 2) & 4);
+        return kRows == 256 ? (k & 7) | ((k >> 1) & 8) : kRows == 128 ? ((k >> 1) & 3) | ((k >> 2) & 4) : ((k >> 2) & 1) | ((k >> 3) & 2);
     }
     __device__ __forceinline__ static const char* base(const Operand& o, int64_t row0, int64_t k0) {
         return static_cast<const char*>(o.p) + k0 * o.ld + row0;
@@ -109,7 +112,7 @@ struct CodesKR {
         i32x8 r;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            // k 8 on has another permutation than k: bit 3 of k leaves mix alone at 256, and 128, bytes
+            // bits 3 and 6 of k do not enter mix
             const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(uintptr_t)(p + (64 * (j >> 1) + 8 * (j & 1)) * kRows));
             r[2 * j] = x[0];
             r[2 * j + 1] = x[1];
@@ -146,24 +149,37 @@ struct Multiply<true> {
     }
 };
 
+// Tile l of a grid of them: workgroups are dealt to the 8 XCDs in turn; each XCD
+// takes one contiguous eighth, in groups of group_m tiles of m by all n, so the
+// workgroups that run on it together share operands in its L2.
+__device__ __forceinline__ void place_of(int b, int tiles_m, int tiles_n, int splits, int group_m, int& tm, int& tn, int& split) {
+    const int total = tiles_m * tiles_n * splits;
+    const int x = b & 7, each = total >> 3, more = total & 7;
+    int l = x * each + min(x, more) + (b >> 3);
+    split = l / (tiles_m * tiles_n);
+    l -= split * tiles_m * tiles_n;
+    const int group = l / (group_m * tiles_n);
+    const int m0 = group * group_m;
+    const int width = min(group_m, tiles_m - m0);
+    const int in = l - group * group_m * tiles_n;
+    tm = m0 + in % width;
+    tn = in / width;
+}
+
 template <class A, class B, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact, class Epilogue>
-__global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(ProductArgs g, Epilogue epilogue) {
+__device__ __forceinline__ void run_tile(const ProductArgs& g, const Epilogue& epilogue, uint32_t lds, int tm, int split, int64_t n0) {
     constexpr int kTM = kTileM / kWavesM / 16, kTN = kTileN / kWavesN / 16;
     static_assert(kTileDim % (kTM * 16) == 0 && kTileDim % (kTN * 16) == 0, "a wave's rows and tokens lie in one tile each");
     constexpr uint32_t kStage = A::kBytes + B::kBytes;
     constexpr uint32_t kOther = kStage;
     typedef Multiply<kExact> Mul;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / kWavesN, wn = wave % kWavesN;
-    int tm, tn, split;
-    tile_of(g, tm, tn, split);
-    const int64_t m0 = (int64_t)tm * kTileM, n0 = (int64_t)tn * kTileN;
+    const int64_t m0 = (int64_t)tm * kTileM;
     const int64_t k0 = split * g.k_per_split;
     const int64_t k1 = min(g.k, k0 + g.k_per_split);
     const int steps = (int)((max(k1 - k0, (int64_t)0) + kTileDim - 1) / kTileDim);
 
-    const uint32_t lds = lds_address(smem);
     const A fa(lds, wm * kTM * 16, lane);
     const B fb(lds + A::kBytes, wn * kTN * 16, lane);
     uint32_t off_a[A::kLoads], off_b[B::kLoads];
@@ -328,6 +344,35 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
     }
     const WaveTile w{mw, nw, tm, wm, split, lane};
     epilogue.template run<kTM, kTN>(acc, w);
+}
+
+// Operands and LDS of a tile of this shape.
+template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWaves>
+struct TileOf {
+    template <bool kKR, int kRows, int kTiles>
+    using Layout = std::conditional_t<kKR, CodesKR<kRows, kWaves, kTiles>, CodesKC<kRows, kWaves>>;
+    static constexpr int kLds = 2 * 128 * (kTileM + kTileN);
+};
+
+// Whole tiles, then, where a last round of them would leave CUs idle, tiles half as
+// wide for the last columns.
+template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact, bool kHalves, class Epilogue>
+__global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(ProductArgs g, Epilogue epilogue) {
+    typedef TileOf<kAKR, kBKR, kTileM, kTileN, kWavesM * kWavesN> Tile;
+    typedef typename Tile::template Layout<kAKR, kTileM, kTileM / kWavesM / 16> A;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const uint32_t lds = lds_address(smem);
+    const int whole = g.tiles_m * g.tiles_n * g.splits;
+    int tm, tn, split;
+    if (!kHalves || (int)blockIdx.x < whole) {
+        typedef typename Tile::template Layout<kBKR, kTileN, kTileN / kWavesN / 16> B;
+        place_of(blockIdx.x, g.tiles_m, g.tiles_n, g.splits, g.group_m, tm, tn, split);
+        run_tile<A, B, kTileM, kTileN, kWavesM, kWavesN, kExact>(g, epilogue, lds, tm, split, (int64_t)tn * kTileN);
+    } else if constexpr (kHalves) {
+        typedef typename Tile::template Layout<kBKR, kTileN / 2, kTileN / 2 / kWavesN / 16> Half;
+        place_of(blockIdx.x - whole, g.tiles_m, g.half_tiles_n, 1, g.group_m, tm, tn, split);
+        run_tile<A, Half, kTileM, kTileN / 2, kWavesM, kWavesN, kExact>(g, epilogue, lds, tm, split, (int64_t)g.tiles_n * kTileN + (int64_t)tn * (kTileN / 2));
+    }
 }
 
 }  // namespace bfz

@@ -3,7 +3,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "codes_gemm.h"
 #include "layer_internal.h"
@@ -107,6 +106,7 @@ struct StoreEpilogue {
             const int64_t token = w.n0 + 16 * u + (w.lane & 15);
 #pragma unroll
             for (int t = 0; t < kTM; t += 2) {
+                __builtin_amdgcn_sched_barrier(0);  // one store's registers at a time
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -175,10 +175,39 @@ __global__ __launch_bounds__(kThreads) void copy_weight_kernel(const uint8_t* __
 
 // ---- host -------------------------------------------------------------------------
 
-template <class A, class B, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact>
+constexpr int kCus = 256;
+
+// Columns of n that go into whole tiles; the others go into tiles half as wide, so
+// that the last round of workgroups is a short one.  A half tile takes some 0.55 of
+// a whole one's time, and the CUs that the last whole tiles leave take it first.
+int64_t whole_columns(int64_t tiles_m, int64_t n, int64_t width) {
+    const int64_t tiles_n = (n + width - 1) / width;
+    constexpr double kHalf = 0.55;
+    int64_t best = tiles_n;
+    double least = (double)((tiles_m * tiles_n + kCus - 1) / kCus);
+    for (int64_t c = tiles_n - 1; c >= 0 && c >= tiles_n - 8; --c) {
+        const int64_t whole = tiles_m * c, busy = whole % kCus;
+        const int64_t halves = tiles_m * ((n - c * width + width / 2 - 1) / (width / 2));
+        // by the end of a last round of length t, the CUs that are free at its start
+        // take t / kHalf of them, the busy ones (t - 1) / kHalf
+        for (double t : {kHalf, 1.0, 2 * kHalf, 1.0 + kHalf, 3 * kHalf, 1.0 + 2 * kHalf}) {
+            const int64_t room = (kCus - busy) * (int64_t)(t / kHalf + 1e-6) + busy * (int64_t)(std::max(0.0, t - 1.0) / kHalf + 1e-6);
+            if (room < halves || (busy > 0 && t < 1.0)) continue;
+            const double time = (double)(whole / kCus) + t;
+            if (time < least - 0.05) {
+                least = time;
+                best = c;
+            }
+            break;
+        }
+    }
+    return best;
+}
+
+template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact, bool kHalves>
 int launch_tiles(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
-    constexpr int kLds = 2 * (A::kBytes + B::kBytes);
-    const auto kernel = codes_gemm_kernel<A, B, kTileM, kTileN, kWavesM, kWavesN, kExact, StoreEpilogue>;
+    constexpr int kLds = TileOf<kAKR, kBKR, kTileM, kTileN, kWavesM * kWavesN>::kLds;
+    const auto kernel = codes_gemm_kernel<kAKR, kBKR, kTileM, kTileN, kWavesM, kWavesN, kExact, kHalves, StoreEpilogue>;
     static std::atomic<bool> ready{false};
     if (!ready.load(std::memory_order_relaxed)) {
         const hipError_t rc = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -188,12 +217,15 @@ int launch_tiles(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
     g.tiles_m = (int32_t)((g.a.extent + kTileM - 1) / kTileM);
     g.tiles_n = (int32_t)((g.b.extent + kTileN - 1) / kTileN);
     g.group_m = std::min(g.tiles_m, 4);
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)(g.tiles_m * g.tiles_n * g.splits)), dim3(64 * kWavesM * kWavesN), kLds, stream, g, e);
+    if constexpr (kHalves) {
+        const int64_t whole = whole_columns(g.tiles_m, g.b.extent, kTileN);
+        g.half_tiles_n = (int32_t)(std::max<int64_t>(0, g.b.extent - whole * kTileN + kTileN / 2 - 1) / (kTileN / 2));
+        g.tiles_n = (int32_t)whole;
+    }
+    const int64_t wgs = (int64_t)g.tiles_m * ((int64_t)g.tiles_n * g.splits + g.half_tiles_n);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)wgs), dim3(64 * kWavesM * kWavesN), kLds, stream, g, e);
     return hipGetLastError();
 }
-
-template <bool kAKR, int kRows, int kWaves, int kTiles>
-using Layout = std::conditional_t<kAKR, CodesKR<kRows, kWaves, kTiles>, CodesKC<kRows, kWaves>>;
 
 // Splits of k until there are tiles for every CU.
 int32_t splits_for(int64_t tiles, int64_t k, int64_t m, int64_t n) {
@@ -206,14 +238,11 @@ bool wide_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 
 
 template <bool kAKR, bool kBKR, bool kExact>
 int launch_product(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
-    if constexpr (kExact) {
-        if (wide_tiles(g.a.extent, g.b.extent))
-            return launch_tiles<Layout<kAKR, 256, 8, 4>, Layout<kBKR, 128, 8, 4>, 256, 128, 4, 2, true>(g, e, stream);
-    } else {
-        if (wide_tiles(g.a.extent, g.b.extent))
-            return launch_tiles<Layout<kAKR, 256, 8, 8>, Layout<kBKR, 256, 8, 4>, 256, 256, 2, 4, false>(g, e, stream);
+    if (wide_tiles(g.a.extent, g.b.extent)) {
+        if constexpr (kExact) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, true, true>(g, e, stream);
+        else return launch_tiles<kAKR, kBKR, 256, 256, 2, 4, false, true>(g, e, stream);
     }
-    return launch_tiles<Layout<kAKR, 128, 4, 4>, Layout<kBKR, 128, 4, 4>, 128, 128, 2, 2, kExact>(g, e, stream);
+    return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, kExact, false>(g, e, stream);
 }
 
 template <bool kAKR, bool kBKR>
@@ -223,13 +252,16 @@ int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* su
     StoreEpilogue e{a.out, a.out_ld, 0, m, n, a.out_type, a.accumulate, 0};
     e.vec = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_ld * size)) & 15u) == 0;
     const int64_t blocks = std::max<int64_t>(1, (g.k + kTileDim - 1) / kTileDim);
-    g.splits = wide_tiles(m, n) ? 1 : splits_for(((m + 127) / 128) * ((n + 127) / 128), g.k, m, n);
-    g.k_per_split = (blocks + g.splits - 1) / g.splits * kTileDim;
+    g.splits = g.k == 0 ? 0 : wide_tiles(m, n) ? 1 : splits_for(((m + 127) / 128) * ((n + 127) / 128), g.k, m, n);
+    if (g.splits > 0) {
+        g.k_per_split = (blocks + g.splits - 1) / g.splits * kTileDim;
+        g.splits = (int32_t)((g.k + g.k_per_split - 1) / g.k_per_split);
+    }
     if (g.splits == 1) return exact ? launch_product<kAKR, kBKR, true>(g, e, stream) : launch_product<kAKR, kBKR, false>(g, e, stream);
     const int64_t pieces = (m + 7) / 8;
     e.slab = pieces * 8 * n;
     const StoreEpilogue part{sums, pieces * 8, e.slab, pieces * 8, n, kF32, 0, 1};
-    const int rc = exact ? launch_product<kAKR, kBKR, true>(g, part, stream) : launch_product<kAKR, kBKR, false>(g, part, stream);
+    const int rc = g.splits == 0 ? hipSuccess : exact ? launch_product<kAKR, kBKR, true>(g, part, stream) : launch_product<kAKR, kBKR, false>(g, part, stream);
     if (rc) return rc;
     const dim3 wgs((uint32_t)((n * pieces + kThreads - 1) / kThreads));
     if (a.out_type == kF32) hipLaunchKernelGGL((join_splits_kernel<float>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);
