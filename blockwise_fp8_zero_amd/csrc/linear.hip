@@ -242,6 +242,7 @@ int launch_product(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
         if constexpr (kExact) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, true, true>(g, e, stream);
         else return launch_tiles<kAKR, kBKR, 256, 256, 2, 4, false, true>(g, e, stream);
     }
+    if (!kExact && ((g.a.extent + 255) / 256) * ((g.b.extent + 127) / 128) >= 192 && g.splits == 1) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, kExact, true>(g, e, stream);
     return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, kExact, false>(g, e, stream);
 }
 
