@@ -375,4 +375,124 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
     }
 }
 
+// ---- few tokens -------------------------------------------------------------------
+// The same product, both operands with k contiguous, for up to 16 kTN tokens in
+// all, bound by reading A once.  Nothing is staged: eight waves of a workgroup take
+// 16 kTM rows of A and share out the blocks of k; a lane loads its fragments of
+// rows and tokens straight into registers, two or
+// four rounds ahead.  The waves' sums meet
+// in LDS.  kQuantize: B is a matrix of values, which each workgroup quantizes by
+// rows into LDS while its first loads of A are under way.
+constexpr int kFewKWaves = 8;
+
+template <int kTM, int kTN, bool kExact, bool kQuantize, class Inputs, class Epilogue>
+__global__ __launch_bounds__(64 * kFewKWaves) void few_codes_kernel(ProductArgs g, Inputs inputs, Epilogue epilogue) {
+    constexpr int kAhead = kTM == 1 ? 4 : 2;  // rounds in registers
+    typedef Multiply<kExact> Mul;
+    __shared__ f32x4 sums[kFewKWaves][kTM][kTN][64];
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, r = lane & 15;
+    const int64_t m0 = (int64_t)blockIdx.x * (16 * kTM);
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(g.a.p) + m0 * g.a.ld), (short)0,
+                                                                        (int)kBufferBytes, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(g.b.p)), (short)0, (int)kBufferBytes,
+                                                                        0x00020000);
+    const int blocks = (int)((g.k + kTileDim - 1) / kTileDim);
+    const float* scale_a = g.grid + m0 / kTileDim * g.grid_m;
+    const int last = (int)g.b.extent - 1;
+
+    struct Round {
+        i32x8 a[kTM], b[kTN];
+        float scale[kTN];
+    };
+    auto fragment = [&](const __amdgpu_buffer_rsrc_t& buf, uint32_t row, bool there, int kb, int64_t k) {
+        i32x4 half[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = kb * kTileDim + 64 * h + 16 * q;
+            half[h] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, there && at < k ? (int)(row + (uint32_t)at) : (int)kNowhere, 0, 0));
+        }
+        return __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto load_a = [&](Round& x, int kb) {
+#pragma unroll
+        for (int t = 0; t < kTM; ++t) x.a[t] = fragment(ra, (uint32_t)((16 * t + r) * g.a.ld), m0 + 16 * t + r < g.a.extent, kb, g.a.k);
+    };
+    auto load_b = [&](Round& x, int kb) {
+        const int at = min(kb, blocks - 1);
+        const float sa = scale_a[at * g.grid_k];
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) {
+            const int token = min(16 * u + r, last);
+            if constexpr (kQuantize) {
+                x.b[u] = inputs.fragment(smem, 16 * u + r, kb, q);
+                x.scale[u] = sa * inputs.scale(smem, token, at);
+            } else {
+                x.b[u] = fragment(rb, (uint32_t)(token * g.b.ld), 16 * u + r <= last, kb, g.b.k);
+                x.scale[u] = sa * g.scales[g.tiles == kTilesOfN ? token / kTileDim * g.scales_ld + at : at * g.scales_ld + token];
+            }
+        }
+    };
+    Round x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_a(x[i], wave + i * kFewKWaves);
+    if constexpr (kQuantize) {
+        inputs.quantize(smem);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_b(x[i], wave + i * kFewKWaves);
+
+    f32x4 acc[kTM][kTN];
+#pragma unroll
+    for (int t = 0; t < kTM; ++t)
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b0 = wave; b0 < blocks; b0 += kAhead * kFewKWaves) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int kb = b0 + i * kFewKWaves;
+            if (kb >= blocks) break;
+            Round& y = x[i];
+            f32x4 part[kTM][kTN];
+#pragma unroll
+            for (int j = 0; j < Mul::kParts; ++j)
+#pragma unroll
+                for (int t = 0; t < kTM; ++t) {
+                    const typename Mul::Value av = Mul::value(y.a[t], j);
+#pragma unroll
+                    for (int u = 0; u < kTN; ++u)
+                        part[t][u] = Mul::run(av, Mul::value(y.b[u], j), j == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[t][u]);
+                }
+            float by[kTN];
+#pragma unroll
+            for (int u = 0; u < kTN; ++u) by[u] = y.scale[u];
+            const int next = kb + kAhead * kFewKWaves;
+            if (next < blocks) {
+                load_a(y, next);
+                load_b(y, next);
+            }
+#pragma unroll
+            for (int t = 0; t < kTM; ++t)
+#pragma unroll
+                for (int u = 0; u < kTN; ++u)
+#pragma unroll
+                    for (int l = 0; l < 4; ++l) acc[t][u][l] = __builtin_fmaf(part[t][u][l], by[u], acc[t][u][l]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kTM; ++t)
+#pragma unroll
+        for (int u = 0; u < kTN; ++u) sums[wave][t][u][lane] = acc[t][u];
+    __syncthreads();
+    for (int i = wave; i < kTM * kTN; i += kFewKWaves) {
+        const int t = i / kTN, u = i % kTN;
+        f32x4 sum = sums[0][t][u][lane];
+#pragma unroll
+        for (int w = 1; w < kFewKWaves; ++w) sum += sums[w][t][u][lane];
+        epilogue.put4(16 * u + r, m0 + 16 * t + 4 * q, sum);
+    }
+}
+
 }  // namespace bfz

@@ -17,25 +17,29 @@ constexpr int64_t kMostSums = int64_t(1) << 23;  // floats that the splits of a 
 // ---- quantizer ------------------------------------------------------------------
 
 // Row groups: 16 lanes hold a group, 8 columns each; a wave 4 groups of a row.
-constexpr int kRowsOfWg = 32, kGroupsOfWave = 4;
+constexpr int kRowsOfWave = 2, kRowsOfWg = kRowsOfWave * kThreads / 64, kGroupsOfWave = 4;
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a, int32_t col_wgs, int32_t vec) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t block = blockIdx.x;
     const int64_t c = (block % col_wgs) * (kGroupsOfWave * kTileDim) + 8 * lane;
-    const int64_t r0 = block / col_wgs * kRowsOfWg;
+    const int64_t r0 = block / col_wgs * kRowsOfWg + wave * kRowsOfWave;
     const int64_t left = a.dim - c;
     const int count = left <= 0 ? 0 : left >= 8 ? 8 : (int)left;
     const int64_t width = (a.dim + 15) / 16 * 16;
-    for (int64_t r = r0 + wave; r < min(r0 + kRowsOfWg, a.n); r += kThreads / 64) {
-        float x[8];
-        load8_any(static_cast<const T*>(a.x) + r * a.x_ld + c, count, vec, x);
-        const float scale = scale_of(row_max(abs_max8(x)), a.pow2);
+    float x[kRowsOfWave][8];
+#pragma unroll
+    for (int k = 0; k < kRowsOfWave; ++k)
+        load8_any(static_cast<const T*>(a.x) + (r0 + k) * a.x_ld + c, r0 + k < a.n ? count : 0, vec, x[k]);
+#pragma unroll
+    for (int k = 0; k < kRowsOfWave; ++k) {
+        const float scale = scale_of(row_max(abs_max8(x[k])), a.pow2);
         uint32_t w[2];
-        quantize8(x, Quotient(scale), w);
-        if (c < width) *reinterpret_cast<u32x2*>(a.codes + r * a.codes_ld + c) = u32x2{w[0], w[1]};
-        if ((lane & 15) == 0 && c < a.dim) a.scales[c / kTileDim * a.scales_ld + r] = scale;
+        quantize8(x[k], Quotient(scale), w);
+        if (r0 + k >= a.n) continue;
+        if (c < width) *reinterpret_cast<u32x2*>(a.codes + (r0 + k) * a.codes_ld + c) = u32x2{w[0], w[1]};
+        if ((lane & 15) == 0 && c < a.dim) a.scales[c / kTileDim * a.scales_ld + r0 + k] = scale;
     }
 }
 
@@ -123,6 +127,25 @@ struct StoreEpilogue {
             }
         }
     }
+    // 4 results of a token from m on
+    __device__ __forceinline__ void put4(int64_t token, int64_t c, const f32x4& x) const {
+        if (token >= n) return;
+        const int64_t at = token * ld + c;
+        if (type == kF32) put4(static_cast<float*>(out) + at, c, x);
+        else if (type == kBF16) put4(static_cast<bf16_t*>(out) + at, c, x);
+        else put4(static_cast<f16_t*>(out) + at, c, x);
+    }
+    template <class O>
+    __device__ __forceinline__ void put4(O* p, int64_t c, const f32x4& x) const {
+        if (vec && c + 4 <= m) {
+            if constexpr (sizeof(O) == 4) *reinterpret_cast<f32x4*>(p) = x;
+            else *reinterpret_cast<u32x2*>(p) = u32x2{pack2<O>(x[0], x[1]), pack2<O>(x[2], x[3])};
+        } else {
+#pragma unroll
+            for (int l = 0; l < 4; ++l)
+                if (c + l < m) p[l] = Elem<O>::to(x[l]);
+        }
+    }
     template <class O>
     __device__ __forceinline__ void put(O* p, int64_t c, float (&x)[8]) const {
         if (vec && c + 8 <= m) {
@@ -138,6 +161,45 @@ struct StoreEpilogue {
             for (int l = 0; l < 8; ++l)
                 if (c + l < m) p[l] = Elem<O>::to(add ? Elem<O>::get(p[l]) + x[l] : x[l]);
         }
+    }
+};
+
+// Inputs of a product of few tokens that the product itself quantizes by rows: in
+// LDS the codes, rows of `width` bytes with zeros at the end, then the scales
+// [token][block].
+struct RowInputs {
+    const void* x;
+    int32_t type, vec;
+    int64_t ld;
+    int32_t n, dim, width, blocks;
+    template <class T>
+    __device__ __forceinline__ void quantize_type(char* lds) const {
+        float* scales = reinterpret_cast<float*>(lds + n * width);
+        const int pieces = blocks * 16;  // of 8 columns, whole groups
+        for (int i = threadIdx.x; i < n * pieces; i += 64 * kFewKWaves) {
+            const int token = i / pieces, c = 8 * (i - token * pieces);
+            float y[8];
+            load8_any(static_cast<const T*>(x) + token * ld + c, min(8, max(0, dim - c)), vec, y);
+            const float scale = scale_of(row_max(abs_max8(y)), false);
+            uint32_t w[2];
+            quantize8(y, Quotient(scale), w);
+            *reinterpret_cast<u32x2*>(lds + token * width + c) = u32x2{w[0], w[1]};
+            if ((threadIdx.x & 15) == 0) scales[token * blocks + c / kTileDim] = scale;
+        }
+    }
+    __device__ __forceinline__ void quantize(char* lds) const {
+        if (type == kF32) quantize_type<float>(lds);
+        else if (type == kBF16) quantize_type<bf16_t>(lds);
+        else quantize_type<f16_t>(lds);
+    }
+    __device__ __forceinline__ i32x8 fragment(const char* lds, int token, int kb, int q) const {
+        if (token >= n || kb >= blocks) return i32x8{0, 0, 0, 0, 0, 0, 0, 0};
+        const char* p = lds + token * width + kb * kTileDim + 16 * q;
+        const i32x4 lo = *reinterpret_cast<const i32x4*>(p), hi = *reinterpret_cast<const i32x4*>(p + 64);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    __device__ __forceinline__ float scale(const char* lds, int token, int kb) const {
+        return reinterpret_cast<const float*>(lds + n * width)[token * blocks + kb];
     }
 };
 
@@ -271,6 +333,37 @@ int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* su
     return hipGetLastError();
 }
 
+constexpr int64_t kFewTokensMost = 64;
+
+template <int kTM, int kTN, bool kExact, bool kQuantize>
+int launch_few(const ProductArgs& g, const RowInputs& x, const StoreEpilogue& e, hipStream_t stream) {
+    const int lds = kQuantize ? x.n * x.width + 4 * x.n * x.blocks : 0;
+    const auto kernel = few_codes_kernel<kTM, kTN, kExact, kQuantize, RowInputs, StoreEpilogue>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)((e.m + 16 * kTM - 1) / (16 * kTM))),
+                       dim3(64 * kFewKWaves), (size_t)lds, stream, g, x, e);
+    return hipGetLastError();
+}
+
+// As few rows a workgroup, 16 to 48, as still fit the device in one round: one
+// workgroup a CU with 33 tokens and more, whose registers and LDS leave no room for
+// a second, else two.
+template <int kTN, bool kExact, bool kQuantize>
+int few_rows(const ProductArgs& g, const RowInputs& x, const StoreEpilogue& e, hipStream_t stream) {
+    constexpr int64_t kRound = 16 * kCus * (kTN == 4 ? 1 : 2);
+    if (e.m <= 16 * kCus) return launch_few<1, kTN, kExact, kQuantize>(g, x, e, stream);
+    if (kTN < 4 || e.m <= 2 * kRound) return launch_few<2, kTN, kExact, kQuantize>(g, x, e, stream);
+    return launch_few<3, kTN, kExact, kQuantize>(g, x, e, stream);
+}
+
+template <bool kExact>
+int few_tokens(const ProductArgs& g, const RowInputs* x, const StoreEpilogue& e, hipStream_t stream) {
+    if (x) return few_rows<1, kExact, true>(g, *x, e, stream);
+    const RowInputs none{};
+    if (e.n <= 16) return few_rows<1, kExact, false>(g, none, e, stream);
+    if (e.n <= 32) return few_rows<2, kExact, false>(g, none, e, stream);
+    return few_rows<4, kExact, false>(g, none, e, stream);
+}
+
 void token_scales(ProductArgs& g, const Codes& c) {
     g.scales = c.scales;
     g.scales_ld = c.scales_ld;
@@ -336,6 +429,11 @@ int launch_linear(const LinearArgs& a, void* work, void* stream) {
     g.blocks_m = (a.rows + kTileDim - 1) / kTileDim;
     g.blocks_k = wide;
     token_scales(g, a.x);
+    if (a.n <= kFewTokensMost) {
+        const bool vec = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_ld * dtype_size(a.out_type))) & 15u) == 0;
+        const StoreEpilogue e{a.out, a.out_ld, 0, a.rows, a.n, a.out_type, 0, vec};
+        return a.out_type == kF32 ? few_tokens<true>(g, nullptr, e, (hipStream_t)stream) : few_tokens<false>(g, nullptr, e, (hipStream_t)stream);
+    }
     return product<false, false>(g, a, a.rows, a.n, static_cast<float*>(work), (hipStream_t)stream);
 }
 
