@@ -41,6 +41,13 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 // [k / 128][n / 128], rows scales_ld apart.
 constexpr int kEachOfN = 0, kTilesOfN = 1, kTilesOfK = 2;
 
+typedef __attribute__((address_space(3))) const char* lds_pointer;
+
+template <class T>
+__device__ __forceinline__ T lds_at(lds_pointer p) {
+    return *(__attribute__((address_space(3))) const T*)p;
+}
+
 struct ProductArgs : GemmArgs {  // grid: scale of (m / 128, k / 128) at grid_m, grid_k; k_per_split a multiple of 128
     const float* scales;
     int64_t scales_ld;
@@ -166,19 +173,40 @@ __device__ __forceinline__ void place_of(int b, int tiles_m, int tiles_n, int sp
     tn = in / width;
 }
 
-template <class A, class B, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact, class Epilogue>
+// 4 bytes a lane from memory to LDS at lds + 4 * lane.
+__device__ __forceinline__ void load_word_to_lds(const i32x4& buf, uint32_t offset, uint32_t lds) {
+    __asm__ volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dword %1, %2, 0 offen lds"
+        :
+        : "s"(lds), "v"(offset), "s"(buf)
+        : "memory");
+}
+
+template <int kCount>
+__device__ __forceinline__ void wait_all_but() {
+    __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kCount) : "memory");
+}
+
+// One tile.  Everything that the loop loads goes through LDS, scales included, in
+// kStages buffers, by loads that the compiler does not count: a wave waits for the
+// block it needs next and leaves those behind it in flight.
+template <class A, class B, int kTileM, int kTileN, int kWavesM, int kWavesN, int kStages, bool kExact, class Epilogue>
 __device__ __forceinline__ void run_tile(const ProductArgs& g, const Epilogue& epilogue, uint32_t lds, int tm, int split, int64_t n0) {
     constexpr int kTM = kTileM / kWavesM / 16, kTN = kTileN / kWavesN / 16;
-    static_assert(kTileDim % (kTM * 16) == 0 && kTileDim % (kTN * 16) == 0, "a wave's rows and tokens lie in one tile each");
-    constexpr uint32_t kStage = A::kBytes + B::kBytes;
-    constexpr uint32_t kOther = kStage;
+    static_assert(kTileDim % (kTM * 16) == 0, "a wave's rows lie in one tile");
+    constexpr uint32_t kScales = A::kBytes + B::kBytes;  // of the tile's tokens, behind the operands
+    constexpr uint32_t kStage = kScales + 4 * kTileN;
+    constexpr int kWaves = kWavesM * kWavesN;
     typedef Multiply<kExact> Mul;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / kWavesN, wn = wave % kWavesN;
     const int64_t m0 = (int64_t)tm * kTileM;
     const int64_t k0 = split * g.k_per_split;
     const int64_t k1 = min(g.k, k0 + g.k_per_split);
-    const int steps = (int)((max(k1 - k0, (int64_t)0) + kTileDim - 1) / kTileDim);
+    const int steps = (int)((k1 - k0 + kTileDim - 1) / kTileDim);
+    const int64_t mw = m0 + wm * kTM * 16, nw = n0 + wn * kTN * 16;
 
     const A fa(lds, wm * kTM * 16, lane);
     const B fb(lds + A::kBytes, wn * kTN * 16, lane);
@@ -191,7 +219,20 @@ __device__ __forceinline__ void run_tile(const ProductArgs& g, const Epilogue& e
     const char* base_b = B::base(g.b, n0, k0);
     const int64_t adv_a = A::advance(g.a), adv_b = B::advance(g.b);
     const uint32_t lds_a = lds + wave * 1024, lds_b = lds_a + A::kBytes;
-    constexpr int kWaves = kWavesM * kWavesN;
+
+    // Scales: each wave loads those of 64 tokens, in turn over the tile's (which
+    // several waves load where it has fewer than 64 a wave: the same values).
+    // Tokens beyond the last have its tile's, or zero.
+    const int first = 64 * (wave % (kTileN / 64)) + lane;
+    const int64_t tile0 = n0 / kTileDim, tile = min(n0 + first, g.b.extent - 1) / kTileDim;
+    const bool each_n = g.tiles == kEachOfN;
+    const uint32_t off_s = each_n ? (n0 + first < g.b.extent ? 4u * first : kNowhere)
+                                  : (uint32_t)(4 * (tile - tile0) * (g.tiles == kTilesOfN ? g.scales_ld : 1));
+    const char* base_s = reinterpret_cast<const char*>(g.tiles == kTilesOfN ? g.scales + tile0 * g.scales_ld + k0 / kTileDim
+                                                                            : g.scales + k0 / kTileDim * g.scales_ld + (each_n ? n0 : tile0));
+    const int64_t adv_s = 4 * (g.tiles == kTilesOfN ? 1 : g.scales_ld);
+    const uint32_t lds_s = lds + kScales + 256 * (wave % (kTileN / 64));
+    const uint32_t at_s = lds + kScales + 4 * (wn * kTN * 16 + (lane & 15));
 
     // Loads of the next block into buffer `stage`, `parts` calls of which part p
     // issues its share; past the end of k they give zero (no branch: the lanes'
@@ -202,6 +243,10 @@ __device__ __forceinline__ void run_tile(const ProductArgs& g, const Epilogue& e
         constexpr int p = decltype(part)::value, parts = decltype(of)::value;
         constexpr int from = p * kLoads / parts, to = (p + 1) * kLoads / parts;
         const i32x4 ra = buffer_of(base_a), rb = buffer_of(base_b);
+        if constexpr (p == 0) {
+            load_word_to_lds(buffer_of(base_s), left_b > 0 ? off_s : kNowhere, lds_s + stage);
+            base_s += adv_s;
+        }
         each<to - from>([&](auto i) {
             constexpr int j = from + decltype(i)::value;
             if constexpr (j < A::kLoads)
@@ -219,35 +264,17 @@ __device__ __forceinline__ void run_tile(const ProductArgs& g, const Epilogue& e
     constexpr std::integral_constant<int, 0> kNone{};
     constexpr std::integral_constant<int, 1> kOnce{};
 
-    // scales of this wave's rows and of the lane's tokens in a block, beyond the
-    // edges those of the last
-    const int64_t mw = m0 + wm * kTM * 16, nw = n0 + wn * kTN * 16;
+    // the rows' scale of a block, by a scalar load
+    typedef __attribute__((address_space(4))) const float constant_float;
     const float* scale_a = g.grid + min(mw / kTileDim, g.blocks_m - 1) * g.grid_m + k0 / kTileDim * g.grid_k;
-    const int64_t nlast = g.b.extent - 1;
-    const int64_t tile_b = min(nw, nlast) / kTileDim;
-    const float* scale_b = g.tiles == kTilesOfN ? g.scales + tile_b * g.scales_ld + k0 / kTileDim
-                                                : g.scales + k0 / kTileDim * g.scales_ld + (g.tiles ? tile_b : 0);
-    const int64_t step_b = g.tiles == kTilesOfN ? 1 : g.scales_ld;
-    int32_t token[kTN];
-#pragma unroll
-    for (int u = 0; u < kTN; ++u) token[u] = g.tiles ? 0 : (int32_t)min(nw + 16 * u + (lane & 15), nlast);
-    float next[kTN], next_a, now[kTN], by[kTN];
-    auto load_scales = [&](bool there) {
-        if (!there) return;
-        next_a = *scale_a;
-#pragma unroll
-        for (int u = 0; u < kTN; ++u) next[u] = scale_b[token[u]];
+    float next_a, now[kTN], by[kTN];
+    auto load_scale = [&]() {
+        next_a = *(constant_float*)(uintptr_t)scale_a;
         scale_a += g.grid_k;
-        scale_b += step_b;
     };
-    // Here, so that the wait which the compiler puts before their use does not
-    // catch the loads issued after it.
-    auto take_scales = [&]() {
+    auto take_scales = [&](uint32_t stage) {
 #pragma unroll
-        for (int u = 0; u < kTN; ++u) {
-            now[u] = next[u] * next_a;
-            __asm__ volatile("" : "+v"(now[u]));
-        }
+        for (int u = 0; u < kTN; ++u) now[u] = lds_at<float>((lds_pointer)(uintptr_t)(at_s + stage) + 64 * u) * next_a;
     };
 
     f32x4 acc[kTM][kTN];
@@ -256,92 +283,91 @@ __device__ __forceinline__ void run_tile(const ProductArgs& g, const Epilogue& e
 #pragma unroll
         for (int u = 0; u < kTN; ++u) acc[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (steps > 0) {
-        load_scales(true);
-        take_scales();
-        // A block's loads go out over kSpread rows of tiles, from the last row of the
-        // block before on: all at once they fill the queue, and a wave that waits
-        // there cannot multiply.
-        constexpr int kSpread = kTM / 2;
-        constexpr std::integral_constant<int, kSpread> kParted{};
-        issue(0, kNone, kOnce);
-        issue(kOther, kNone, kParted);
-        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads / kSpread) : "memory");
-        __builtin_amdgcn_s_barrier();
-        constexpr int kParts = Mul::kParts;
-        // Rows of A are read kAhead rows before their use: two where they are converted
-        // during the row before.
-        constexpr int kAhead = kExact ? 2 : 1;
-        i32x8 a[2], raw[kTN];
-        typename Mul::Value av[kParts], b[kTN][kParts];
-        f32x4 part[kTN];
-        a[0] = fa.read(0, 0);
-        if constexpr (kAhead == 2) a[1] = fa.read(0, 1);
+    // A block's loads go out over kSpread rows of tiles, from the last row of the
+    // block before on: all at once they fill the queue, and a wave that waits
+    // there cannot multiply.
+    constexpr int kSpread = kTM / 2;
+    constexpr std::integral_constant<int, kSpread> kParted{};
+    load_scale();
+    each<kStages - 1>([&](auto i) { issue(decltype(i)::value * kStage, kNone, kOnce); });
+    uint32_t cur = 0, into = (kStages - 1) * kStage;
+    issue(into, kNone, kParted);
+    wait_all_but<(kStages - 2) * (kLoads + 1) + kLoads / kSpread + 1>();
+    __builtin_amdgcn_s_barrier();
+    take_scales(0);
+    constexpr int kParts = Mul::kParts;
+    // Rows of A are read kAhead rows before their use: two where they are converted
+    // during the row before.
+    constexpr int kAhead = kExact ? 2 : 1;
+    i32x8 a[2], raw[kTN];
+    typename Mul::Value av[kParts], b[kTN][kParts];
+    f32x4 part[kTN];
+    a[0] = fa.read(0, 0);
+    if constexpr (kAhead == 2) a[1] = fa.read(0, 1);
 #pragma unroll
-        for (int u = 0; u < kTN; ++u) raw[u] = fb.read(0, u);
+    for (int u = 0; u < kTN; ++u) raw[u] = fb.read(0, u);
 #pragma unroll
-        for (int j = 0; j < kParts; ++j) av[j] = Mul::value(a[0], j);
-        auto scale_row = [&](auto row, auto col) {
-            constexpr int t = decltype(row)::value, u = decltype(col)::value;
+    for (int j = 0; j < kParts; ++j) av[j] = Mul::value(a[0], j);
+    auto scale_row = [&](auto row, auto col) {
+        constexpr int t = decltype(row)::value, u = decltype(col)::value;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(part[u][i], by[u], acc[t][u][i]);
-        };
+        for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(part[u][i], by[u], acc[t][u][i]);
+    };
 #pragma unroll
-        for (int u = 0; u < kTN; ++u) {
-            part[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            by[u] = 0.0f;
-        }
-        uint32_t cur = 0;
-        for (int s = 0; s < steps; ++s) {
-            load_scales(s + 1 < steps);
-            each<kTM>([&](auto row) {
-                constexpr int t = decltype(row)::value;
-                constexpr bool kLast = t == kTM - 1;
-                if constexpr (kLast) {
-                    // every fragment of this block is read; the next block has arrived
-                    wait_loads();
-                    __builtin_amdgcn_s_barrier();
-                    __builtin_amdgcn_sched_barrier(0);
-                    take_scales();
-                    cur = kOther - cur;
-                }
-                if constexpr (kAhead == 1) {
-                    a[(t + 1) & 1] = fa.read(cur, kLast ? 0 : t + 1);
-                } else if constexpr (kLast) {
-                    a[(t + 1) & 1] = fa.read(cur, 0);
-                    a[t & 1] = fa.read(cur, 1);
-                } else if constexpr (t + 2 < kTM) {
-                    a[t & 1] = fa.read(cur, t + 2);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                f32x4 p[kTN];
-                each<kParts * kTN>([&](auto both) {
-                    constexpr int j = decltype(both)::value / kTN, u = decltype(both)::value % kTN;
-                    constexpr std::integral_constant<int, u> col{};
-                    if constexpr (t == 0) b[u][j] = Mul::value(raw[u], j);
-                    p[u] = Mul::run(av[j], b[u][j], j == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p[u]);
-                    if constexpr (kLast && j == kParts - 1) raw[u] = fb.read(cur, u);
-                    if constexpr (j == 0 && u == 1 && kLast) issue(kOther - cur, kNone, kParted);
-                    if constexpr (j == 0 && u == 1 && t + 1 < kSpread) issue(kOther - cur, std::integral_constant<int, t + 1>{}, kParted);
-                    if constexpr (j == 0) {
-                        scale_row(std::integral_constant<int, (t + kTM - 1) % kTM>{}, col);
-                        if constexpr (t == 0) by[u] = now[u];
-                    }
-                    // the next row's values, a part at a time, once this row's are used
-                    if constexpr (u == kTN - 1 && !(kLast && kAhead == 2)) av[j] = Mul::value(a[(t + 1) & 1], j);
-                    __builtin_amdgcn_sched_barrier(0);
-                });
-                if constexpr (kLast && kAhead == 2) {
-#pragma unroll
-                    for (int j = 0; j < kParts; ++j) av[j] = Mul::value(a[(t + 1) & 1], j);
-                }
-#pragma unroll
-                for (int u = 0; u < kTN; ++u) part[u] = p[u];
-            });
-        }
-        each<kTN>([&](auto col) { scale_row(std::integral_constant<int, kTM - 1>{}, col); });
-        wait_loads();  // the loads issued past the end
+    for (int u = 0; u < kTN; ++u) {
+        part[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        by[u] = 0.0f;
     }
+    for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps) load_scale();
+        each<kTM>([&](auto row) {
+            constexpr int t = decltype(row)::value;
+            constexpr bool kLast = t == kTM - 1;
+            if constexpr (kLast) {
+                // every fragment of this block is read; the next block has arrived
+                wait_all_but<(kStages - 2) * (kLoads + 1)>();
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                into = cur;
+                cur = cur + kStage == kStages * kStage ? 0 : cur + kStage;
+                take_scales(cur);
+            }
+            if constexpr (kAhead == 1) {
+                a[(t + 1) & 1] = fa.read(cur, kLast ? 0 : t + 1);
+            } else if constexpr (kLast) {
+                a[(t + 1) & 1] = fa.read(cur, 0);
+                a[t & 1] = fa.read(cur, 1);
+            } else if constexpr (t + 2 < kTM) {
+                a[t & 1] = fa.read(cur, t + 2);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 p[kTN];
+            each<kParts * kTN>([&](auto both) {
+                constexpr int j = decltype(both)::value / kTN, u = decltype(both)::value % kTN;
+                constexpr std::integral_constant<int, u> col{};
+                if constexpr (t == 0) b[u][j] = Mul::value(raw[u], j);
+                p[u] = Mul::run(av[j], b[u][j], j == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p[u]);
+                if constexpr (kLast && j == kParts - 1) raw[u] = fb.read(cur, u);
+                if constexpr (j == 0 && u == 1 && kLast) issue(into, kNone, kParted);
+                if constexpr (j == 0 && u == 1 && t + 1 < kSpread) issue(into, std::integral_constant<int, t + 1>{}, kParted);
+                if constexpr (j == 0) {
+                    scale_row(std::integral_constant<int, (t + kTM - 1) % kTM>{}, col);
+                    if constexpr (t == 0) by[u] = now[u];
+                }
+                // the next row's values, a part at a time, once this row's are used
+                if constexpr (u == kTN - 1 && !(kLast && kAhead == 2)) av[j] = Mul::value(a[(t + 1) & 1], j);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if constexpr (kLast && kAhead == 2) {
+#pragma unroll
+                for (int j = 0; j < kParts; ++j) av[j] = Mul::value(a[(t + 1) & 1], j);
+            }
+#pragma unroll
+            for (int u = 0; u < kTN; ++u) part[u] = p[u];
+        });
+    }
+    each<kTN>([&](auto col) { scale_row(std::integral_constant<int, kTM - 1>{}, col); });
+    wait_loads();  // the loads issued past the end
     const WaveTile w{mw, nw, tm, wm, split, lane};
     epilogue.template run<kTM, kTN>(acc, w);
 }
@@ -351,12 +377,12 @@ template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWaves>
 struct TileOf {
     template <bool kKR, int kRows, int kTiles>
     using Layout = std::conditional_t<kKR, CodesKR<kRows, kWaves, kTiles>, CodesKC<kRows, kWaves>>;
-    static constexpr int kLds = 2 * 128 * (kTileM + kTileN);
+    static constexpr int kStage = 128 * (kTileM + kTileN) + 4 * kTileN;
 };
 
 // Whole tiles, then, where a last round of them would leave CUs idle, tiles half as
 // wide for the last columns.
-template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact, bool kHalves, class Epilogue>
+template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN, int kStages, bool kExact, bool kHalves, class Epilogue>
 __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(ProductArgs g, Epilogue epilogue) {
     typedef TileOf<kAKR, kBKR, kTileM, kTileN, kWavesM * kWavesN> Tile;
     typedef typename Tile::template Layout<kAKR, kTileM, kTileM / kWavesM / 16> A;
@@ -367,11 +393,11 @@ __global__ __launch_bounds__(64 * kWavesM * kWavesN, 2) void codes_gemm_kernel(P
     if (!kHalves || (int)blockIdx.x < whole) {
         typedef typename Tile::template Layout<kBKR, kTileN, kTileN / kWavesN / 16> B;
         place_of(blockIdx.x, g.tiles_m, g.tiles_n, g.splits, g.group_m, tm, tn, split);
-        run_tile<A, B, kTileM, kTileN, kWavesM, kWavesN, kExact>(g, epilogue, lds, tm, split, (int64_t)tn * kTileN);
+        run_tile<A, B, kTileM, kTileN, kWavesM, kWavesN, kStages, kExact>(g, epilogue, lds, tm, split, (int64_t)tn * kTileN);
     } else if constexpr (kHalves) {
         typedef typename Tile::template Layout<kBKR, kTileN / 2, kTileN / 2 / kWavesN / 16> Half;
         place_of(blockIdx.x - whole, g.tiles_m, g.half_tiles_n, 1, g.group_m, tm, tn, split);
-        run_tile<A, Half, kTileM, kTileN / 2, kWavesM, kWavesN, kExact>(g, epilogue, lds, tm, split, (int64_t)g.tiles_n * kTileN + (int64_t)tn * (kTileN / 2));
+        run_tile<A, Half, kTileM, kTileN / 2, kWavesM, kWavesN, kStages, kExact>(g, epilogue, lds, tm, split, (int64_t)g.tiles_n * kTileN + (int64_t)tn * (kTileN / 2));
     }
 }
 

@@ -44,7 +44,7 @@ int check_codes(const uint8_t* p, int64_t rows, int64_t dim, int64_t ld, const c
 int check_scales(const float* p, int64_t ld, int32_t tiles, int64_t n, int64_t dim, const char* what, const char* where) {
     if (n > 0 && !p) return fail(BFZ_EINVAL, "%s: %s: null pointer", where, what);
     const int64_t width = tiles ? blocks_of(dim) : n;
-    if (ld < width || ld > (int64_t(1) << 32))
+    if (ld < width || ld > kMostTokens)
         return fail(BFZ_EINVAL, "%s: %s: rows %lld scales apart, %lld wide", where, what, (long long)ld, (long long)width);
     if (!aligned(p, 4)) return fail(BFZ_EALIGN, "%s: %s must be 4-byte aligned", where, what);
     return BFZ_OK;

@@ -266,10 +266,10 @@ int64_t whole_columns(int64_t tiles_m, int64_t n, int64_t width) {
     return best;
 }
 
-template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kExact, bool kHalves>
+template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN, int kStages, bool kExact, bool kHalves>
 int launch_tiles(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
-    constexpr int kLds = TileOf<kAKR, kBKR, kTileM, kTileN, kWavesM * kWavesN>::kLds;
-    const auto kernel = codes_gemm_kernel<kAKR, kBKR, kTileM, kTileN, kWavesM, kWavesN, kExact, kHalves, StoreEpilogue>;
+    constexpr int kLds = kStages * TileOf<kAKR, kBKR, kTileM, kTileN, kWavesM * kWavesN>::kStage;
+    const auto kernel = codes_gemm_kernel<kAKR, kBKR, kTileM, kTileN, kWavesM, kWavesN, kStages, kExact, kHalves, StoreEpilogue>;
     static std::atomic<bool> ready{false};
     if (!ready.load(std::memory_order_relaxed)) {
         const hipError_t rc = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -301,11 +301,12 @@ bool wide_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 
 template <bool kAKR, bool kBKR, bool kExact>
 int launch_product(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
     if (wide_tiles(g.a.extent, g.b.extent)) {
-        if constexpr (kExact) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, true, true>(g, e, stream);
-        else return launch_tiles<kAKR, kBKR, 256, 256, 2, 4, false, true>(g, e, stream);
+        if constexpr (kExact) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, true, true>(g, e, stream);
+        else return launch_tiles<kAKR, kBKR, 256, 256, 2, 4, 2, false, true>(g, e, stream);
     }
-    if (!kExact && ((g.a.extent + 255) / 256) * ((g.b.extent + 127) / 128) >= 192 && g.splits == 1) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, kExact, true>(g, e, stream);
-    return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, kExact, false>(g, e, stream);
+    if (!kExact && ((g.a.extent + 255) / 256) * ((g.b.extent + 127) / 128) >= 192 && g.splits == 1) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, kExact, true>(g, e, stream);
+    if (((g.a.extent + 127) / 128) * ((g.b.extent + 127) / 128) * g.splits <= 256) return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, 4, kExact, false>(g, e, stream);
+    return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, 2, kExact, false>(g, e, stream);
 }
 
 template <bool kAKR, bool kBKR>
