@@ -127,16 +127,11 @@ extern "C" int bfz_linear(const void* x, int32_t x_dtype, int64_t x_ld, const fl
         if (scales || tiles) return fail(BFZ_EINVAL, "%s: only E4M3 codes come with scales", where);
         rc = check_out(x, x_dtype, n, cols, x_ld, "x", where);
         if (rc) return rc;
-        uint8_t* codes;
-        float* made;
-        int64_t ld;
-        linear_work_codes(work, n, cols, &codes, &ld, &made);
         if (blocks_of(n) * blocks_of(cols) >= (int64_t(1) << 23))
             return fail(BFZ_EINVAL, "%s: %lld rows of width %lld are too many for one call", where, (long long)n, (long long)cols);
-        const QuantizeArgs q{x, x_dtype, 0, 0, x_ld, n, cols, codes, ld, made, n};
-        if (n > 0) rc = launched(where, launch_quantize(q, stream));
-        if (rc) return rc;
-        a.x = Codes{codes, ld, made, n, 0};
+        a.values = x;
+        a.values_type = x_dtype;
+        a.values_ld = x_ld;
     }
     a.weight = weight;
     a.grid = grid;

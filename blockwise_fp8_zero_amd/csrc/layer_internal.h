@@ -36,6 +36,9 @@ struct Codes {
 struct LinearArgs {
     Codes x;                // forward: the input; gradients: of the output
     Codes other;            // gradient of the weight: the input
+    const void* values;     // forward: the input where x is yet to be made of it, else null
+    int32_t values_type;
+    int64_t values_ld;
     const uint8_t* weight;  // [rows, cols]
     const float* grid;
     int64_t weight_ld;
@@ -47,8 +50,6 @@ struct LinearArgs {
 // Of the products' workspace; copy: the weight's rows have to be copied;
 // quantize: so have the inputs' codes and scales to be made.
 int64_t linear_work_bytes(int64_t n, int64_t rows, int64_t cols, int copy, int quantize);
-// Codes and scales of inputs that bfz_linear quantizes itself, in the workspace.
-void linear_work_codes(void* work, int64_t n, int64_t cols, uint8_t** codes, int64_t* ld, float** scales);
 int launch_linear(const LinearArgs& a, void* work, void* stream);
 int launch_linear_grad_input(const LinearArgs& a, void* work, void* stream);
 int launch_linear_grad_weight(const LinearArgs& a, void* work, void* stream);

@@ -14,7 +14,7 @@ Without gradients, bfz.linear(x, weight, w_grid, y, work) quantizes x itself.
 """
 from . import _check, lib
 from . import _tensors
-from ._tensors import E4M3, dtype_code, home_device, matrix, raw_stream, tile_grid, work_pointer
+from ._tensors import E4M3, home_device, matrix, raw_stream, tile_grid, work_pointer
 
 
 def quantize_buffers(n, dim, tiles=False, device="cuda"):
@@ -33,21 +33,20 @@ def _rows(t, name, home):
     p, code, rows, cols, ld = matrix(t, name, home, codes=True)
     if code != E4M3:
         raise TypeError(f"{name}: need E4M3 codes (uint8)")
-    if rows == 1:
-        ld = max(t.stride(0), -(-cols // 16) * 16)  # a single row's stride says nothing
-    if cols % 16 and rows:
-        end = t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16
-        if end > t.untyped_storage().nbytes():
+    if cols & 15 and rows:
+        wide = -(-cols // 16) * 16
+        if rows == 1:
+            ld = max(t.stride(0), wide)  # a single row's stride says nothing
+        if t.storage_offset() + (rows - 1) * ld + wide > t.untyped_storage().nbytes():
             raise ValueError(f"{name}: rows have to reach to the next multiple of 16 columns (see quantize_buffers)")
     return p, rows, cols, ld
 
 
 def _scales(t, name, home, n, dim, tiles):
     """(pointer, row stride) of the scales of (n, dim) codes."""
-    shape = (-(-n // 128), -(-dim // 128)) if tiles else (-(-dim // 128), n)
     p, code, rows, cols, ld = matrix(t, name, home)
-    if code != 0 or (rows, cols) != shape:
-        raise ValueError(f"{name}: need float32 {shape}")
+    if code or (rows, cols) != ((-(-n // 128), -(-dim // 128)) if tiles else (-(-dim // 128), n)):
+        raise ValueError(f"{name}: need float32 {(-(-n // 128), -(-dim // 128)) if tiles else (-(-dim // 128), n)}")
     return p, ld
 
 
@@ -68,8 +67,16 @@ def quantize(x, codes, scales, tiles=False, pow2=False, stream=None):
         _check(rc)
 
 
-def _unaligned(weight):
-    return int(bool((weight.data_ptr() | weight.stride(0) | weight.shape[1]) & 15))
+_bytes = {}  # of workspaces, by sizes
+
+
+def _work_bytes(*sizes):
+    need = _bytes.get(sizes)
+    if need is None:
+        if len(_bytes) > 4096:
+            _bytes.clear()
+        need = _bytes[sizes] = int(lib().bfz_linear_work_bytes(*sizes))
+    return need
 
 
 def linear_workspace(n, weight, x_dtype=None, device=None):
@@ -79,15 +86,18 @@ def linear_workspace(n, weight, x_dtype=None, device=None):
     _tensors._load()
     rows, cols = weight.shape
     code = E4M3 if x_dtype is None else _tensors._codes[x_dtype]
-    need = int(lib().bfz_linear_work_bytes(int(n), rows, cols, code, _unaligned(weight)))
+    copy = (weight.data_ptr() | (weight.stride(0) if rows > 1 else 0)) & 15
+    need = _work_bytes(int(n), rows, cols, code, int(copy != 0))
     return torch.empty(max(256, need), dtype=torch.uint8, device=weight.device if device is None else device)
 
 
 def _weight(weight, grid, home):
+    """(pointer, row stride, pointer of the grid, rows, columns, whether the rows
+    are copied)"""
     w, code, rows, cols, ld = matrix(weight, "weight", home, codes=True)
     if code != E4M3:
         raise TypeError("weight: need E4M3 codes (uint8)")
-    return w, ld, tile_grid(grid, home, code, rows, cols), rows, cols
+    return w, ld, tile_grid(grid, home, code, rows, cols), rows, cols, int(((w | ld) & 15) != 0)
 
 
 def _result(t, name, home, shape):
@@ -97,33 +107,29 @@ def _result(t, name, home, shape):
     return p, code, ld
 
 
-def _work(work, home, n, rows, cols, code, copy):
-    return work_pointer(work, home, lib().bfz_linear_work_bytes(n, rows, cols, code, copy))
-
-
 def linear(x, weight, grid, out, work, scales=None, tiles=False, stream=None):
     """out = X W^T.  x: (n, cols) E4M3 codes with the scales that quantize gave
     them (tiles: as there), or float32, bfloat16 or float16 values, which are
     quantized by rows; weight: (rows, cols) E4M3 codes with their tile scales
     `grid`; out: (n, rows) float32, bfloat16 or float16."""
     home = home_device()
-    code = dtype_code(x, "x", home, codes=True)
-    w, wld, g, rows, cols = _weight(weight, grid, home)
+    p, code, n, dim, ld = matrix(x, "x", home, codes=True)
+    w, wld, g, rows, cols, copy = _weight(weight, grid, home)
     if code == E4M3:
-        p, n, dim, ld = _rows(x, "x", home)
+        if dim & 15 or n == 1:
+            p, n, dim, ld = _rows(x, "x", home)
         if scales is None:
             raise TypeError("scales: E4M3 codes need theirs")
         s, sld = _scales(scales, "scales", home, n, dim, tiles)
     else:
         if scales is not None or tiles:
             raise ValueError("scales, tiles: only E4M3 codes have them")
-        p, code, n, dim, ld = matrix(x, "x", home)
         s, sld = None, 0
     if dim != cols:
         raise ValueError(f"x is {(n, dim)}, weight {(rows, cols)}")
     o, ocode, old = _result(out, "out", home, (n, rows))
     rc = lib().bfz_linear(p, code, ld, s, sld, int(bool(tiles)), n, w, wld, g, rows, cols, o, ocode, old,
-                          _work(work, home, n, rows, cols, code, _unaligned(weight)), raw_stream(stream, home))
+                          work_pointer(work, home, _work_bytes(n, rows, cols, code, copy)), raw_stream(stream, home))
     if rc:
         _check(rc)
 
@@ -133,14 +139,14 @@ def linear_grad_input(dout, weight, grid, dx, work, scales, tiles=False, accumul
     with the scales that quantize gave them; dx: (n, cols) float32, bfloat16 or
     float16."""
     home = home_device()
-    w, wld, g, rows, cols = _weight(weight, grid, home)
+    w, wld, g, rows, cols, copy = _weight(weight, grid, home)
     p, n, dim, ld = _rows(dout, "dout", home)
     if dim != rows:
         raise ValueError(f"dout is {(n, dim)}, weight {(rows, cols)}")
     s, sld = _scales(scales, "scales", home, n, dim, tiles)
     o, ocode, old = _result(dx, "dx", home, (n, cols))
     rc = lib().bfz_linear_grad_input(p, ld, s, sld, int(bool(tiles)), n, w, wld, g, rows, cols, o, ocode, old, int(bool(accumulate)),
-                                     _work(work, home, n, rows, cols, E4M3, _unaligned(weight)), raw_stream(stream, home))
+                                     work_pointer(work, home, _work_bytes(n, rows, cols, E4M3, copy)), raw_stream(stream, home))
     if rc:
         _check(rc)
 
@@ -158,6 +164,6 @@ def linear_grad_weight(dout, dout_grid, x, x_grid, dweight, work, accumulate=Fal
     t, tld = _scales(x_grid, "x_grid", home, n, cols, True)
     o, ocode, old = _result(dweight, "dweight", home, (rows, cols))
     rc = lib().bfz_linear_grad_weight(p, ld, s, sld, q, qld, t, tld, n, rows, cols, o, ocode, old, int(bool(accumulate)),
-                                      _work(work, home, n, rows, cols, E4M3, 0), raw_stream(stream, home))
+                                      work_pointer(work, home, _work_bytes(n, rows, cols, E4M3, 0)), raw_stream(stream, home))
     if rc:
         _check(rc)
