@@ -16,12 +16,11 @@ __device__ __forceinline__ float pow2_scale_of(float amax) {
     return __builtin_amdgcn_ldexpf(1.0f, T);
 }
 
-// Scale of a group from the largest |x| of its numbers (NaN aside).
-__device__ __forceinline__ float scale_of(float amax, bool pow2) {
-    if (amax == 0.0f) return 1.0f;
-    if (pow2 && amax < INFINITY) return pow2_scale_of(amax);
-    const float s = amax / 448.0f;
-    return s == 0.0f ? 0x1p-149f : s;
+// x / by, correctly rounded, from the rounded reciprocal of `by`: see Quotient.
+__device__ __forceinline__ float quotient_of(float x, float by, float back) {
+    float q = x * back;
+    q = __builtin_fmaf(-__builtin_fmaf(q, by, -x), back, q);
+    return __builtin_fmaf(-__builtin_fmaf(q, by, -x), back, q);
 }
 
 // Quotients x / scale, correctly rounded, from one division for the group: with
@@ -35,11 +34,7 @@ struct Quotient {
     float scale, back;
     bool direct;
     __device__ __forceinline__ explicit Quotient(float s) : scale(s), back(1.0f / s), direct(!(s >= 0x1p-60f && s <= 0x1p60f)) {}
-    __device__ __forceinline__ float fast(float x) const {
-        float q = x * back;
-        q = __builtin_fmaf(-__builtin_fmaf(q, scale, -x), back, q);
-        return __builtin_fmaf(-__builtin_fmaf(q, scale, -x), back, q);
-    }
+    __device__ __forceinline__ float fast(float x) const { return quotient_of(x, scale, back); }
     // kept within +-448, since scales of few bits (subnormal) may lie below
     // amax / 448; a NaN stays one
     __device__ __forceinline__ float slow(float x) const {
@@ -47,6 +42,15 @@ struct Quotient {
         return q > 448.0f ? 448.0f : q < -448.0f ? -448.0f : q;
     }
 };
+
+// Scale of a group from the largest |x| of its numbers (NaN aside).
+__device__ __forceinline__ float scale_of(float amax, bool pow2) {
+    if (pow2 && amax > 0.0f && amax < INFINITY) return pow2_scale_of(amax);
+    if (__builtin_expect(amax >= 0x1p-60f && amax <= 0x1p100f, 1)) return quotient_of(amax, 448.0f, 1.0f / 448.0f);
+    if (amax == 0.0f) return 1.0f;
+    const float s = amax / 448.0f;
+    return s == 0.0f ? 0x1p-149f : s;
+}
 
 // Codes of four values, the first in the lowest byte: to the nearest, ties to
 // even (the conversion's own rounding; quotients beyond 448 round to 448 since
@@ -76,6 +80,15 @@ __device__ __forceinline__ float row_max(float x) {
     x = fmaxf(x, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), 0x124, 0xf, 0xf, false)));
     x = fmaxf(x, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), 0x122, 0xf, 0xf, false)));
     return fmaxf(x, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), 0x121, 0xf, 0xf, false)));
+}
+
+// Largest value over a wave, in all its lanes.
+__device__ __forceinline__ float wave_max(float x) {
+    x = row_max(x);
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 template <class T>
