@@ -130,12 +130,13 @@ __device__ __forceinline__ bool on_fours(const void* p, int type) {
 constexpr int kPieces = (int)(kAdamwChunk / (4 * kThreads));
 static_assert(kStateBlock == 4 * 64 && kPieces * kThreads * 4 == kAdamwChunk, "a wave to a block");
 
-// kWhole: all of it lies in the tensor, on boundaries of 4 elements.  Without those
+// From element e0 on, a wave's blocks.  kWhole: all of them lie in the tensor, on boundaries of 4 elements.  Without those
 // checks, and with the types known, it is a third of the instructions: 256M
-// elements with f32 parameters, bf16 gradients and 8-bit states 716 us, with them
+// elements with f32 parameters, bf16 gradients and 8-bit states 690 us, with them
 // 797.
 template <bool kCodes, bool kWhole>
 __device__ __forceinline__ void adamw_chunk(const AdamwList& list, const StepScalars& s, int k, int64_t e0, int pt, int gt) {
+    constexpr int kMany = kWhole ? kPieces : 1;
     const int64_t n = list.n[k];
     constexpr int st = kCodes ? kE4M3 : kF32;
     void* param = list.param[k];
@@ -149,11 +150,11 @@ __device__ __forceinline__ void adamw_chunk(const AdamwList& list, const StepSca
     // infinities and zeros putting right
     const float back = 1.0f / s.sbc2;
     const int lane = threadIdx.x & 63;
-    const int64_t b0 = e0 + (int64_t)(threadIdx.x >> 6) * (kPieces * kStateBlock) + 4 * lane;
-    Raw rp[kPieces], rg[kPieces], rm[kPieces], rv[kPieces];
-    float ms[kPieces], vs[kPieces];
+    const int64_t b0 = e0 + 4 * lane;
+    Raw rp[kMany], rg[kMany], rm[kMany], rv[kMany];
+    float ms[kMany], vs[kMany];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < kMany; ++i) {
         const int64_t e = b0 + i * kStateBlock, left = n - e;
         const int count = kWhole || left >= 4 ? 4 : left <= 0 ? 0 : (int)left;
         rp[i] = load_raw(param, pt, e, count, vec);
@@ -167,7 +168,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamwList& list, const StepSca
         }
     }
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < kMany; ++i) {
         const int64_t e = b0 + i * kStateBlock, left = n - e;
         const int count = kWhole || left >= 4 ? 4 : left <= 0 ? 0 : (int)left;
         float p[4], g[4], mm[4], vv[4], root[4];
@@ -215,11 +216,19 @@ __device__ __forceinline__ void adamw_tensor(const AdamwList& list, const StepSc
     constexpr int st = kCodes ? kE4M3 : kF32;
     const bool whole = e0 + kAdamwChunk <= list.n[k] && on_fours(list.param[k], pt) && on_fours(list.grad[k], gt) && on_fours(list.m[k], st) &&
                        on_fours(list.v[k], st);
-    if (!whole) return adamw_chunk<kCodes, false>(list, s, k, e0, pt, gt);
+    if (!whole) {
+        // a block at a time, in turn over the waves: little code, which a small
+        // tensor's time goes into fetching
+#pragma unroll 1
+        for (int64_t e = e0 + (threadIdx.x >> 6) * kStateBlock; e < min(e0 + kAdamwChunk, list.n[k]); e += kThreads / 64 * kStateBlock)
+            adamw_chunk<kCodes, false>(list, s, k, e, pt, gt);
+        return;
+    }
+    const int64_t mine = e0 + (int64_t)(threadIdx.x >> 6) * (kPieces * kStateBlock);
     const auto with_grad = [&](auto param) {
-        if (gt == kF32) adamw_chunk<kCodes, true>(list, s, k, e0, decltype(param)::value, kF32);
-        else if (gt == kBF16) adamw_chunk<kCodes, true>(list, s, k, e0, decltype(param)::value, kBF16);
-        else adamw_chunk<kCodes, true>(list, s, k, e0, decltype(param)::value, kF16);
+        if (gt == kF32) adamw_chunk<kCodes, true>(list, s, k, mine, decltype(param)::value, kF32);
+        else if (gt == kBF16) adamw_chunk<kCodes, true>(list, s, k, mine, decltype(param)::value, kBF16);
+        else adamw_chunk<kCodes, true>(list, s, k, mine, decltype(param)::value, kF16);
     };
     if (pt == kF32) with_grad(std::integral_constant<int, kF32>{});
     else if (pt == kBF16) with_grad(std::integral_constant<int, kBF16>{});
