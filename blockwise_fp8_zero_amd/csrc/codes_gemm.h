@@ -425,12 +425,11 @@ __global__ __launch_bounds__(64 * kFewKWaves) void few_codes_kernel(ProductArgs 
     const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(g.b.p)), (short)0, (int)kBufferBytes,
                                                                         0x00020000);
     const int blocks = (int)((g.k + kTileDim - 1) / kTileDim);
-    const float* scale_a = g.grid + m0 / kTileDim * g.grid_m;
     const int last = (int)g.b.extent - 1;
 
     struct Round {
         i32x8 a[kTM], b[kTN];
-        float scale[kTN];
+        float scale[kTN], rows[kTM];
     };
     auto fragment = [&](const __amdgpu_buffer_rsrc_t& buf, uint32_t row, bool there, int kb, int64_t k) {
         i32x4 half[2];
@@ -443,20 +442,23 @@ __global__ __launch_bounds__(64 * kFewKWaves) void few_codes_kernel(ProductArgs 
     };
     auto load_a = [&](Round& x, int kb) {
 #pragma unroll
-        for (int t = 0; t < kTM; ++t) x.a[t] = fragment(ra, (uint32_t)((16 * t + r) * g.a.ld), m0 + 16 * t + r < g.a.extent, kb, g.a.k);
+        for (int t = 0; t < kTM; ++t) {
+            x.a[t] = fragment(ra, (uint32_t)((16 * t + r) * g.a.ld), m0 + 16 * t + r < g.a.extent, kb, g.a.k);
+            // 16 rows lie in one tile, 48 may not
+            x.rows[t] = g.grid[min((m0 + 16 * t) / kTileDim, g.blocks_m - 1) * g.grid_m + min(kb, blocks - 1) * g.grid_k];
+        }
     };
     auto load_b = [&](Round& x, int kb) {
         const int at = min(kb, blocks - 1);
-        const float sa = scale_a[at * g.grid_k];
 #pragma unroll
         for (int u = 0; u < kTN; ++u) {
             const int token = min(16 * u + r, last);
             if constexpr (kQuantize) {
                 x.b[u] = inputs.fragment(smem, 16 * u + r, kb, q);
-                x.scale[u] = sa * inputs.scale(smem, token, at);
+                x.scale[u] = inputs.scale(smem, token, at);
             } else {
                 x.b[u] = fragment(rb, (uint32_t)(token * g.b.ld), 16 * u + r <= last, kb, g.b.k);
-                x.scale[u] = sa * g.scales[g.tiles == kTilesOfN ? token / kTileDim * g.scales_ld + at : at * g.scales_ld + token];
+                x.scale[u] = g.scales[g.tiles == kTilesOfN ? token / kTileDim * g.scales_ld + at : at * g.scales_ld + token];
             }
         }
     };
@@ -491,9 +493,11 @@ __global__ __launch_bounds__(64 * kFewKWaves) void few_codes_kernel(ProductArgs 
                     for (int u = 0; u < kTN; ++u)
                         part[t][u] = Mul::run(av, Mul::value(y.b[u], j), j == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : part[t][u]);
                 }
-            float by[kTN];
+            float by[kTM][kTN];
 #pragma unroll
-            for (int u = 0; u < kTN; ++u) by[u] = y.scale[u];
+            for (int t = 0; t < kTM; ++t)
+#pragma unroll
+                for (int u = 0; u < kTN; ++u) by[t][u] = y.scale[u] * y.rows[t];
             const int next = kb + kAhead * kFewKWaves;
             if (next < blocks) {
                 load_a(y, next);
@@ -504,7 +508,7 @@ __global__ __launch_bounds__(64 * kFewKWaves) void few_codes_kernel(ProductArgs 
 #pragma unroll
                 for (int u = 0; u < kTN; ++u)
 #pragma unroll
-                    for (int l = 0; l < 4; ++l) acc[t][u][l] = __builtin_fmaf(part[t][u][l], by[u], acc[t][u][l]);
+                    for (int l = 0; l < 4; ++l) acc[t][u][l] = __builtin_fmaf(part[t][u][l], by[t][u], acc[t][u][l]);
         }
     }
 #pragma unroll

@@ -219,6 +219,25 @@ def test_linear(n, rows, cols):
             check(out, xv, wv.t(), blocks)
 
 
+@pytest.mark.parametrize("rows", [4200, 8300, 12400])
+@pytest.mark.parametrize("n", [1, 16, 20, 33, 64])
+def test_few_tokens_many_rows(n, rows):
+    """Every share of rows that a workgroup may have, 16, 32 or 48, beside the
+    128 rows of a tile scale."""
+    torch.manual_seed(n + rows)
+    cols = 200
+    w, grid, wv = weight(rows, cols)
+    grid *= torch.exp2(torch.randint(-3, 4, grid.shape, device="cuda").float())
+    wv = value(w, grid, True)
+    codes, scales = quantized(torch.randn(n, cols, device="cuda"))
+    xv = value(codes, scales, False)
+    work = bfz.linear_workspace(n, w)
+    for t in (F32, BF16):
+        out = torch.full((n, rows), float("nan"), dtype=t, device="cuda")
+        bfz.linear(codes, w, grid, out, work, scales=scales)
+        check(out, xv, wv.t(), 2)
+
+
 @pytest.mark.parametrize("n,rows,cols", [(1, 4096, 4096), (1, 300, 1001), (4, 256, 512), (17, 130, 200), (300, 513, 640)])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_linear_of_values(n, rows, cols, dtype):
