@@ -43,35 +43,37 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a,
     }
 }
 
-// Tiles: 16 lanes a row, 16 rows at a time, the whole tile in registers.
+// Tiles: 16 lanes a row, the whole tile in registers, 4 rows a thread.
+constexpr int kTileThreads = 512, kTileRows = kTileDim * 16 / kTileThreads, kTileStep = kTileThreads / 16;
 template <class T>
-__global__ __launch_bounds__(kThreads) void quantize_tiles_kernel(QuantizeArgs a, int32_t col_tiles, int32_t vec) {
-    __shared__ float tops[kThreads / 64];
+__global__ __launch_bounds__(kTileThreads) void quantize_tiles_kernel(QuantizeArgs a, int32_t col_tiles, int32_t vec) {
+    __shared__ float tops[kTileThreads / 64];
     const int64_t i = blockIdx.x / col_tiles, j = blockIdx.x % col_tiles;
     const int64_t c = j * kTileDim + 8 * (threadIdx.x & 15);
     const int64_t left = a.dim - c;
     const int count = left <= 0 ? 0 : left >= 8 ? 8 : (int)left;
     const int64_t r0 = i * kTileDim + (threadIdx.x >> 4);
     const int64_t width = (a.dim + 15) / 16 * 16;
-    float x[8][8];
+    float x[kTileRows][8];
     float top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int64_t r = r0 + 16 * k;
+    for (int k = 0; k < kTileRows; ++k) {
+        const int64_t r = r0 + kTileStep * k;
         load8_any(static_cast<const T*>(a.x) + r * a.x_ld + c, r < a.n ? count : 0, vec, x[k]);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, abs_max8(x[k]));
-    top = row_max(top);
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    for (int k = 0; k < kTileRows; ++k) top = fmaxf(top, abs_max8(x[k]));
+    top = wave_max(top);
     if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
     __syncthreads();
-    const float scale = scale_of(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), a.pow2);
+    top = tops[0];
+#pragma unroll
+    for (int w = 1; w < kTileThreads / 64; ++w) top = fmaxf(top, tops[w]);
+    const float scale = scale_of(top, a.pow2);
     const Quotient q(scale);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int64_t r = r0 + 16 * k;
+    for (int k = 0; k < kTileRows; ++k) {
+        const int64_t r = r0 + kTileStep * k;
         uint32_t w[2];
         quantize8(x[k], q, w);
         if (r < a.n && c < width) *reinterpret_cast<u32x2*>(a.codes + r * a.codes_ld + c) = u32x2{w[0], w[1]};
@@ -84,7 +86,7 @@ int quantize(const QuantizeArgs& a, hipStream_t stream) {
     const int32_t vec = ((reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.x_ld * sizeof(T))) & 15u) == 0;
     if (a.tiles) {
         const int64_t wide = (a.dim + kTileDim - 1) / kTileDim, high = (a.n + kTileDim - 1) / kTileDim;
-        hipLaunchKernelGGL((quantize_tiles_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kThreads), 0, stream, a, (int32_t)wide, vec);
+        hipLaunchKernelGGL((quantize_tiles_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kTileThreads), 0, stream, a, (int32_t)wide, vec);
     } else {
         const int64_t wide = (a.dim + kGroupsOfWave * kTileDim - 1) / (kGroupsOfWave * kTileDim), high = (a.n + kRowsOfWg - 1) / kRowsOfWg;
         hipLaunchKernelGGL((quantize_rows_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kThreads), 0, stream, a, (int32_t)wide, vec);
@@ -289,11 +291,22 @@ int launch_tiles(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Splits of k until there are tiles for every CU.
-int32_t splits_for(int64_t tiles, int64_t k, int64_t m, int64_t n) {
+// Splits of k, by modelled time in us: a block of a 128 x 128 tile takes 0.65, or 1.05
+// with bf16 instructions; splits cost a launch to join them and their sums' way out
+// and back (1013 x 1544 x 1008: 17 us in two splits, 10 in one; 100 x 4096 x 11008:
+// 62 and 25 in seven).
+int32_t splits_for(int64_t tiles, int64_t k, int64_t m, int64_t n, bool exact) {
     const int64_t blocks = (k + kTileDim - 1) / kTileDim;
-    int64_t s = std::min<int64_t>(std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), blocks / 4), 16);
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(s, kMostSums / std::max<int64_t>(1, m * n)));
+    int64_t best = 1;
+    double least = 1e30;
+    for (int64_t s = 1; s <= 16 && s <= blocks && (s == 1 || (s * tiles <= kCus && s * m * n <= kMostSums)); ++s) {
+        const double time = (double)((blocks + s - 1) / s) * (exact ? 1.05 : 0.65) + (s > 1 ? 5.0 + (double)(s * m * n) * 8 / 4e6 : 0.0);
+        if (time < least) {
+            least = time;
+            best = s;
+        }
+    }
+    return (int32_t)best;
 }
 
 bool wide_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256) >= 192; }
@@ -305,7 +318,7 @@ int launch_product(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
         else return launch_tiles<kAKR, kBKR, 256, 256, 2, 4, 2, false, true>(g, e, stream);
     }
     if (!kExact && ((g.a.extent + 255) / 256) * ((g.b.extent + 127) / 128) >= 192 && g.splits == 1) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, kExact, true>(g, e, stream);
-    if (((g.a.extent + 127) / 128) * ((g.b.extent + 127) / 128) * g.splits <= 256) return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, 4, kExact, false>(g, e, stream);
+    if (((g.a.extent + 127) / 128) * ((g.b.extent + 127) / 128) * g.splits <= 256) return launch_tiles<kAKR, kBKR, 128, 128, 4, 2, 4, kExact, false>(g, e, stream);
     return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, 2, kExact, false>(g, e, stream);
 }
 
@@ -316,7 +329,7 @@ int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* su
     StoreEpilogue e{a.out, a.out_ld, 0, m, n, a.out_type, a.accumulate, 0};
     e.vec = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_ld * size)) & 15u) == 0;
     const int64_t blocks = std::max<int64_t>(1, (g.k + kTileDim - 1) / kTileDim);
-    g.splits = g.k == 0 ? 0 : wide_tiles(m, n) ? 1 : splits_for(((m + 127) / 128) * ((n + 127) / 128), g.k, m, n);
+    g.splits = g.k == 0 ? 0 : wide_tiles(m, n) ? 1 : splits_for(((m + 127) / 128) * ((n + 127) / 128), g.k, m, n, exact);
     if (g.splits > 0) {
         g.k_per_split = (blocks + g.splits - 1) / g.splits * kTileDim;
         g.splits = (int32_t)((g.k + g.k_per_split - 1) / g.k_per_split);
