@@ -291,34 +291,47 @@ int launch_tiles(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Splits of k, by modelled time in us: a block of a 128 x 128 tile takes 0.65, or 1.05
-// with bf16 instructions; splits cost a launch to join them and their sums' way out
-// and back (1013 x 1544 x 1008: 17 us in two splits, 10 in one; 100 x 4096 x 11008:
-// 62 and 25 in seven).
-int32_t splits_for(int64_t tiles, int64_t k, int64_t m, int64_t n, bool exact) {
+// Width of the tiles of a product that is too small for 256-wide ones, and splits of
+// k, by modelled time in us: a block of a 128 x 128 tile takes 0.7, or 1.35 with bf16
+// instructions, of a 128 x 64 one 0.6 of that; splits cost a launch to join them and
+// their sums' way out and back (1013 x 1544 x 1008: 17 us in two splits, 9 in one;
+// 100 x 4096 x 11008: 62 in one, 20 in seven).
+struct Small {
+    int32_t width, splits;
+};
+Small small_tiles(int64_t k, int64_t m, int64_t n, bool exact) {
     const int64_t blocks = (k + kTileDim - 1) / kTileDim;
-    int64_t best = 1;
+    Small best{128, 1};
     double least = 1e30;
-    for (int64_t s = 1; s <= 16 && s <= blocks && (s == 1 || (s * tiles <= kCus && s * m * n <= kMostSums)); ++s) {
-        const double time = (double)((blocks + s - 1) / s) * (exact ? 1.05 : 0.65) + (s > 1 ? 5.0 + (double)(s * m * n) * 8 / 4e6 : 0.0);
-        if (time < least) {
-            least = time;
-            best = s;
+    for (int32_t width : {128, 64}) {
+        const int64_t tiles = ((m + 127) / 128) * ((n + width - 1) / width);
+        const double step = (exact ? 1.35 : 0.7) * (width == 64 ? 0.6 : 1.0);
+        for (int64_t s = 1; s <= 16 && s <= blocks && (s == 1 || (s * tiles <= kCus && s * m * n <= kMostSums)); ++s) {
+            const double rounds = (double)((s * tiles + kCus - 1) / kCus);
+            const double time = rounds * (double)((blocks + s - 1) / s) * step + (s > 1 ? 5.0 + (double)(s * m * n) * 8 / 4e6 : 0.0);
+            if (time < least) {
+                least = time;
+                best = Small{width, (int32_t)s};
+            }
         }
     }
-    return (int32_t)best;
+    return best;
 }
 
+// Products with enough tiles of 256 x 256, or 256 x 128, to occupy the CUs.
+bool mid_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 127) / 128) >= 192; }
 bool wide_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256) >= 192; }
 
 template <bool kAKR, bool kBKR, bool kExact>
-int launch_product(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
+int launch_product(ProductArgs& g, const StoreEpilogue& e, int32_t width, hipStream_t stream) {
     if (wide_tiles(g.a.extent, g.b.extent)) {
         if constexpr (kExact) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, true, true>(g, e, stream);
         else return launch_tiles<kAKR, kBKR, 256, 256, 2, 4, 2, false, true>(g, e, stream);
     }
-    if (!kExact && ((g.a.extent + 255) / 256) * ((g.b.extent + 127) / 128) >= 192 && g.splits == 1) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, kExact, true>(g, e, stream);
-    if (((g.a.extent + 127) / 128) * ((g.b.extent + 127) / 128) * g.splits <= 256) return launch_tiles<kAKR, kBKR, 128, 128, 4, 2, 4, kExact, false>(g, e, stream);
+    if (!kExact && mid_tiles(g.a.extent, g.b.extent)) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, kExact, true>(g, e, stream);
+    // one workgroup a CU, eight waves and four blocks in flight, or two a CU
+    if (width == 64) return launch_tiles<kAKR, kBKR, 128, 64, 4, 2, 4, kExact, false>(g, e, stream);
+    if (((g.a.extent + 127) / 128) * ((g.b.extent + 127) / 128) * g.splits <= kCus) return launch_tiles<kAKR, kBKR, 128, 128, 4, 2, 4, kExact, false>(g, e, stream);
     return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, 2, kExact, false>(g, e, stream);
 }
 
@@ -329,16 +342,17 @@ int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* su
     StoreEpilogue e{a.out, a.out_ld, 0, m, n, a.out_type, a.accumulate, 0};
     e.vec = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_ld * size)) & 15u) == 0;
     const int64_t blocks = std::max<int64_t>(1, (g.k + kTileDim - 1) / kTileDim);
-    g.splits = g.k == 0 ? 0 : wide_tiles(m, n) ? 1 : splits_for(((m + 127) / 128) * ((n + 127) / 128), g.k, m, n, exact);
+    const Small small = wide_tiles(m, n) || (!exact && mid_tiles(m, n)) ? Small{128, 1} : small_tiles(g.k, m, n, exact);
+    g.splits = g.k == 0 ? 0 : small.splits;
     if (g.splits > 0) {
         g.k_per_split = (blocks + g.splits - 1) / g.splits * kTileDim;
         g.splits = (int32_t)((g.k + g.k_per_split - 1) / g.k_per_split);
     }
-    if (g.splits == 1) return exact ? launch_product<kAKR, kBKR, true>(g, e, stream) : launch_product<kAKR, kBKR, false>(g, e, stream);
+    if (g.splits == 1) return exact ? launch_product<kAKR, kBKR, true>(g, e, small.width, stream) : launch_product<kAKR, kBKR, false>(g, e, small.width, stream);
     const int64_t pieces = (m + 7) / 8;
     e.slab = pieces * 8 * n;
     const StoreEpilogue part{sums, pieces * 8, e.slab, pieces * 8, n, kF32, 0, 1};
-    const int rc = g.splits == 0 ? hipSuccess : exact ? launch_product<kAKR, kBKR, true>(g, part, stream) : launch_product<kAKR, kBKR, false>(g, part, stream);
+    const int rc = g.splits == 0 ? hipSuccess : exact ? launch_product<kAKR, kBKR, true>(g, part, small.width, stream) : launch_product<kAKR, kBKR, false>(g, part, small.width, stream);
     if (rc) return rc;
     const dim3 wgs((uint32_t)((n * pieces + kThreads - 1) / kThreads));
     if (a.out_type == kF32) hipLaunchKernelGGL((join_splits_kernel<float>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);
