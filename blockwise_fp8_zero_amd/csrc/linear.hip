@@ -20,7 +20,7 @@ constexpr int64_t kMostSums = int64_t(1) << 23;  // floats that the splits of a 
 constexpr int kRowsOfWave = 2, kRowsOfWg = kRowsOfWave * kThreads / 64, kGroupsOfWave = 4;
 
 template <class T>
-__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a, int32_t col_wgs, int32_t vec) {
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a, int32_t col_wgs) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t block = blockIdx.x;
     const int64_t c = (block % col_wgs) * (kGroupsOfWave * kTileDim) + 8 * lane;
@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a,
     float x[kRowsOfWave][8];
 #pragma unroll
     for (int k = 0; k < kRowsOfWave; ++k)
-        load8_any(static_cast<const T*>(a.x) + (r0 + k) * a.x_ld + c, r0 + k < a.n ? count : 0, vec, x[k]);
+        load8_any(static_cast<const T*>(a.x) + (r0 + k) * a.x_ld + c, r0 + k < a.n ? count : 0, x[k]);
 #pragma unroll
     for (int k = 0; k < kRowsOfWave; ++k) {
         const float scale = scale_of(row_max(abs_max8(x[k])), a.pow2);
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a,
 // Tiles: 16 lanes a row, the whole tile in registers, 4 rows a thread.
 constexpr int kTileThreads = 512, kTileRows = kTileDim * 16 / kTileThreads, kTileStep = kTileThreads / 16;
 template <class T>
-__global__ __launch_bounds__(kTileThreads) void quantize_tiles_kernel(QuantizeArgs a, int32_t col_tiles, int32_t vec) {
+__global__ __launch_bounds__(kTileThreads) void quantize_tiles_kernel(QuantizeArgs a, int32_t col_tiles) {
     __shared__ float tops[kTileThreads / 64];
     const int64_t i = blockIdx.x / col_tiles, j = blockIdx.x % col_tiles;
     const int64_t c = j * kTileDim + 8 * (threadIdx.x & 15);
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kTileThreads) void quantize_tiles_kernel(QuantizeAr
 #pragma unroll
     for (int k = 0; k < kTileRows; ++k) {
         const int64_t r = r0 + kTileStep * k;
-        load8_any(static_cast<const T*>(a.x) + r * a.x_ld + c, r < a.n ? count : 0, vec, x[k]);
+        load8_any(static_cast<const T*>(a.x) + r * a.x_ld + c, r < a.n ? count : 0, x[k]);
     }
 #pragma unroll
     for (int k = 0; k < kTileRows; ++k) top = fmaxf(top, abs_max8(x[k]));
@@ -83,13 +83,12 @@ __global__ __launch_bounds__(kTileThreads) void quantize_tiles_kernel(QuantizeAr
 
 template <class T>
 int quantize(const QuantizeArgs& a, hipStream_t stream) {
-    const int32_t vec = ((reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.x_ld * sizeof(T))) & 15u) == 0;
     if (a.tiles) {
         const int64_t wide = (a.dim + kTileDim - 1) / kTileDim, high = (a.n + kTileDim - 1) / kTileDim;
-        hipLaunchKernelGGL((quantize_tiles_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kTileThreads), 0, stream, a, (int32_t)wide, vec);
+        hipLaunchKernelGGL((quantize_tiles_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kTileThreads), 0, stream, a, (int32_t)wide);
     } else {
         const int64_t wide = (a.dim + kGroupsOfWave * kTileDim - 1) / (kGroupsOfWave * kTileDim), high = (a.n + kRowsOfWg - 1) / kRowsOfWg;
-        hipLaunchKernelGGL((quantize_rows_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kThreads), 0, stream, a, (int32_t)wide, vec);
+        hipLaunchKernelGGL((quantize_rows_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kThreads), 0, stream, a, (int32_t)wide);
     }
     return hipGetLastError();
 }
@@ -171,7 +170,7 @@ struct StoreEpilogue {
 // [token][block].
 struct RowInputs {
     const void* x;
-    int32_t type, vec;
+    int32_t type;
     int64_t ld;
     int32_t n, dim, width, blocks;
     template <class T>
@@ -181,7 +180,7 @@ struct RowInputs {
         for (int i = threadIdx.x; i < n * pieces; i += 64 * kFewKWaves) {
             const int token = i / pieces, c = 8 * (i - token * pieces);
             float y[8];
-            load8_any(static_cast<const T*>(x) + token * ld + c, min(8, max(0, dim - c)), vec, y);
+            load8_any(static_cast<const T*>(x) + token * ld + c, min(8, max(0, dim - c)), y);
             const float scale = scale_of(row_max(abs_max8(y)), false);
             uint32_t w[2];
             quantize8(y, Quotient(scale), w);
@@ -466,8 +465,7 @@ int launch_linear(const LinearArgs& given, void* work, void* stream) {
     g.blocks_k = wide;
     token_scales(g, a.x);
     if (a.n > kFewTokensMost) return product<false, false>(g, a, a.rows, a.n, static_cast<float*>(work), s);
-    const bool aligned = ((reinterpret_cast<uintptr_t>(a.values) | (uint64_t)(a.values_ld * dtype_size(a.values_type))) & 15u) == 0;
-    const RowInputs x{a.values, a.values_type, aligned, a.values_ld, (int32_t)a.n, (int32_t)a.cols, (int32_t)(wide * kTileDim), (int32_t)wide};
+    const RowInputs x{a.values, a.values_type, a.values_ld, (int32_t)a.n, (int32_t)a.cols, (int32_t)(wide * kTileDim), (int32_t)wide};
     return a.out_type == kF32 ? few_tokens<true>(g, inside ? &x : nullptr, e, s) : few_tokens<false>(g, inside ? &x : nullptr, e, s);
 }
 

@@ -2,6 +2,8 @@
 // tiles, for kernels that quantize as they go.
 #pragma once
 
+#include <type_traits>
+
 #include "ops_device.h"
 
 namespace bfz {
@@ -91,10 +93,25 @@ __device__ __forceinline__ float wave_max(float x) {
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
+// The first `count` of 8 elements, zeros for the others.  Loads of 16 bytes take any
+// element's boundary on this hardware (1013 x 1001 floats, element by element, 10 us;
+// so 5).
 template <class T>
-__device__ __forceinline__ void load8_any(const T* p, int count, bool vec, float (&x)[8]) {
-    if (vec && count >= 8) {
-        load8(p, x);
+__device__ __forceinline__ void load8_any(const T* p, int count, float (&x)[8]) {
+    if (count >= 8) {
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        typedef uint32_t on_words __attribute__((ext_vector_type(4), aligned(4)));
+        typedef uint32_t on_halves __attribute__((ext_vector_type(4), aligned(2)));
+        typedef std::conditional_t<sizeof(T) == 4, on_words, on_halves> loose;
+        const u32x4 a = *reinterpret_cast<const loose*>(p);
+        if constexpr (sizeof(T) == 4) {
+            const u32x4 b = *(reinterpret_cast<const loose*>(p) + 1);
+#pragma unroll
+            for (int l = 0; l < 8; ++l) x[l] = __uint_as_float(l < 4 ? a[l & 3] : b[l & 3]);
+        } else {
+#pragma unroll
+            for (int l = 0; l < 8; ++l) x[l] = Elem<T>::from_block(a, l);
+        }
         return;
     }
 #pragma unroll
