@@ -349,7 +349,7 @@ __device__ __forceinline__ void run_tile(const ProductArgs& g, const Epilogue& e
                 p[u] = Mul::run(av[j], b[u][j], j == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : p[u]);
                 if constexpr (kLast && j == kParts - 1) raw[u] = fb.read(cur, u);
                 if constexpr (j == 0 && u == 1 && kLast) issue(into, kNone, kParted);
-                if constexpr (j == 0 && u == 1 && t + 1 < kSpread) issue(into, std::integral_constant<int, t + 1>{}, kParted);
+                if constexpr (j == 0 && u == 1 && t + 1 < kSpread) issue(into, std::integral_constant<int, (t + 1) % kSpread>{}, kParted);
                 if constexpr (j == 0) {
                     scale_row(std::integral_constant<int, (t + kTM - 1) % kTM>{}, col);
                     if constexpr (t == 0) by[u] = now[u];
