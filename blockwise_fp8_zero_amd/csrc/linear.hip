@@ -12,7 +12,10 @@ namespace bfz {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kMostSums = int64_t(1) << 23;  // floats that the splits of a product may take
+constexpr int kCus = 256;
+// Floats that the splits of a product may take: splits and tiles of 128 by 128 at
+// most are one a CU.
+constexpr int64_t kMostSums = int64_t(kCus) * kTileDim * kTileDim;
 
 // ---- quantizer ------------------------------------------------------------------
 
@@ -238,8 +241,6 @@ __global__ __launch_bounds__(kThreads) void copy_weight_kernel(const uint8_t* __
 
 // ---- host -------------------------------------------------------------------------
 
-constexpr int kCus = 256;
-
 // Columns of n that go into whole tiles; the others go into tiles half as wide, so
 // that the last round of workgroups is a short one.  A half tile takes some 0.55 of
 // a whole one's time, and the CUs that the last whole tiles leave take it first.
@@ -305,7 +306,7 @@ Small small_tiles(int64_t k, int64_t m, int64_t n, bool exact) {
     for (int32_t width : {128, 64}) {
         const int64_t tiles = ((m + 127) / 128) * ((n + width - 1) / width);
         const double step = (exact ? 1.35 : 0.7) * (width == 64 ? 0.6 : 1.0);
-        for (int64_t s = 1; s <= 16 && s <= blocks && (s == 1 || (s * tiles <= kCus && s * m * n <= kMostSums)); ++s) {
+        for (int64_t s = 1; s <= 16 && s <= blocks && (s == 1 || s * tiles <= kCus); ++s) {
             const double rounds = (double)((s * tiles + kCus - 1) / kCus);
             const double time = rounds * (double)((blocks + s - 1) / s) * step + (s > 1 ? 5.0 + (double)(s * m * n) * 8 / 4e6 : 0.0);
             if (time < least) {
