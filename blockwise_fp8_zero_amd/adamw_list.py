@@ -76,12 +76,11 @@ class AdamWList:
     def _put(self, grads):
         if len(grads) != len(self.params):
             raise ValueError(f"grads: {len(grads)} tensors for {len(self.params)}")
-        words = self._words
-        for k, g in enumerate(grads):
-            at = _WORDS * k
-            code = self._array(g, "grads", k, words[at + 6])
-            words[at + 1] = g.data_ptr()
-            words[at + 7] = self._codes[k] | (code << 32)
+        # all are looked at before any is taken: a refused list leaves the last one
+        words, codes = self._words, [self._array(g, "grads", k, self._words[_WORDS * k + 6]) for k, g in enumerate(grads)]
+        for k, (g, code) in enumerate(zip(grads, codes)):
+            words[_WORDS * k + 1] = g.data_ptr()
+            words[_WORDS * k + 7] = self._codes[k] | (code << 32)
 
     def step(self, hp, grads=None, grad_scale=None, stream=None):
         """One step: hp, an AdamW or a dict of its fields; grads: float32,

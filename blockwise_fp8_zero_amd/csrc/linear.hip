@@ -207,21 +207,22 @@ struct RowInputs {
     }
 };
 
-// The sums of a split product: out = slabs added in their order.
+// The sums of a split product, out = slabs added in their order; zeros where there
+// is none.
 template <class O>
 __global__ __launch_bounds__(kThreads) void join_splits_kernel(const float* __restrict__ sums, int32_t splits, StoreEpilogue s) {
     const int64_t pieces = (s.m + 7) / 8;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= s.n * pieces) return;
-    const int64_t token = i / pieces, c = 8 * (i - token * pieces);
-    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int32_t k = 0; k < splits; ++k) {
-        float y[8];
-        load8(sums + k * s.slab + token * (pieces * 8) + c, y);
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < s.n * pieces; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t token = i / pieces, c = 8 * (i - token * pieces);
+        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        for (int32_t k = 0; k < splits; ++k) {
+            float y[8];
+            load8(sums + k * s.slab + token * (pieces * 8) + c, y);
 #pragma unroll
-        for (int l = 0; l < 8; ++l) x[l] += y[l];
+            for (int l = 0; l < 8; ++l) x[l] += y[l];
+        }
+        s.put(static_cast<O*>(s.out) + token * s.ld + c, c, x);
     }
-    s.put(static_cast<O*>(s.out) + token * s.ld + c, c, x);
 }
 
 // A weight whose rows the products cannot read in place, copied into rows of
@@ -240,6 +241,18 @@ __global__ __launch_bounds__(kThreads) void copy_weight_kernel(const uint8_t* __
 }
 
 // ---- host -------------------------------------------------------------------------
+
+// More than 64 KiB of LDS is allowed for a kernel once on each device.
+int allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess) return err;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (ready.load(std::memory_order_acquire) & bit)) return hipSuccess;
+    err = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == hipSuccess) ready.fetch_or(bit, std::memory_order_release);
+    return err;
+}
 
 // Columns of n that go into whole tiles; the others go into tiles half as wide, so
 // that the last round of workgroups is a short one.  A half tile takes some 0.55 of
@@ -272,12 +285,9 @@ template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN
 int launch_tiles(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
     constexpr int kLds = kStages * TileOf<kAKR, kBKR, kTileM, kTileN, kWavesM * kWavesN>::kStage;
     const auto kernel = codes_gemm_kernel<kAKR, kBKR, kTileM, kTileN, kWavesM, kWavesN, kStages, kExact, kHalves, StoreEpilogue>;
-    static std::atomic<bool> ready{false};
-    if (!ready.load(std::memory_order_relaxed)) {
-        const hipError_t rc = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-        if (rc != hipSuccess) return rc;
-        ready.store(true, std::memory_order_relaxed);
-    }
+    static std::atomic<uint64_t> ready{0};  // a bit for each device
+    const int rc = allow_lds(reinterpret_cast<const void*>(kernel), kLds, ready);
+    if (rc) return rc;
     g.tiles_m = (int32_t)((g.a.extent + kTileM - 1) / kTileM);
     g.tiles_n = (int32_t)((g.b.extent + kTileN - 1) / kTileN);
     g.group_m = std::min(g.tiles_m, 4);
@@ -354,7 +364,7 @@ int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* su
     const StoreEpilogue part{sums, pieces * 8, e.slab, pieces * 8, n, kF32, 0, 1};
     const int rc = g.splits == 0 ? hipSuccess : exact ? launch_product<kAKR, kBKR, true>(g, part, small.width, stream) : launch_product<kAKR, kBKR, false>(g, part, small.width, stream);
     if (rc) return rc;
-    const dim3 wgs((uint32_t)((n * pieces + kThreads - 1) / kThreads));
+    const dim3 wgs((uint32_t)std::min<int64_t>((n * pieces + kThreads - 1) / kThreads, 1 << 20));
     if (a.out_type == kF32) hipLaunchKernelGGL((join_splits_kernel<float>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);
     else if (a.out_type == kBF16) hipLaunchKernelGGL((join_splits_kernel<bf16_t>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);
     else hipLaunchKernelGGL((join_splits_kernel<f16_t>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);

@@ -245,3 +245,13 @@ def test_adamw_list_class(at_home):
             bfz.AdamWList(*args)
     with pytest.raises(ValueError):
         bfz.adamw_states(p, bits=16)
+
+
+def test_refused_gradients_leave_the_list_as_it_was(at_home):
+    p, g = [_z(300), _z(30)], [_z(300), _z(30)]
+    opt = bfz.AdamWList(p, [_z(300), _z(30)], [_z(300), _z(30)], grads=g)
+    before = list(opt._words)
+    hp = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=1)
+    with pytest.raises(ValueError):
+        opt.step(hp, grads=[_z(300, dtype=torch.bfloat16), _z(31)])
+    assert list(opt._words) == before
