@@ -1,4 +1,17 @@
 // AdamW over many tensors at once, states in 32 or 8 bits.
+//
+//   m' = b1 m + (1-b1) g,  v' = b2 v + (1-b2) g g
+//   p' = p - lr/(1-b1^t) m' / (sqrt(v') / sqrt(1-b2^t) + eps),  p' -= lr wd p'
+//
+// 8-bit states: E4M3 codes of m and of r = sqrt(v), which has half of v's range of
+// exponents, one scale for each 256 elements, made anew from m' and r' in the pass
+// that reads the old ones.  r rather than v also keeps a small root away from zero:
+// a positive one has a code.
+//
+// Bound by memory with 32-bit states: 256M elements, f32 parameters and bf16
+// gradients, 1.15 ms (6.0 TB/s); with 8-bit ones by memory and the four divisions
+// and the root an element has left, 0.69 ms (5.5 TB/s).  Few small tensors: 56 of
+// 100 elements 6 us, most of it the launch and fetching code.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

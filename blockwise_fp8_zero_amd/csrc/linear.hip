@@ -1,4 +1,18 @@
 // The linear layer in E4M3: quantizer of activations, and the three products.
+//
+//   code = E4M3(x / s), s = amax / 448 of 128 columns of a row or of a 128x128 tile
+//   y = X W^T,  dx = dY W,  dW = dY^T X, each value a code times its scale
+//
+// Quantizer: bound by memory, a group in registers between its largest value and its
+// codes; 8192 x 4096 bf16 by rows 18 us (5.6 TB/s), by tiles 19 us (5.2).
+//
+// Products, bound by the matrix cores (codes_gemm.h): forward and dx read the weight
+// and the codes as they lie, k along rows or across them; dW contracts over tokens
+// and reads both operands across.  8192 x 11008 x 4096: forward 328 us (2.25
+// PFLOP/s), dx 300 (2.46), dW in bf16 320 (2.3), in f32, by bf16 instructions, 650
+// (1.14); the library's product of two E4M3 matrices with one scale each runs at
+// 2.12 there.  Up to 64 tokens, bound by reading the weight: 4096 x 4096, 1 token 5.7
+// us (3.0 TB/s; 3.6 of it the bytes), 11008 x 4096, 64 tokens 17 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
