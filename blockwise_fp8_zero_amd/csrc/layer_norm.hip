@@ -13,11 +13,12 @@
 // adds: sums in an order that the sizes fix.
 //
 // 32768 x 4096 bf16: 100 us (5.4 TB/s), the gradient 153 (5.3, a copy reaches 4.8);
-// 3001 x 1001 floats 10 and 16 us, one row 3.3 of a 7 us call.  16384 x 1024: 14 and 24.
-// Beyond 16384 columns a thread's 32 elements spill (2000 x 20000: 170 and 427 us).
+// 3001 x 1001 floats 7.2 and 15.5 us, one row 3.3 of a 7 us call.  16384 x 1024: 14 and 24.
+// Beyond 16384 columns a thread's 32 elements spill (2000 x 20000: 170 and 427 us, 2000 x 20001: 179 and 447).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "layer_internal.h"
 #include "ops_device.h"
@@ -44,13 +45,15 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x;
 }
 
-// A thread's elements of a row.  kVec: pieces of 8 side by side, at 16-byte
-// boundaries; else 8 elements kLanes apart, which any alignment can load.  Either
-// way those within the row are the first of a piece.  kWide: an array may hold
-// 4-byte elements.
-template <int kLanes, int kPieces, bool kVec, bool kWide>
+// 16 bytes on any element's boundary, which this hardware's loads and stores take.
+typedef uint32_t on_words __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t on_halves __attribute__((ext_vector_type(4), aligned(2)));
+
+// A thread's elements of a row: pieces of 8 side by side, of which those within the
+// row are the first.  kWide: an array may hold 4-byte elements.
+template <int kLanes, int kPieces, bool kWide>
 struct Row {
-    static constexpr int kWords = kVec && !kWide ? 4 : 8;
+    static constexpr int kWords = kWide ? 8 : 4;
     struct Raw {
         uint32_t w[kPieces][kWords];
     };
@@ -58,33 +61,38 @@ struct Row {
     __device__ __forceinline__ Row(int lane, int dim) : lane(lane) {
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            const int left = kVec ? dim - (j * kLanes + lane) * 8 : (dim - j * 8 * kLanes - lane + kLanes - 1) / kLanes;
+            const int left = dim - column(j, 0);
             count[j] = left < 0 ? 0 : left > 8 ? 8 : left;
         }
     }
-    __device__ __forceinline__ int column(int j, int l) const { return kVec ? (j * kLanes + lane) * 8 + l : (j * 8 + l) * kLanes + lane; }
+    __device__ __forceinline__ int column(int j, int l) const { return (j * kLanes + lane) * 8 + l; }
     // loads only: what is loaded is converted when it is used
     __device__ __forceinline__ void load(const void* row, int type, Raw& r) const {
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            if constexpr (kVec) {
-                if (count[j] == 8) {
-                    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(row) + (int64_t)column(j, 0) * (kWide && type == kF32 ? 4 : 2));
-                    const u32x4 a = *p;
+            if (count[j] == 8) {
+                const char* p = static_cast<const char*>(row) + (int64_t)column(j, 0) * (kWide && type == kF32 ? 4 : 2);
+                if constexpr (kWide) {
+                    if (type != kF32) {
+                        const u32x4 a = *reinterpret_cast<const on_halves*>(p);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) r.w[j][i] = a[i];
-                    if constexpr (kWide) {
-                        if (type == kF32) {
-                            const u32x4 b = p[1];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) r.w[j][4 + i] = b[i];
-                        }
+                        for (int i = 0; i < 4; ++i) r.w[j][i] = a[i];
+                        continue;
                     }
-                    continue;
                 }
+                typedef std::conditional_t<kWide, on_words, on_halves> Read;
+                const u32x4 a = *reinterpret_cast<const Read*>(p);
 #pragma unroll
-                for (int i = 0; i < kWords; ++i) r.w[j][i] = 0;
+                for (int i = 0; i < 4; ++i) r.w[j][i] = a[i];
+                if constexpr (kWide) {
+                    const u32x4 b = reinterpret_cast<const Read*>(p)[1];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r.w[j][4 + i] = b[i];
+                }
+                continue;
             }
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) r.w[j][i] = 0;
 #pragma unroll
             for (int l = 0; l < 8; ++l) {
                 const int c = column(j, l);
@@ -93,8 +101,7 @@ struct Row {
                     if (kWide && type == kF32) x = static_cast<const uint32_t*>(row)[c];
                     else x = static_cast<const uint16_t*>(row)[c];
                 }
-                if constexpr (!kVec) r.w[j][l] = x;
-                else if (kWide && type == kF32) r.w[j][l & (kWords - 1)] = x;
+                if (kWide && type == kF32) r.w[j][l & (kWords - 1)] = x;
                 else r.w[j][l >> 1] |= x << (16 * (l & 1));
             }
         }
@@ -111,7 +118,7 @@ struct Row {
         for (int j = 0; j < kPieces; ++j)
 #pragma unroll
             for (int l = 0; l < 8; ++l) {
-                const uint32_t h = kVec ? r.w[j][l >> 1] >> (16 * (l & 1)) : r.w[j][l];
+                const uint32_t h = r.w[j][l >> 1] >> (16 * (l & 1));
                 if (type == kBF16) x[j][l] = __uint_as_float(h << 16);
                 else x[j][l] = (float)__builtin_bit_cast(f16_t, (uint16_t)h);
             }
@@ -120,10 +127,19 @@ struct Row {
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
             const int c = column(j, 0);
-            if (kVec && count[j] == 8) {
-                if (type == kF32) store8(static_cast<float*>(row) + c, x[j]);
-                else if (type == kBF16) store8(static_cast<bf16_t*>(row) + c, x[j]);
-                else store8(static_cast<f16_t*>(row) + c, x[j]);
+            if (count[j] == 8) {
+                if (type == kF32) {
+                    on_words* p = reinterpret_cast<on_words*>(static_cast<float*>(row) + c);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        p[h] = u32x4{__float_as_uint(x[j][4 * h]), __float_as_uint(x[j][4 * h + 1]), __float_as_uint(x[j][4 * h + 2]),
+                                     __float_as_uint(x[j][4 * h + 3])};
+                } else {
+                    u32x4 a;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[i] = type == kBF16 ? pack2<bf16_t>(x[j][2 * i], x[j][2 * i + 1]) : pack2<f16_t>(x[j][2 * i], x[j][2 * i + 1]);
+                    *reinterpret_cast<on_halves*>(static_cast<uint16_t*>(row) + c) = a;
+                }
             } else {
 #pragma unroll
                 for (int l = 0; l < 8; ++l)
@@ -138,7 +154,7 @@ struct Row {
 #pragma unroll
         for (int j = 0; j < kMany; ++j) {
             const int c = column(j0 + j, 0);
-            if (kVec && p && count[j0 + j] == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+            if (p && count[j0 + j] == 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
                 if (type == kF32) load8(static_cast<const float*>(p) + c, x[j]);
                 else if (type == kBF16) load8(static_cast<const bf16_t*>(p) + c, x[j]);
                 else load8(static_cast<const f16_t*>(p) + c, x[j]);
@@ -178,12 +194,12 @@ __device__ __forceinline__ const char* row_of(const void* p, int type, int64_t r
 
 constexpr int most(int a, int b) { return a > b ? a : b; }
 
-template <int kLanes, int kPieces, bool kVec, bool kWide>
+template <int kLanes, int kPieces, bool kWide>
 __global__ __launch_bounds__(most(kLanes, 256)) void layer_norm_kernel(LayerNormArgs a) {
     constexpr int kRows = most(kLanes, 256) / kLanes;
     __shared__ float lds[2][kRows][kLanes / 64];
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    typedef Row<kLanes, kPieces, kVec, kWide> Mine;
+    typedef Row<kLanes, kPieces, kWide> Mine;
     const Mine row(lane, (int)a.dim);
     const int64_t step = (int64_t)gridDim.x * kRows;
     const float scale = 1.0f / (float)a.dim;
@@ -250,14 +266,14 @@ __device__ __forceinline__ void put_param(const LayerNormGradArgs& a, int k, int
 // few partial rows leave.
 constexpr int kGradThreads = 1024;
 
-template <int kLanes, int kPieces, bool kVec, bool kWide>
+template <int kLanes, int kPieces, bool kWide>
 __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(LayerNormGradArgs a, float* partial) {
     constexpr int kRows = kGradThreads / kLanes, kWaves = kLanes / 64;
     constexpr bool kAhead = kPieces == 1 || (kPieces == 2 && !kWide);  // the next row's loads under way: where registers allow
     __shared__ float lds[2][kRows][2 * kWaves];
     __shared__ float sums[kRows][8][kLanes];
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    typedef Row<kLanes, kPieces, kVec, kWide> Mine;
+    typedef Row<kLanes, kPieces, kWide> Mine;
     const Mine row(lane, (int)a.dim);
     const int64_t step = (int64_t)gridDim.x * kRows;
     const float scale = 1.0f / (float)a.dim;
@@ -330,12 +346,11 @@ __global__ __launch_bounds__(kGradThreads) void layer_norm_grad_kernel(LayerNorm
             for (int l = 0; l < 8; ++l) sums[group][l][lane] = x[l];
             __syncthreads();
             for (int i = threadIdx.x; i < 8 * kLanes; i += kGradThreads) {
-                // neighbours write side by side where a thread's columns do
-                const int of = kVec ? i >> 3 : i % kLanes, l = kVec ? i & 7 : i / kLanes;
+                const int of = i >> 3, l = i & 7;
                 float sum = 0.0f;
 #pragma unroll
                 for (int g = 0; g < kRows; ++g) sum += sums[g][l][of];
-                const int64_t c = kVec ? (j * kLanes + of) * 8 + l : (j * 8 + l) * kLanes + of;
+                const int64_t c = (j * kLanes + of) * 8 + l;
                 if (c >= a.dim) continue;
                 if (gridDim.x == 1) put_param(a, k, c, sum);
                 else partial[(int64_t)blockIdx.x * 2 * a.dim + k * a.dim + c] = sum;
@@ -371,10 +386,6 @@ __global__ __launch_bounds__(kJoinColumns* kJoinSlices) void join_params_kernel(
 
 // ---- host -------------------------------------------------------------------------
 
-bool aligned16(const void* p, int64_t ld, int type) {
-    return ((reinterpret_cast<uintptr_t>(p) | (uint64_t)(ld * dtype_size(type))) & 15u) == 0;
-}
-
 // Calls f(threads of a row, pieces of 8 elements a thread) with the first of
 // these that hold dim columns.
 template <class F>
@@ -403,10 +414,8 @@ int with_grad_shape(int64_t dim, F&& f) {
 }
 
 template <class F>
-int with_flags(bool vec, bool wide, F&& f) {
-    using std::bool_constant;
-    if (vec) return wide ? f(bool_constant<true>{}, bool_constant<true>{}) : f(bool_constant<true>{}, bool_constant<false>{});
-    return wide ? f(bool_constant<false>{}, bool_constant<true>{}) : f(bool_constant<false>{}, bool_constant<false>{});
+int with_width(bool wide, F&& f) {
+    return wide ? f(std::true_type{}) : f(std::false_type{});
 }
 
 // Workgroups of the gradient: one a CU, or one for every two rows of each
@@ -417,13 +426,12 @@ int64_t grad_wgs(int64_t n, int64_t rows) { return std::max<int64_t>(1, std::min
 }  // namespace
 
 int launch_layer_norm(const LayerNormArgs& a, void* stream) {
-    const bool vec = aligned16(a.x, a.x_ld, a.x_type) && aligned16(a.out, a.out_ld, a.out_type);
     return with_shape(a.dim, [&](auto lanes, auto pieces) {
-        return with_flags(vec, a.x_type == kF32, [&](auto v, auto wide) {
+        return with_width(a.x_type == kF32, [&](auto wide) {
             constexpr int kLanes = decltype(lanes)::value, kPieces = decltype(pieces)::value, kThreads = most(kLanes, 256);
             constexpr int64_t kRows = kThreads / kLanes;
             const int64_t wgs = std::min<int64_t>((a.n + kRows - 1) / kRows, 256 * 2048 / kThreads);
-            hipLaunchKernelGGL((layer_norm_kernel<kLanes, kPieces, decltype(v)::value, decltype(wide)::value>), dim3((uint32_t)wgs),
+            hipLaunchKernelGGL((layer_norm_kernel<kLanes, kPieces, decltype(wide)::value>), dim3((uint32_t)wgs),
                                dim3(kThreads), 0, (hipStream_t)stream, a);
             return (int)hipGetLastError();
         });
@@ -440,16 +448,14 @@ int64_t layer_norm_work_bytes(int64_t n, int64_t dim) {
 }
 
 int launch_layer_norm_grad(const LayerNormGradArgs& a, void* work, void* stream) {
-    const bool vec = aligned16(a.x, a.x_ld, a.x_type) && aligned16(a.dout, a.dout_ld, a.dout_type) &&
-                     (!a.dx || aligned16(a.dx, a.dx_ld, a.dx_type));
     float* partial = a.dweight || a.dbias ? static_cast<float*>(work) : nullptr;
     if (!partial && !a.dx) return hipSuccess;
     int64_t wgs = 0;
     const int rc = with_grad_shape(a.dim, [&](auto lanes, auto pieces) {
-        return with_flags(vec, a.x_type == kF32 || a.dout_type == kF32, [&](auto v, auto wide) {
+        return with_width(a.x_type == kF32 || a.dout_type == kF32, [&](auto wide) {
             constexpr int kLanes = decltype(lanes)::value, kPieces = decltype(pieces)::value;
             wgs = grad_wgs(a.n, kGradThreads / kLanes);
-            hipLaunchKernelGGL((layer_norm_grad_kernel<kLanes, kPieces, decltype(v)::value, decltype(wide)::value>), dim3((uint32_t)wgs),
+            hipLaunchKernelGGL((layer_norm_grad_kernel<kLanes, kPieces, decltype(wide)::value>), dim3((uint32_t)wgs),
                                dim3(kGradThreads), 0, (hipStream_t)stream, a, partial);
             return (int)hipGetLastError();
         });
