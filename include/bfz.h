@@ -577,11 +577,12 @@ int bfz_quantize(const void* x, int32_t x_dtype, int64_t x_ld, int64_t n, int64_
  *               scale_x(t, k) grid(o / 128, k) sum_i x[t][i] weight[o][i]
  * Sums of a block and over blocks are binary32, each in an order that the
  * sizes fix; the products of two scales are binary32 and must not overflow.
- * The result is rounded once to out's type.  A block's products are those of the
- * E4M3 matrix instructions for BFZ_BF16 and BFZ_F16 results: groups of 8 are
- * aligned to their largest and cut off 13 bits below its exponent, some 5e-5 of a
- * result.  A BFZ_F32 result, which would show that, is made of exact products by
- * bf16 instructions, at half the rate.
+ * The result is rounded once to out's type.  BFZ_F32 and BFZ_F16 results, and those
+ * of up to 16 tokens, are made of exact products by bf16 instructions.  A block's
+ * products of other BFZ_BF16 results are those of the E4M3 matrix instructions, at
+ * twice the rate: groups of 8 are aligned to their largest and cut off 13 bits below
+ * its exponent, towards zero, some 5e-5 of a result whose rounding is 1.7e-3.  Where
+ * large products cancel that shows; a caller to whom it matters takes BFZ_F32 results.
  * x: [n, cols], E4M3 codes as bfz_quantize leaves them (zeros up to the next
  * multiple of 16 columns) with their scales in its row (tiles == 0) or tile
  * form; or BFZ_F32, BFZ_BF16 or BFZ_F16 values with scales NULL and tiles 0,
@@ -612,7 +613,8 @@ int bfz_linear(const void* x, int32_t x_dtype, int64_t x_ld, const float* scales
  *   bfz_linear_grad_weight:  dweight = dOut^T X  [rows, cols], likewise
  * The first takes dout's scales in either form, the second both operands' in
  * the tile form, whose scales hold whichever way a tile is read: the codes that
- * the forward product read serve here, and no transposed copy is made.
+ * the forward product read serve here, and no transposed copy is made.  BFZ_BF16
+ * gradients take the E4M3 instructions whatever n is.
  * accumulate adds in binary32 before the one rounding.  dweight with n = 0 is
  * zero.  Other arguments, limits and errors as above.
  */
