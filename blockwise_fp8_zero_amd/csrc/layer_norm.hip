@@ -3,9 +3,12 @@
 //   h = (x - mean) rstd,  out = h weight + bias,  g = dout weight
 //   dx = rstd (g - mean(g) - h mean(g h)),  dweight = sum dout h,  dbias = sum dout
 //
-// Bound by memory: a row is read once, kept in registers while its sums are made
-// (the variance as the mean of (x - mean)^2, in two steps, so that a large common
-// offset costs nothing), and written once.  A row belongs to 64 to 1024 threads
+// Bound by memory: a row is read once, kept in registers while its sums are made,
+// and written once.  The sums take two steps, so that a large common offset costs
+// nothing but its own rounding in the mean that is kept: the mean; then the mean of
+// what is left, by which the first one was off (up to 52 roundings of the offset:
+// a constant row of 16321.2 in 11008 columns came out as 0.88 instead of 0), and of
+// its square, less the square of that.  A row belongs to 64 to 1024 threads
 // with 8 or 16 (32 beyond 16384 columns) of its elements each; workgroups walk
 // rows, the next row's loads under way while one is summed, and keep weight and
 // bias, and in the gradient their columns' sums for dweight and dbias, in
@@ -13,8 +16,9 @@
 // adds: sums in an order that the sizes fix.
 //
 // 32768 x 4096 bf16: 100 us (5.4 TB/s), the gradient 153 (5.3, a copy reaches 4.8);
-// 3001 x 1001 floats 7.2 and 15.5 us, one row 3.3 of a 7 us call.  16384 x 1024: 14 and 24.
-// Beyond 16384 columns a thread's 32 elements spill (2000 x 20000: 170 and 427 us, 2000 x 20001: 179 and 447).
+// 3001 x 1001 floats 7.2 and 15.5 us, one row 3.3 of a 7 us call.  16384 x 1024: 15 and 24.
+// Taking the first mean's error off costs 1% of the largest, 3% of 16384 x 1024.
+// Beyond 16384 columns a thread's 32 elements spill (2000 x 20000: 131 and 427 us, 2000 x 20001: 128 and 447).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -199,7 +203,7 @@ constexpr int most(int a, int b) { return a > b ? a : b; }
 template <int kLanes, int kPieces, bool kWide>
 __global__ __launch_bounds__(most(kLanes, 256)) void layer_norm_kernel(LayerNormArgs a) {
     constexpr int kRows = most(kLanes, 256) / kLanes;
-    __shared__ float lds[2][kRows][kLanes / 64];
+    __shared__ float lds[kRows][3 * (kLanes / 64)];
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
     typedef Row<kLanes, kPieces, kWide> Mine;
     const Mine row(lane, (int)a.dim);
@@ -217,39 +221,49 @@ __global__ __launch_bounds__(most(kLanes, 256)) void layer_norm_kernel(LayerNorm
     // the same number of turns for all rows of a workgroup, which share barriers
     for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.n; r0 += step, r += step) {
         float x[kPieces][8];
-        if constexpr (!kKeep) row.load(row_of(a.x, a.x_type, min(r, a.n - 1), a.x_ld), a.x_type, raw);
-        row.values(raw, a.x_type, x);
+        Mine now = row;
+        // four pieces' addresses, made anew in each turn: kept from one to the next,
+        // they spill, with them the row (2000 x 20000 bf16: 219 us instead of 131)
+        if constexpr (!kKeep) __asm__ volatile("" : "+v"(now.lane));
+        if constexpr (!kKeep) now.load(row_of(a.x, a.x_type, min(r, a.n - 1), a.x_ld), a.x_type, raw);
+        now.values(raw, a.x_type, x);
         if constexpr (kKeep) {
-            if (r0 + step < a.n) row.load(row_of(a.x, a.x_type, min(r + step, a.n - 1), a.x_ld), a.x_type, raw);
+            if (r0 + step < a.n) now.load(row_of(a.x, a.x_type, min(r + step, a.n - 1), a.x_ld), a.x_type, raw);
         }
         float sum[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < kPieces; ++j)
 #pragma unroll
             for (int l = 0; l < 8; ++l) sum[0] += x[j][l];
-        row_sums<kLanes>(sum, lds[0][group], lane);
-        const float mean = sum[0] * scale;
-        float square[1] = {0.0f};
+        row_sums<kLanes>(sum, lds[group], lane);
+        const float first = sum[0] * scale;
+        // of x - first, and of its square
+        float rest[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < kPieces; ++j)
 #pragma unroll
             for (int l = 0; l < 8; ++l) {
-                x[j][l] -= mean;
-                square[0] = __builtin_fmaf(l < row.count[j] ? x[j][l] : 0.0f, x[j][l], square[0]);
+                x[j][l] -= first;
+                const float mine = l < now.count[j] ? x[j][l] : 0.0f;
+                rest[0] += mine;
+                rest[1] = __builtin_fmaf(mine, mine, rest[1]);
             }
-        row_sums<kLanes>(square, lds[1][group], lane);
-        const float rstd = 1.0f / sqrtf(__builtin_fmaf(square[0], scale, a.eps));
+        row_sums<kLanes>(rest, lds[group] + kLanes / 64, lane);
+        const float off = rest[0] * scale, mean = first + off, square = rest[1] * scale;
+        // an infinite square (or NaN) stays
+        const float var = square < INFINITY ? fmaxf(__builtin_fmaf(-off, off, square), 0.0f) : square;
+        const float rstd = 1.0f / sqrtf(var + a.eps), shift = -off * rstd;
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
             if constexpr (!kKeep) {
-                row.params(a.weight, a.param_type, 1.0f, w, j);
-                row.params(a.bias, a.param_type, 0.0f, b, j);
+                now.params(a.weight, a.param_type, 1.0f, w, j);
+                now.params(a.bias, a.param_type, 0.0f, b, j);
             }
 #pragma unroll
-            for (int l = 0; l < 8; ++l) x[j][l] = __builtin_fmaf(x[j][l] * rstd, w[kKeep ? j : 0][l], b[kKeep ? j : 0][l]);
+            for (int l = 0; l < 8; ++l) x[j][l] = __builtin_fmaf(__builtin_fmaf(x[j][l], rstd, shift), w[kKeep ? j : 0][l], b[kKeep ? j : 0][l]);
         }
         if (r < a.n) {
-            row.store(const_cast<char*>(row_of(a.out, a.out_type, r, a.out_ld)), a.out_type, x);
+            now.store(const_cast<char*>(row_of(a.out, a.out_type, r, a.out_ld)), a.out_type, x);
             if (lane == 0) {
                 if (a.mean) a.mean[r] = mean;
                 if (a.rstd) a.rstd[r] = rstd;

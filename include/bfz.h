@@ -633,7 +633,9 @@ int bfz_linear_grad_weight(const uint8_t* dout, int64_t dout_ld, const float* do
  * Layer norm of rows:
  *   mean = sum x / dim,  rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps)
  *   out  = (x - mean) rstd weight + bias
- * in binary32, rounded once to out's type.  weight and bias: dim elements of
+ * in binary32, rounded once to out's type; the mean is corrected by that of what it
+ * leaves, so that a row's common offset costs no more than the rounding of the mean
+ * that is kept, and out not that.  weight and bias: dim elements of
  * param_dtype, each may be NULL (ones, zeros).  mean, rstd: n floats, for the
  * gradient, each may be NULL.  x, out: [n, dim], BFZ_F32, BFZ_BF16 or BFZ_F16,
  * any element alignment; out may be x itself when type and stride are equal.
