@@ -30,6 +30,12 @@ int check_matrix(const void* p, int dtype, int64_t rows, int64_t dim, int64_t ld
     return BFZ_OK;
 }
 
+int check_quantize(int64_t n, int64_t dim, int32_t tiles, const char* where) {
+    if (!quantize_fits(n, dim, tiles != 0))
+        return fail(BFZ_EINVAL, "%s: %lld rows of width %lld are too many for one call", where, (long long)n, (long long)dim);
+    return BFZ_OK;
+}
+
 // Codes that products read: rows on 16-byte boundaries, read to the next
 // multiple of 16 columns.
 int check_codes(const uint8_t* p, int64_t rows, int64_t dim, int64_t ld, const char* what, const char* where) {
@@ -90,9 +96,8 @@ extern "C" int bfz_quantize(const void* x, int32_t x_dtype, int64_t x_ld, int64_
     const char* where = "bfz_quantize";
     if (n < 0 || dim < 1 || n > kMostTokens || dim > kMostDim)
         return fail(BFZ_EINVAL, "%s: need 0 <= n <= 2^24, 1 <= dim <= 2^20", where);
-    if (blocks_of(n) * blocks_of(dim) >= (int64_t(1) << 23))
-        return fail(BFZ_EINVAL, "%s: %lld rows of width %lld are too many for one call", where, (long long)n, (long long)dim);
-    int rc = check_out(x, x_dtype, n, dim, x_ld, "x", where);
+    int rc = check_quantize(n, dim, tiles, where);
+    if (!rc) rc = check_out(x, x_dtype, n, dim, x_ld, "x", where);
     if (!rc) rc = check_codes(codes, n, dim, codes_ld, "codes", where);
     if (!rc) rc = check_scales(scales, scales_ld, tiles, n, dim, "scales", where);
     if (rc) return rc;
@@ -126,9 +131,8 @@ extern "C" int bfz_linear(const void* x, int32_t x_dtype, int64_t x_ld, const fl
     } else {
         if (scales || tiles) return fail(BFZ_EINVAL, "%s: only E4M3 codes come with scales", where);
         rc = check_out(x, x_dtype, n, cols, x_ld, "x", where);
+        if (!rc) rc = check_quantize(n, cols, 0, where);
         if (rc) return rc;
-        if (blocks_of(n) * blocks_of(cols) >= (int64_t(1) << 23))
-            return fail(BFZ_EINVAL, "%s: %lld rows of width %lld are too many for one call", where, (long long)n, (long long)cols);
         a.values = x;
         a.values_type = x_dtype;
         a.values_ld = x_ld;

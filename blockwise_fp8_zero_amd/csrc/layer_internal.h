@@ -21,6 +21,18 @@ struct QuantizeArgs {
 };
 int launch_quantize(const QuantizeArgs& a, void* stream);
 
+// The quantizer's workgroups: 8 rows by 512 columns with 256 threads, or a tile with
+// 512.  A launch counts its work-items in 32 bits.
+constexpr int kQuantizeRowsThreads = 256, kQuantizeTilesThreads = 512;
+constexpr int64_t kQuantizeRows = 8, kQuantizeCols = 512;
+inline int64_t quantize_wgs(int64_t n, int64_t dim, int tiles) {
+    const int64_t high = tiles ? kTileDim : kQuantizeRows, wide = tiles ? kTileDim : kQuantizeCols;
+    return ((n + high - 1) / high) * ((dim + wide - 1) / wide);
+}
+inline bool quantize_fits(int64_t n, int64_t dim, int tiles) {
+    return quantize_wgs(n, dim, tiles) < (int64_t(1) << 32) / (tiles ? kQuantizeTilesThreads : kQuantizeRowsThreads);
+}
+
 // ---- products ---------------------------------------------------------------
 
 // Codes of activations or of their gradients, [n, dim], with their scales in

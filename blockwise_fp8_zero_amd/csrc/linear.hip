@@ -35,6 +35,7 @@ constexpr int64_t kMostSums = int64_t(kCus) * kTileDim * kTileDim;
 
 // Row groups: 16 lanes hold a group, 8 columns each; a wave 4 groups of a row.
 constexpr int kRowsOfWave = 2, kRowsOfWg = kRowsOfWave * kThreads / 64, kGroupsOfWave = 4;
+static_assert(kThreads == kQuantizeRowsThreads && kRowsOfWg == kQuantizeRows && kGroupsOfWave * kTileDim == kQuantizeCols, "what the size checks count");
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a, int32_t col_wgs) {
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeArgs a,
 }
 
 // Tiles: 16 lanes a row, the whole tile in registers, 4 rows a thread.
-constexpr int kTileThreads = 512, kTileRows = kTileDim * 16 / kTileThreads, kTileStep = kTileThreads / 16;
+constexpr int kTileThreads = kQuantizeTilesThreads, kTileRows = kTileDim * 16 / kTileThreads, kTileStep = kTileThreads / 16;
 template <class T>
 __global__ __launch_bounds__(kTileThreads) void quantize_tiles_kernel(QuantizeArgs a, int32_t col_tiles) {
     __shared__ float tops[kTileThreads / 64];
@@ -100,12 +101,11 @@ __global__ __launch_bounds__(kTileThreads) void quantize_tiles_kernel(QuantizeAr
 
 template <class T>
 int quantize(const QuantizeArgs& a, hipStream_t stream) {
+    const dim3 wgs((uint32_t)quantize_wgs(a.n, a.dim, a.tiles));
     if (a.tiles) {
-        const int64_t wide = (a.dim + kTileDim - 1) / kTileDim, high = (a.n + kTileDim - 1) / kTileDim;
-        hipLaunchKernelGGL((quantize_tiles_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kTileThreads), 0, stream, a, (int32_t)wide);
+        hipLaunchKernelGGL((quantize_tiles_kernel<T>), wgs, dim3(kTileThreads), 0, stream, a, (int32_t)((a.dim + kTileDim - 1) / kTileDim));
     } else {
-        const int64_t wide = (a.dim + kGroupsOfWave * kTileDim - 1) / (kGroupsOfWave * kTileDim), high = (a.n + kRowsOfWg - 1) / kRowsOfWg;
-        hipLaunchKernelGGL((quantize_rows_kernel<T>), dim3((uint32_t)(wide * high)), dim3(kThreads), 0, stream, a, (int32_t)wide);
+        hipLaunchKernelGGL((quantize_rows_kernel<T>), wgs, dim3(kThreads), 0, stream, a, (int32_t)((a.dim + kQuantizeCols - 1) / kQuantizeCols));
     }
     return hipGetLastError();
 }

@@ -563,7 +563,9 @@ int bfz_vocab_loss_shape(int64_t n, int64_t vocab, int64_t dim, int32_t dweight_
  * zeros, others of a row left alone.  scales: rows scales_ld floats apart, of
  * [ceil(dim/128), n] for row groups, one row for each 128 columns, and of the
  * row-major grid [ceil(n/128), ceil(dim/128)] for tiles.
- * At most 2^24 rows, dim 2^20, codes_ld 2^21.
+ * At most 2^24 rows, dim 2^20, codes_ld 2^21; and as a launch counts its work-items
+ * in 32 bits, ceil(n/8) ceil(dim/512) < 2^24 for row groups (some 2^36 elements),
+ * ceil(n/128) ceil(dim/128) < 2^23 for tiles.
  * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
  */
 int bfz_quantize(const void* x, int32_t x_dtype, int64_t x_ld, int64_t n, int64_t dim,
@@ -596,7 +598,8 @@ int bfz_quantize(const void* x, int32_t x_dtype, int64_t x_ld, int64_t n, int64_
  * 256-byte aligned, not shared by calls that may run at the same time; copy != 0
  * where the weight's pointer or weight_ld is not a multiple of 16.  It serves
  * every smaller n, and with x_dtype BFZ_E4M3 both gradients.
- * At most 2^24 tokens, 2^20 rows and columns, strides of codes 2^21.
+ * At most 2^24 tokens, 2^20 rows and columns, strides of codes 2^21, and fewer than
+ * 2^23 pieces of 64 by 64 of a result; values within the limits of bfz_quantize.
  * Errors: BFZ_EINVAL, BFZ_EALIGN, BFZ_EHIP.
  */
 int64_t bfz_linear_work_bytes(int64_t n, int64_t rows, int64_t cols, int32_t x_dtype, int32_t copy);
