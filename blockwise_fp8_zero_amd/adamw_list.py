@@ -62,7 +62,7 @@ class AdamWList:
         self._codes = [self._words[_WORDS * k + 7] for k in range(len(params))]
         self.grads = None
         if grads is not None:
-            self._put(grads)
+            self._put(grads, self._words)
             self.grads = list(grads)
 
     def _array(self, t, name, k, n, codes=False):
@@ -73,11 +73,11 @@ class AdamWList:
             raise ValueError(f"{name}[{k}]: has {t.numel()} elements, needs {n}")
         return code
 
-    def _put(self, grads):
+    def _put(self, grads, words):
+        """The gradients' pointers and types into a table."""
         if len(grads) != len(self.params):
             raise ValueError(f"grads: {len(grads)} tensors for {len(self.params)}")
-        # all are looked at before any is taken: a refused list leaves the last one
-        words, codes = self._words, [self._array(g, "grads", k, self._words[_WORDS * k + 6]) for k, g in enumerate(grads)]
+        codes = [self._array(g, "grads", k, words[_WORDS * k + 6]) for k, g in enumerate(grads)]
         for k, (g, code) in enumerate(zip(grads, codes)):
             words[_WORDS * k + 1] = g.data_ptr()
             words[_WORDS * k + 7] = self._codes[k] | (code << 32)
@@ -89,15 +89,14 @@ class AdamWList:
         home = home_device()
         if self._home != home and self.params:
             elsewhere(self.params[0], "params", home)
+        words = self._words
         if grads is not None:
-            self._put(grads)
+            # a table of this call's own: another thread may be in a step of its own
+            words = type(words).from_buffer_copy(words)
+            self._put(grads, words)
         elif self.grads is None:
             raise ValueError("grads: the list has none of its own")
-        try:
-            rc = lib().bfz_adamw_list(self._words, len(self.params), C.byref(_hparams(hp)), scalar(grad_scale, "grad_scale", home),
-                                      raw_stream(stream, home))
-        finally:
-            if grads is not None and self.grads is not None:
-                self._put(self.grads)
+        rc = lib().bfz_adamw_list(words, len(self.params), C.byref(_hparams(hp)), scalar(grad_scale, "grad_scale", home),
+                                  raw_stream(stream, home))
         if rc:
             _check(rc)
