@@ -36,7 +36,7 @@ def _rows(t, name, home):
     if cols & 15 and rows:
         wide = -(-cols // 16) * 16
         if rows == 1:
-            ld = max(t.stride(0), wide)  # a single row's stride says nothing
+            ld = wide  # a single row's stride says nothing
         if t.storage_offset() + (rows - 1) * ld + wide > t.untyped_storage().nbytes():
             raise ValueError(f"{name}: rows have to reach to the next multiple of 16 columns (see quantize_buffers)")
     return p, rows, cols, ld
