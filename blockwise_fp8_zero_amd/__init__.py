@@ -101,6 +101,7 @@ def lib():
         L.bfz_linear.argtypes = [P, i32, i64, P, i64, i32, i64, P, i64, P, i64, i64, P, i32, i64, P, P]
         L.bfz_linear_grad_input.argtypes = [P, i64, P, i64, i32, i64, P, i64, P, i64, i64, P, i32, i64, i32, P, P]
         L.bfz_linear_grad_weight.argtypes = [P, i64, P, i64, P, i64, P, i64, i64, i64, i64, P, i32, i64, i32, P, P]
+        L.bfz_linear_shape.argtypes = [i32, i64, i64, i64, i32, P]
         L.bfz_layer_norm.argtypes = [P, i32, i64, i64, i64, P, P, i32, f32, P, i32, i64, P, P, P]
         L.bfz_layer_norm_work_bytes.argtypes = [i64, i64]
         L.bfz_layer_norm_work_bytes.restype = i64

@@ -295,72 +295,99 @@ int64_t whole_columns(int64_t tiles_m, int64_t n, int64_t width) {
     return best;
 }
 
-template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN, int kStages, bool kExact, bool kHalves>
-int launch_tiles(ProductArgs& g, const StoreEpilogue& e, hipStream_t stream) {
-    constexpr int kLds = kStages * TileOf<kAKR, kBKR, kTileM, kTileN, kWavesM * kWavesN>::kStage;
-    const auto kernel = codes_gemm_kernel<kAKR, kBKR, kTileM, kTileN, kWavesM, kWavesN, kStages, kExact, kHalves, StoreEpilogue>;
-    static std::atomic<uint64_t> ready{0};  // a bit for each device
-    const int rc = allow_lds(reinterpret_cast<const void*>(kernel), kLds, ready);
-    if (rc) return rc;
-    g.tiles_m = (int32_t)((g.a.extent + kTileM - 1) / kTileM);
-    g.tiles_n = (int32_t)((g.b.extent + kTileN - 1) / kTileN);
-    g.group_m = std::min(g.tiles_m, 4);
-    if constexpr (kHalves) {
-        const int64_t whole = whole_columns(g.tiles_m, g.b.extent, kTileN);
-        g.half_tiles_n = (int32_t)(std::max<int64_t>(0, g.b.extent - whole * kTileN + kTileN / 2 - 1) / (kTileN / 2));
-        g.tiles_n = (int32_t)whole;
-    }
-    const int64_t wgs = (int64_t)g.tiles_m * ((int64_t)g.tiles_n * g.splits + g.half_tiles_n);
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)wgs), dim3(64 * kWavesM * kWavesN), kLds, stream, g, e);
-    return hipGetLastError();
-}
-
-// Width of the tiles of a product that is too small for 256-wide ones, and splits of
-// k, by modelled time in us: a block of a 128 x 128 tile takes 0.7, or 1.35 with bf16
-// instructions, of a 128 x 64 one 0.6 of that; splits cost a launch to join them and
-// their sums' way out and back (1013 x 1544 x 1008: 17 us in two splits, 9 in one;
-// 100 x 4096 x 11008: 62 in one, 20 in seven).
+// Tiles of a product that is too small for 256-wide ones, and splits of k, by modelled
+// time in us: a round of workgroups takes `start` and `step` a block of k, as measured
+// at 2 to 86 blocks; splits cost a launch to join them and their sums' way out and
+// back.  (On 45 sizes of 3e7 to 8e10 products the choice was the fastest, but for
+// four by 4 to 16%.)  Modelled and measured, with bf16 instructions: 1013 x 1544 x 1008 11.8 and
+// 11.3 in tiles 64 wide, 16.8 and 14.7 in 128; 3000 x 1700 x 3600 56 and 57 in pairs
+// of workgroups, 81 and 76 in 64.  With E4M3 ones, 100 x 4096 x 11008 40.6 and 38.9 in
+// one, 19.9 and 19.5 in four splits; 1300 x 4096 x 4096 36 and 37 in pairs, 54 and 49
+// in 64.
+struct Form {
+    int32_t width, waves, of_cu;
+    double start[2], step[2];  // with E4M3 instructions, with bf16 ones
+};
+constexpr Form kForms[] = {
+    {128, 8, 1, {6.0, 8.0}, {0.6, 1.1}},
+    {128, 4, 2, {6.0, 10.0}, {0.95, 1.6}},
+    {64, 8, 1, {4.5, 6.0}, {0.42, 0.72}},
+};
 struct Small {
-    int32_t width, splits;
+    int32_t width, waves, splits;
 };
 Small small_tiles(int64_t k, int64_t m, int64_t n, bool exact) {
     const int64_t blocks = (k + kTileDim - 1) / kTileDim;
-    Small best{128, 1};
+    Small best{128, 8, 1};
     double least = 1e30;
-    for (int32_t width : {128, 64}) {
-        const int64_t tiles = ((m + 127) / 128) * ((n + width - 1) / width);
-        const double step = (exact ? 1.35 : 0.7) * (width == 64 ? 0.6 : 1.0);
-        for (int64_t s = 1; s <= 16 && s <= blocks && (s == 1 || s * tiles <= kCus); ++s) {
-            const double rounds = (double)((s * tiles + kCus - 1) / kCus);
-            const double time = rounds * (double)((blocks + s - 1) / s) * step + (s > 1 ? 5.0 + (double)(s * m * n) * 8 / 4e6 : 0.0);
+    for (const Form& f : kForms) {
+        const int64_t tiles = ((m + 127) / 128) * ((n + f.width - 1) / f.width);
+        // splits where one workgroup a CU holds them all
+        for (int64_t s = 1; s <= 16 && s <= std::max<int64_t>(1, blocks) && (s == 1 || (f.of_cu == 1 && s * tiles <= kCus)); ++s) {
+            const double rounds = (double)((s * tiles + f.of_cu * kCus - 1) / (f.of_cu * kCus));
+            const double join = s > 1 ? 3.5 + 0.3 * (double)s + (double)(s * m * n) * 8 / 6e6 : 0.0;
+            const double time = rounds * (f.start[exact] + (double)((blocks + s - 1) / s) * f.step[exact]) + join;
             if (time < least) {
                 least = time;
-                best = Small{width, (int32_t)s};
+                best = Small{f.width, f.waves, (int32_t)s};
             }
         }
     }
     return best;
 }
 
-// Products with enough tiles of 256 x 256, or 256 x 128, to occupy the CUs.
-bool mid_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 127) / 128) >= 192; }
-bool wide_tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256) >= 192; }
-
-template <bool kAKR, bool kBKR, bool kExact>
-int launch_product(ProductArgs& g, const StoreEpilogue& e, int32_t width, hipStream_t stream) {
-    if (wide_tiles(g.a.extent, g.b.extent)) {
-        if constexpr (kExact) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, true, true>(g, e, stream);
-        else return launch_tiles<kAKR, kBKR, 256, 256, 2, 4, 2, false, true>(g, e, stream);
-    }
-    if (!kExact && mid_tiles(g.a.extent, g.b.extent)) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, kExact, true>(g, e, stream);
-    // one workgroup a CU, eight waves and four blocks in flight, or two a CU
-    if (width == 64) return launch_tiles<kAKR, kBKR, 128, 64, 4, 2, 4, kExact, false>(g, e, stream);
-    if (((g.a.extent + 127) / 128) * ((g.b.extent + 127) / 128) * g.splits <= kCus) return launch_tiles<kAKR, kBKR, 128, 128, 4, 2, 4, kExact, false>(g, e, stream);
-    return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, 2, kExact, false>(g, e, stream);
-}
-
 // Results that would show what the E4M3 instructions cut off (codes_gemm.h).
 bool exact_products(int type) { return type != kBF16; }
+
+// How a product is cut: tiles of m x n with so many waves each, splits of k, columns
+// of whole tiles (the others are half as wide).
+struct Shape {
+    int32_t tile_m, tile_n, waves, splits;
+    int64_t k_per_split, whole;
+};
+
+// 256 x 256 or, with bf16 instructions, 256 x 128 where tiles of 256 x 256 occupy the
+// CUs; 256 x 128 where those do; else 128 x 64 or 128 x 128, one workgroup a CU with
+// eight waves and four blocks in flight, or two of four waves a CU.
+Shape shape_of(int64_t k, int64_t m, int64_t n, bool exact) {
+    const auto tiles = [&](int64_t high, int64_t wide) { return ((m + high - 1) / high) * ((n + wide - 1) / wide); };
+    const int64_t blocks = std::max<int64_t>(1, (k + kTileDim - 1) / kTileDim);
+    if (tiles(256, 256) >= 192 || (!exact && tiles(256, 128) >= 192)) {
+        const int32_t wide = tiles(256, 256) >= 192 && !exact ? 256 : 128;
+        return Shape{256, wide, 8, 1, blocks * kTileDim, whole_columns((m + 255) / 256, n, wide)};
+    }
+    const Small small = small_tiles(k, m, n, exact);
+    Shape s{128, small.width, small.waves, small.splits, (blocks + small.splits - 1) / small.splits * kTileDim, (n + small.width - 1) / small.width};
+    s.splits = (int32_t)((blocks * kTileDim + s.k_per_split - 1) / s.k_per_split);
+    return s;
+}
+
+template <bool kAKR, bool kBKR, int kTileM, int kTileN, int kWavesM, int kWavesN, int kStages, bool kExact, bool kHalves>
+int launch_tiles(ProductArgs& g, const StoreEpilogue& e, const Shape& shape, hipStream_t stream) {
+    constexpr int kLds = kStages * TileOf<kAKR, kBKR, kTileM, kTileN, kWavesM * kWavesN>::kStage;
+    const auto kernel = codes_gemm_kernel<kAKR, kBKR, kTileM, kTileN, kWavesM, kWavesN, kStages, kExact, kHalves, StoreEpilogue>;
+    static std::atomic<uint64_t> ready{0};  // a bit for each device
+    const int rc = allow_lds(reinterpret_cast<const void*>(kernel), kLds, ready);
+    if (rc) return rc;
+    g.tiles_m = (int32_t)((g.a.extent + kTileM - 1) / kTileM);
+    g.tiles_n = (int32_t)shape.whole;
+    g.group_m = std::min(g.tiles_m, 4);
+    g.half_tiles_n = (int32_t)(std::max<int64_t>(0, g.b.extent - shape.whole * kTileN + kTileN / 2 - 1) / (kTileN / 2));
+    const int64_t wgs = (int64_t)g.tiles_m * ((int64_t)g.tiles_n * g.splits + g.half_tiles_n);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)wgs), dim3(64 * kWavesM * kWavesN), kLds, stream, g, e);
+    return hipGetLastError();
+}
+
+template <bool kAKR, bool kBKR, bool kExact>
+int launch_product(ProductArgs& g, const StoreEpilogue& e, const Shape& shape, hipStream_t stream) {
+    if constexpr (!kExact) {
+        if (shape.tile_n == 256) return launch_tiles<kAKR, kBKR, 256, 256, 2, 4, 2, false, true>(g, e, shape, stream);
+    }
+    if (shape.tile_m == 256) return launch_tiles<kAKR, kBKR, 256, 128, 4, 2, 3, kExact, true>(g, e, shape, stream);
+    if (shape.tile_n == 64) return launch_tiles<kAKR, kBKR, 128, 64, 4, 2, 4, kExact, false>(g, e, shape, stream);
+    if (shape.waves == 8) return launch_tiles<kAKR, kBKR, 128, 128, 4, 2, 4, kExact, false>(g, e, shape, stream);
+    return launch_tiles<kAKR, kBKR, 128, 128, 2, 2, 2, kExact, false>(g, e, shape, stream);
+}
 
 template <bool kAKR, bool kBKR>
 int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* sums, hipStream_t stream) {
@@ -368,18 +395,14 @@ int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* su
     const int size = dtype_size(a.out_type);
     StoreEpilogue e{a.out, a.out_ld, 0, m, n, a.out_type, a.accumulate, 0};
     e.vec = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_ld * size)) & 15u) == 0;
-    const int64_t blocks = std::max<int64_t>(1, (g.k + kTileDim - 1) / kTileDim);
-    const Small small = wide_tiles(m, n) || (!exact && mid_tiles(m, n)) ? Small{128, 1} : small_tiles(g.k, m, n, exact);
-    g.splits = g.k == 0 ? 0 : small.splits;
-    if (g.splits > 0) {
-        g.k_per_split = (blocks + g.splits - 1) / g.splits * kTileDim;
-        g.splits = (int32_t)((g.k + g.k_per_split - 1) / g.k_per_split);
-    }
-    if (g.splits == 1) return exact ? launch_product<kAKR, kBKR, true>(g, e, small.width, stream) : launch_product<kAKR, kBKR, false>(g, e, small.width, stream);
+    const Shape shape = shape_of(g.k, m, n, exact);
+    g.splits = g.k == 0 ? 0 : shape.splits;
+    g.k_per_split = shape.k_per_split;
+    if (g.splits == 1) return exact ? launch_product<kAKR, kBKR, true>(g, e, shape, stream) : launch_product<kAKR, kBKR, false>(g, e, shape, stream);
     const int64_t pieces = (m + 7) / 8;
     e.slab = pieces * 8 * n;
     const StoreEpilogue part{sums, pieces * 8, e.slab, pieces * 8, n, kF32, 0, 1};
-    const int rc = g.splits == 0 ? hipSuccess : exact ? launch_product<kAKR, kBKR, true>(g, part, small.width, stream) : launch_product<kAKR, kBKR, false>(g, part, small.width, stream);
+    const int rc = g.splits == 0 ? hipSuccess : exact ? launch_product<kAKR, kBKR, true>(g, part, shape, stream) : launch_product<kAKR, kBKR, false>(g, part, shape, stream);
     if (rc) return rc;
     const dim3 wgs((uint32_t)std::min<int64_t>((n * pieces + kThreads - 1) / kThreads, 1 << 20));
     if (a.out_type == kF32) hipLaunchKernelGGL((join_splits_kernel<float>), wgs, dim3(kThreads), 0, stream, sums, g.splits, e);
@@ -399,25 +422,36 @@ int launch_few(const ProductArgs& g, const RowInputs& x, const StoreEpilogue& e,
     return hipGetLastError();
 }
 
-// As few rows a workgroup, 16 to 48, as still fit the device in one round: one
-// workgroup a CU with 33 tokens and more, whose registers and LDS leave no room for
-// a second, else two.
+// Tiles of 16 rows that a workgroup of few tokens takes, 16 tn of them at most: as
+// few, up to three, as still fit the device in one round.  A CU holds one workgroup
+// with 33 tokens and more, whose registers and LDS leave no room for a second, else
+// two.  More than 12288 rows, or 16384 with up to 32 tokens, take further rounds: a
+// fourth tile, or a third there, is not tried.
+int32_t few_tiles(int64_t m, int32_t tn) {
+    if (m <= 16 * kCus) return 1;
+    return tn < 4 || m <= 2 * 16 * kCus ? 2 : 3;
+}
+
 template <int kTN, bool kExact, bool kQuantize>
 int few_rows(const ProductArgs& g, const RowInputs& x, const StoreEpilogue& e, hipStream_t stream) {
-    constexpr int64_t kRound = 16 * kCus * (kTN == 4 ? 1 : 2);
-    if (e.m <= 16 * kCus) return launch_few<1, kTN, kExact, kQuantize>(g, x, e, stream);
-    if (kTN < 4 || e.m <= 2 * kRound) return launch_few<2, kTN, kExact, kQuantize>(g, x, e, stream);
-    return launch_few<3, kTN, kExact, kQuantize>(g, x, e, stream);
+    const int32_t tiles = few_tiles(e.m, kTN);
+    if (tiles == 1) return launch_few<1, kTN, kExact, kQuantize>(g, x, e, stream);
+    if constexpr (kTN == 4) {
+        if (tiles == 3) return launch_few<3, kTN, kExact, kQuantize>(g, x, e, stream);
+    }
+    return launch_few<2, kTN, kExact, kQuantize>(g, x, e, stream);
 }
 
 // Up to 16 tokens the weight's bytes decide, and exact products cost a bfloat16
 // result 2 to 5% (1 token on 4096 x 4096: 5.1 us instead of 4.9, 16 on 28672 x 8192:
 // 48.4 instead of 48.0).  Beyond them they would cost it 10 to 40% (64 on 11008 x
 // 4096: 21 us instead of 17, 33 on 28672 x 8192: 102 instead of 67).
+bool exact_few(int type, int64_t n) { return n <= 16 || exact_products(type); }
+
 int few_tokens(const ProductArgs& g, const RowInputs* x, const StoreEpilogue& e, hipStream_t stream) {
     if (x) return few_rows<1, true, true>(g, *x, e, stream);
     const RowInputs none{};
-    const bool exact = exact_products(e.type);
+    const bool exact = exact_few(e.type, e.n);
     if (e.n <= 16) return few_rows<1, true, false>(g, none, e, stream);
     if (e.n <= 32) return exact ? few_rows<2, true, false>(g, none, e, stream) : few_rows<2, false, false>(g, none, e, stream);
     return exact ? few_rows<4, true, false>(g, none, e, stream) : few_rows<4, false, false>(g, none, e, stream);
@@ -537,3 +571,24 @@ int launch_linear_grad_weight(const LinearArgs& a, void* work, void* stream) {
 }
 
 }  // namespace bfz
+
+extern "C" int bfz_linear_shape(int32_t product, int64_t n, int64_t rows, int64_t cols, int32_t out_dtype, int64_t* shape) {
+    using namespace bfz;
+    if (!shape || product < 0 || product > 2 || n < 1 || rows < 1 || cols < 1 || n > (int64_t(1) << 24) || rows > (int64_t(1) << 20) ||
+        cols > (int64_t(1) << 20) || (out_dtype != kF32 && out_dtype != kBF16 && out_dtype != kF16))
+        return fail(BFZ_EINVAL, "bfz_linear_shape: null pointer, bad sizes or types");
+    const int64_t m = product == 0 ? rows : cols, across = product == 2 ? rows : n, k = product == 0 ? cols : product == 1 ? rows : n;
+    int64_t out[6];
+    if (product == 0 && n <= kFewTokensMost) {
+        const int32_t tn = n <= 16 ? 1 : n <= 32 ? 2 : 4;
+        const int64_t few[6] = {16 * few_tiles(m, tn), 16 * tn, kFewKWaves, 1, n, exact_few(out_dtype, n)};
+        std::copy(few, few + 6, out);
+    } else {
+        const bool exact = exact_products(out_dtype);
+        const Shape s = shape_of(k, m, across, exact);
+        const int64_t cut[6] = {s.tile_m, s.tile_n, s.waves, s.splits, std::min<int64_t>(across, s.whole * s.tile_n), exact};
+        std::copy(cut, cut + 6, out);
+    }
+    std::copy(out, out + 6, shape);
+    return BFZ_OK;
+}

@@ -633,6 +633,16 @@ int bfz_linear_grad_weight(const uint8_t* dout, int64_t dout_ld, const float* do
                            int64_t dweight_ld, int32_t accumulate, void* work, void* stream);
 
 /*
+ * How the products of these sizes are cut (product: 0 forward, 1 gradient of the
+ * input, 2 of the weight), for tests and timing.  shape: 6 numbers, a tile's extent
+ * along the result's rows' elements and across its rows, waves of a workgroup, splits
+ * of the sum, rows of the result that go into whole tiles (others into tiles half as
+ * high), and 1 for exact products.  Host only.  Errors: BFZ_EINVAL.
+ */
+int bfz_linear_shape(int32_t product, int64_t n, int64_t rows, int64_t cols, int32_t out_dtype,
+                     int64_t* shape);
+
+/*
  * Layer norm of rows:
  *   mean = sum x / dim,  rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps)
  *   out  = (x - mean) rstd weight + bias
