@@ -116,7 +116,7 @@ __device__ __forceinline__ Raw encode(const float (&x)[4], bool positive, float&
 #pragma unroll
     for (int l = 0; l < 4; ++l) y[l] = q.direct ? q.slow(x[l]) : q.fast(x[l]);
     uint32_t w = codes_of(y[0], y[1], y[2], y[3]);
-    if (positive) {
+    if (positive && scale < INFINITY) {  // a block with an infinity is NaN, zeros of it times its scale
 #pragma unroll
         for (int l = 0; l < 4; ++l)
             if (x[l] > 0.0f && ((w >> (8 * l)) & 0xFFu) == 0u) w |= 1u << (8 * l);
