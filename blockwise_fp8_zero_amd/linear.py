@@ -85,7 +85,9 @@ def linear_workspace(n, weight, x_dtype=None, device=None):
     import torch
     _tensors._load()
     rows, cols = weight.shape
-    code = E4M3 if x_dtype is None else _tensors._codes[x_dtype]
+    code = E4M3 if x_dtype is None else _tensors._codes.get(x_dtype)
+    if code is None:
+        raise TypeError(f"x_dtype: {x_dtype} is none of {', '.join(str(x) for x in _tensors._codes)}")
     copy = (weight.data_ptr() | (weight.stride(0) if rows > 1 else 0)) & 15
     need = _work_bytes(int(n), rows, cols, code, int(copy != 0))
     return torch.empty(max(256, need), dtype=torch.uint8, device=weight.device if device is None else device)
