@@ -4,7 +4,7 @@ plain integers here: at the smallest sizes a call costs what its arguments do.
 Each tensor's device is compared with `home`, the device that is current at the
 call's start: a kernel launched there could not follow another one's pointers.
 """
-F32, BF16, F16, E4M3, F32_ROUNDED = 0, 1, 2, 3, 4
+F32, BF16, F16, E4M3, F32_ROUNDED, BF16_EXACT = 0, 1, 2, 3, 4, 5
 
 _torch = _floats = _codes = _raw = None
 _ready = False

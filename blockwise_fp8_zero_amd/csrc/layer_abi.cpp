@@ -89,6 +89,12 @@ int check_out(const void* out, int32_t dtype, int64_t rows, int64_t dim, int64_t
     return check_matrix(out, dtype, rows, dim, ld, int64_t(1) << 32, what, where);
 }
 
+// The type of a product's result, and whether exact products are asked for.
+int32_t result_type(int32_t dtype, int32_t* exact) {
+    *exact = dtype == BFZ_BF16_EXACT;
+    return *exact ? kBF16 : dtype;
+}
+
 }  // namespace
 
 extern "C" int bfz_quantize(const void* x, int32_t x_dtype, int64_t x_ld, int64_t n, int64_t dim, int32_t tiles, int32_t pow2,
@@ -116,6 +122,8 @@ extern "C" int bfz_linear(const void* x, int32_t x_dtype, int64_t x_ld, const fl
                           const uint8_t* weight, int64_t weight_ld, const float* grid, int64_t rows, int64_t cols, void* out,
                           int32_t out_dtype, int64_t out_ld, void* work, void* stream) {
     const char* where = "bfz_linear";
+    int32_t exact;
+    out_dtype = result_type(out_dtype, &exact);
     int rc = check_sizes(n, rows, cols, where);
     if (!rc) rc = check_tiles(rows, n, where);
     if (!rc) rc = check_weight(weight, weight_ld, grid, rows, cols, where);
@@ -144,6 +152,7 @@ extern "C" int bfz_linear(const void* x, int32_t x_dtype, int64_t x_ld, const fl
     a.rows = rows;
     a.cols = cols;
     a.out = out;
+    a.exact = exact;
     a.out_type = out_dtype;
     a.out_ld = out_ld;
     return n == 0 ? BFZ_OK : launched(where, launch_linear(a, work, stream));
@@ -153,6 +162,8 @@ extern "C" int bfz_linear_grad_input(const uint8_t* dout, int64_t dout_ld, const
                                      const uint8_t* weight, int64_t weight_ld, const float* grid, int64_t rows, int64_t cols, void* dx,
                                      int32_t dx_dtype, int64_t dx_ld, int32_t accumulate, void* work, void* stream) {
     const char* where = "bfz_linear_grad_input";
+    int32_t exact;
+    dx_dtype = result_type(dx_dtype, &exact);
     int rc = check_sizes(n, rows, cols, where);
     if (!rc) rc = check_tiles(cols, n, where);
     if (!rc) rc = check_weight(weight, weight_ld, grid, rows, cols, where);
@@ -170,6 +181,7 @@ extern "C" int bfz_linear_grad_input(const uint8_t* dout, int64_t dout_ld, const
     a.rows = rows;
     a.cols = cols;
     a.out = dx;
+    a.exact = exact;
     a.out_type = dx_dtype;
     a.out_ld = dx_ld;
     a.accumulate = accumulate != 0;
@@ -181,6 +193,8 @@ extern "C" int bfz_linear_grad_weight(const uint8_t* dout, int64_t dout_ld, cons
                                       void* dweight, int32_t dweight_dtype, int64_t dweight_ld, int32_t accumulate, void* work,
                                       void* stream) {
     const char* where = "bfz_linear_grad_weight";
+    int32_t exact;
+    dweight_dtype = result_type(dweight_dtype, &exact);
     int rc = check_sizes(n, rows, cols, where);
     if (!rc) rc = check_tiles(cols, rows, where);
     if (!rc) rc = check_codes(dout, n, rows, dout_ld, "dout", where);
@@ -198,6 +212,7 @@ extern "C" int bfz_linear_grad_weight(const uint8_t* dout, int64_t dout_ld, cons
     a.rows = rows;
     a.cols = cols;
     a.out = dweight;
+    a.exact = exact;
     a.out_type = dweight_dtype;
     a.out_ld = dweight_ld;
     a.accumulate = accumulate != 0;

@@ -56,7 +56,7 @@ struct LinearArgs {
     int64_t weight_ld;
     int64_t n, rows, cols;
     void* out;
-    int32_t out_type, accumulate;
+    int32_t out_type, accumulate, exact;
     int64_t out_ld;
 };
 // Of the products' workspace; copy: the weight's rows have to be copied;

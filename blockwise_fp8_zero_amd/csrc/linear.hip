@@ -336,8 +336,9 @@ Small small_tiles(int64_t k, int64_t m, int64_t n, bool exact) {
     return best;
 }
 
-// Results that would show what the E4M3 instructions cut off (codes_gemm.h).
-bool exact_products(int type) { return type != kBF16; }
+// Results that would show what the E4M3 instructions cut off (codes_gemm.h), or whose
+// caller asks for exact products.
+bool exact_products(int type, int asked) { return type != kBF16 || asked; }
 
 // How a product is cut: tiles of m x n with so many waves each, splits of k, columns
 // of whole tiles (the others are half as wide).
@@ -391,7 +392,7 @@ int launch_product(ProductArgs& g, const StoreEpilogue& e, const Shape& shape, h
 
 template <bool kAKR, bool kBKR>
 int product(ProductArgs& g, const LinearArgs& a, int64_t m, int64_t n, float* sums, hipStream_t stream) {
-    const bool exact = exact_products(a.out_type);
+    const bool exact = exact_products(a.out_type, a.exact);
     const int size = dtype_size(a.out_type);
     StoreEpilogue e{a.out, a.out_ld, 0, m, n, a.out_type, a.accumulate, 0};
     e.vec = ((reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.out_ld * size)) & 15u) == 0;
@@ -446,12 +447,12 @@ int few_rows(const ProductArgs& g, const RowInputs& x, const StoreEpilogue& e, h
 // result 2 to 5% (1 token on 4096 x 4096: 5.1 us instead of 4.9, 16 on 28672 x 8192:
 // 48.4 instead of 48.0).  Beyond them they would cost it 10 to 40% (64 on 11008 x
 // 4096: 21 us instead of 17, 33 on 28672 x 8192: 102 instead of 67).
-bool exact_few(int type, int64_t n) { return n <= 16 || exact_products(type); }
+bool exact_few(int type, int asked, int64_t n) { return n <= 16 || exact_products(type, asked); }
 
-int few_tokens(const ProductArgs& g, const RowInputs* x, const StoreEpilogue& e, hipStream_t stream) {
+int few_tokens(const ProductArgs& g, const RowInputs* x, const StoreEpilogue& e, int asked, hipStream_t stream) {
     if (x) return few_rows<1, true, true>(g, *x, e, stream);
     const RowInputs none{};
-    const bool exact = exact_few(e.type, e.n);
+    const bool exact = exact_few(e.type, asked, e.n);
     if (e.n <= 16) return few_rows<1, true, false>(g, none, e, stream);
     if (e.n <= 32) return exact ? few_rows<2, true, false>(g, none, e, stream) : few_rows<2, false, false>(g, none, e, stream);
     return exact ? few_rows<4, true, false>(g, none, e, stream) : few_rows<4, false, false>(g, none, e, stream);
@@ -532,7 +533,7 @@ int launch_linear(const LinearArgs& given, void* work, void* stream) {
     token_scales(g, a.x);
     if (a.n > kFewTokensMost) return product<false, false>(g, a, a.rows, a.n, static_cast<float*>(work), s);
     const RowInputs x{a.values, a.values_type, a.values_ld, (int32_t)a.n, (int32_t)a.cols, (int32_t)(wide * kTileDim), (int32_t)wide};
-    return few_tokens(g, inside ? &x : nullptr, e, s);
+    return few_tokens(g, inside ? &x : nullptr, e, a.exact, s);
 }
 
 int launch_linear_grad_input(const LinearArgs& a, void* work, void* stream) {
@@ -575,16 +576,17 @@ int launch_linear_grad_weight(const LinearArgs& a, void* work, void* stream) {
 extern "C" int bfz_linear_shape(int32_t product, int64_t n, int64_t rows, int64_t cols, int32_t out_dtype, int64_t* shape) {
     using namespace bfz;
     if (!shape || product < 0 || product > 2 || n < 1 || rows < 1 || cols < 1 || n > (int64_t(1) << 24) || rows > (int64_t(1) << 20) ||
-        cols > (int64_t(1) << 20) || (out_dtype != kF32 && out_dtype != kBF16 && out_dtype != kF16))
+        cols > (int64_t(1) << 20) || (out_dtype != kF32 && out_dtype != kBF16 && out_dtype != kF16 && out_dtype != BFZ_BF16_EXACT))
         return fail(BFZ_EINVAL, "bfz_linear_shape: null pointer, bad sizes or types");
     const int64_t m = product == 0 ? rows : cols, across = product == 2 ? rows : n, k = product == 0 ? cols : product == 1 ? rows : n;
+    const int asked = out_dtype == BFZ_BF16_EXACT, type = asked ? kBF16 : out_dtype;
     int64_t out[6];
     if (product == 0 && n <= kFewTokensMost) {
         const int32_t tn = n <= 16 ? 1 : n <= 32 ? 2 : 4;
-        const int64_t few[6] = {16 * few_tiles(m, tn), 16 * tn, kFewKWaves, 1, n, exact_few(out_dtype, n)};
+        const int64_t few[6] = {16 * few_tiles(m, tn), 16 * tn, kFewKWaves, 1, n, exact_few(type, asked, n)};
         std::copy(few, few + 6, out);
     } else {
-        const bool exact = exact_products(out_dtype);
+        const bool exact = exact_products(type, asked);
         const Shape s = shape_of(k, m, across, exact);
         const int64_t cut[6] = {s.tile_m, s.tile_n, s.waves, s.splits, std::min<int64_t>(across, s.whole * s.tile_n), exact};
         std::copy(cut, cut + 6, out);

@@ -14,7 +14,7 @@ Without gradients, bfz.linear(x, weight, w_grid, y, work) quantizes x itself.
 """
 from . import _check, lib
 from . import _tensors
-from ._tensors import E4M3, home_device, matrix, raw_stream, tile_grid, work_pointer
+from ._tensors import BF16, BF16_EXACT, E4M3, home_device, matrix, raw_stream, tile_grid, work_pointer
 
 
 def quantize_buffers(n, dim, tiles=False, device="cuda"):
@@ -102,18 +102,19 @@ def _weight(weight, grid, home):
     return w, ld, tile_grid(grid, home, code, rows, cols), rows, cols, int(((w | ld) & 15) != 0)
 
 
-def _result(t, name, home, shape):
+def _result(t, name, home, shape, exact):
     p, code, rows, cols, ld = matrix(t, name, home)
     if (rows, cols) != shape:
         raise ValueError(f"{name}: is {(rows, cols)}, need {shape}")
-    return p, code, ld
+    return p, BF16_EXACT if exact and code == BF16 else code, ld
 
 
-def linear(x, weight, grid, out, work, scales=None, tiles=False, stream=None):
+def linear(x, weight, grid, out, work, scales=None, tiles=False, stream=None, exact=False):
     """out = X W^T.  x: (n, cols) E4M3 codes with the scales that quantize gave
     them (tiles: as there), or float32, bfloat16 or float16 values, which are
     quantized by rows; weight: (rows, cols) E4M3 codes with their tile scales
-    `grid`; out: (n, rows) float32, bfloat16 or float16."""
+    `grid`; out: (n, rows) float32, bfloat16 or float16.  exact: a bfloat16 result
+    of more than 16 tokens of exact products too, at half the rate (others are)."""
     home = home_device()
     p, code, n, dim, ld = matrix(x, "x", home, codes=True)
     w, wld, g, rows, cols, copy = _weight(weight, grid, home)
@@ -129,34 +130,35 @@ def linear(x, weight, grid, out, work, scales=None, tiles=False, stream=None):
         s, sld = None, 0
     if dim != cols:
         raise ValueError(f"x is {(n, dim)}, weight {(rows, cols)}")
-    o, ocode, old = _result(out, "out", home, (n, rows))
+    o, ocode, old = _result(out, "out", home, (n, rows), exact)
     rc = lib().bfz_linear(p, code, ld, s, sld, int(bool(tiles)), n, w, wld, g, rows, cols, o, ocode, old,
                           work_pointer(work, home, _work_bytes(n, rows, cols, code, copy)), raw_stream(stream, home))
     if rc:
         _check(rc)
 
 
-def linear_grad_input(dout, weight, grid, dx, work, scales, tiles=False, accumulate=False, stream=None):
+def linear_grad_input(dout, weight, grid, dx, work, scales, tiles=False, accumulate=False, stream=None, exact=False):
     """dx = dOut W, or with accumulate added to dx.  dout: (n, rows) E4M3 codes
     with the scales that quantize gave them; dx: (n, cols) float32, bfloat16 or
-    float16."""
+    float16; exact: as for linear, whatever n is."""
     home = home_device()
     w, wld, g, rows, cols, copy = _weight(weight, grid, home)
     p, n, dim, ld = _rows(dout, "dout", home)
     if dim != rows:
         raise ValueError(f"dout is {(n, dim)}, weight {(rows, cols)}")
     s, sld = _scales(scales, "scales", home, n, dim, tiles)
-    o, ocode, old = _result(dx, "dx", home, (n, cols))
+    o, ocode, old = _result(dx, "dx", home, (n, cols), exact)
     rc = lib().bfz_linear_grad_input(p, ld, s, sld, int(bool(tiles)), n, w, wld, g, rows, cols, o, ocode, old, int(bool(accumulate)),
                                      work_pointer(work, home, _work_bytes(n, rows, cols, E4M3, copy)), raw_stream(stream, home))
     if rc:
         _check(rc)
 
 
-def linear_grad_weight(dout, dout_grid, x, x_grid, dweight, work, accumulate=False, stream=None):
+def linear_grad_weight(dout, dout_grid, x, x_grid, dweight, work, accumulate=False, stream=None, exact=False):
     """dweight = dOut^T X, or with accumulate added to dweight.  dout: (n, rows)
     and x: (n, cols), E4M3 codes with their tile scales (quantize, tiles=True);
-    dweight: (rows, cols) float32, bfloat16 or float16."""
+    dweight: (rows, cols) float32, bfloat16 or float16; exact: as for linear,
+    whatever n is."""
     home = home_device()
     p, n, rows, ld = _rows(dout, "dout", home)
     q, count, cols, qld = _rows(x, "x", home)
@@ -164,7 +166,7 @@ def linear_grad_weight(dout, dout_grid, x, x_grid, dweight, work, accumulate=Fal
         raise ValueError(f"dout is {(n, rows)}, x {(count, cols)}")
     s, sld = _scales(dout_grid, "dout_grid", home, n, rows, True)
     t, tld = _scales(x_grid, "x_grid", home, n, cols, True)
-    o, ocode, old = _result(dweight, "dweight", home, (rows, cols))
+    o, ocode, old = _result(dweight, "dweight", home, (rows, cols), exact)
     rc = lib().bfz_linear_grad_weight(p, ld, s, sld, q, qld, t, tld, n, rows, cols, o, ocode, old, int(bool(accumulate)),
                                       work_pointer(work, home, _work_bytes(n, rows, cols, E4M3, 0)), raw_stream(stream, home))
     if rc:

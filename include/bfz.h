@@ -394,6 +394,7 @@ int bfz_fold_adamw_fp8_step_unpack_t_clip(const bfz_plan* plan, const float* con
 #define BFZ_F16 2
 #define BFZ_E4M3 3 /* codes, with a grid of one float scale per 128x128 tile */
 #define BFZ_F32_ROUNDED 4 /* bfz_vocab_loss_grad's dweight only, see there */
+#define BFZ_BF16_EXACT 5  /* results of bfz_linear and its gradients only, see there */
 
 /* n elements back to back at any element alignment. */
 typedef struct {
@@ -584,7 +585,8 @@ int bfz_quantize(const void* x, int32_t x_dtype, int64_t x_ld, int64_t n, int64_
  * products of other BFZ_BF16 results are those of the E4M3 matrix instructions, at
  * twice the rate: groups of 8 are aligned to their largest and cut off 13 bits below
  * its exponent, towards zero, some 5e-5 of a result whose rounding is 1.7e-3.  Where
- * large products cancel that shows; a caller to whom it matters takes BFZ_F32 results.
+ * large products cancel that shows; BFZ_BF16_EXACT asks for BFZ_BF16 results of exact
+ * products whatever n is.
  * x: [n, cols], E4M3 codes as bfz_quantize leaves them (zeros up to the next
  * multiple of 16 columns) with their scales in its row (tiles == 0) or tile
  * form; or BFZ_F32, BFZ_BF16 or BFZ_F16 values with scales NULL and tiles 0,
@@ -592,8 +594,8 @@ int bfz_quantize(const void* x, int32_t x_dtype, int64_t x_ld, int64_t n, int64_
  * their row-major scale grid [ceil(rows/128), ceil(cols/128)], as the step
  * writes both; one expert of a (E, rows, cols) weight is one call.  Rows that
  * start on 16-byte boundaries and are a multiple of 16 wide are read in place,
- * others first copied into the workspace.  out: [n, rows], BFZ_F32, BFZ_BF16 or
- * BFZ_F16, rows out_ld apart, any element alignment.
+ * others first copied into the workspace.  out: [n, rows], BFZ_F32, BFZ_BF16 (or
+ * BFZ_BF16_EXACT) or BFZ_F16, rows out_ld apart, any element alignment.
  * work: bfz_linear_work_bytes(n, rows, cols, x_dtype, copy) of device memory,
  * 256-byte aligned, not shared by calls that may run at the same time; copy != 0
  * where the weight's pointer or weight_ld is not a multiple of 16.  It serves
@@ -617,7 +619,7 @@ int bfz_linear(const void* x, int32_t x_dtype, int64_t x_ld, const float* scales
  * The first takes dout's scales in either form, the second both operands' in
  * the tile form, whose scales hold whichever way a tile is read: the codes that
  * the forward product read serve here, and no transposed copy is made.  BFZ_BF16
- * gradients take the E4M3 instructions whatever n is.
+ * gradients take the E4M3 instructions whatever n is, BFZ_BF16_EXACT ones do not.
  * accumulate adds in binary32 before the one rounding.  dweight with n = 0 is
  * zero.  Other arguments, limits and errors as above.
  */

@@ -1,5 +1,6 @@
 """Results that are made of exact products: float16 ones of every size, as float32
-ones, and any of up to 16 tokens, where the weight's bytes decide the time.
+ones, any of up to 16 tokens, where the weight's bytes decide the time, and bfloat16
+ones whose caller asks for them.
 
 The operands are such that nothing but the last rounding may be off.  In every 8
 columns of the sum two products are 2^15 and -2^15, all others multiples of 1/64
@@ -72,24 +73,34 @@ def test_few_values(n):
     assert torch.equal(out, want.float().to(BF16))
 
 
+@pytest.mark.parametrize("n,rows,cols", [(20, 300, 640), (64, 12400, 512)])
+def test_few_tokens_when_asked(n, rows, cols):
+    x, w, want = operands(n, rows, cols)
+    out = torch.full((n, rows), float("nan"), dtype=BF16, device="cuda")
+    bfz.linear(x, w, ones(blocks(rows), blocks(cols)), out, bfz.linear_workspace(n, w), scales=ones(blocks(cols), n), exact=True)
+    assert torch.equal(out, want.float().to(BF16))
+
+
 @pytest.mark.parametrize("n,rows,cols", [(65, 300, 1001), (300, 513, 640), (1030, 1300, 912), (3590, 1700, 3600)])
-def test_half_results(n, rows, cols):
-    """float16 results of all three products."""
-    _say("exact, f16", n, rows, cols)
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_all_products(n, rows, cols, dtype):
+    """bfloat16 results with `exact`, which changes nothing for others."""
+    _say("exact", n, rows, cols, dtype)
+    exact = dtype == BF16
     x, w, want = operands(n, rows, cols)
     work = bfz.linear_workspace(n, w)
     grid = ones(blocks(rows), blocks(cols))
-    out, dx, dw = (torch.full(s, float("nan"), dtype=F16, device="cuda") for s in ((n, rows), (n, cols), (rows, cols)))
-    bfz.linear(x, w, grid, out, work, scales=ones(blocks(n), blocks(cols)), tiles=True)
-    assert torch.equal(out, want.float().to(F16))
+    out, dx, dw = (torch.full(s, float("nan"), dtype=dtype, device="cuda") for s in ((n, rows), (n, cols), (rows, cols)))
+    bfz.linear(x, w, grid, out, work, scales=ones(blocks(n), blocks(cols)), tiles=True, exact=exact)
+    assert torch.equal(out, want.float().to(dtype))
     # contracted over rows: both operands' codes come as their transposes
     d, wt, want = operands(n, cols, rows)
-    bfz.linear_grad_input(d, wt.t().contiguous(), grid, dx, work, scales=ones(blocks(n), blocks(rows)), tiles=True)
-    assert torch.equal(dx, want.float().to(F16))
+    bfz.linear_grad_input(d, wt.t().contiguous(), grid, dx, work, scales=ones(blocks(n), blocks(rows)), tiles=True, exact=exact)
+    assert torch.equal(dx, want.float().to(dtype))
     dt, xt, want = operands(rows, cols, n)
     d, _ = bfz.quantize_buffers(n, rows)
     x, _ = bfz.quantize_buffers(n, cols)
     d.copy_(dt.t())
     x.copy_(xt.t())
-    bfz.linear_grad_weight(d, ones(blocks(n), blocks(rows)), x, ones(blocks(n), blocks(cols)), dw, work)
-    assert torch.equal(dw, want.float().to(F16))
+    bfz.linear_grad_weight(d, ones(blocks(n), blocks(rows)), x, ones(blocks(n), blocks(cols)), dw, work, exact=exact)
+    assert torch.equal(dw, want.float().to(dtype))
