@@ -7,12 +7,11 @@
 // scaling one fused operation for each result: while a row of tiles is
 // multiplied, the sums of the row before are scaled and added.
 //
-// A workgroup owns a kBM x kBN tile of D and walks k a block at a time.  A
-// block's operands go from memory straight into LDS (16 bytes a lane), into one
-// of two buffers.  When a wave has read the last of a block it meets the others;
-// the loads of the block after next then go into the buffer just read, and the
-// last row of tiles is multiplied while the next block's first fragments are
-// read.
+// A workgroup owns a tile of D and walks k a block at a time.  A block's operands go
+// from memory straight into LDS (16 bytes a lane), into one of two to four buffers.
+// When a wave has read the last of a block it meets the others; the loads of the
+// block that many ahead then go into the buffer just read, and the last row of tiles
+// is multiplied while the next block's first fragments are read.
 //
 // Operands come in two layouts, so that no operand is ever transposed in memory:
 // KC, k contiguous, and KR, m or n contiguous (rows of k), read with the LDS
@@ -22,8 +21,9 @@
 // their 16-byte pieces are permuted by an XOR with the row, chosen so that the
 // lanes that read together touch all banks.
 //
-// 8192 x 11008 x 4096 runs at 2.25 to 2.46 PFLOP/s, the matrix cores busy some 55% of
-// the cycles at a clock that their load lowers to 1.9 GHz.  Without the scaling's
+// 8192 x 11008 x 4096 runs at 2.27 to 2.48 PFLOP/s, the matrix cores busy 50 to 58% of
+// the cycles (46% with bf16 instructions) at a clock that their load lowers to 1.8 to
+// 1.9 GHz.  Without the scaling's
 // vector instructions it would be 8% faster, without the loads from memory 20%.  What
 // is left is the wait where all eight waves meet.  Fixing the order of reads and
 // loads gave 7%, spreading the loads over half of a block's rows of tiles 3%, half

@@ -15,10 +15,11 @@
 // registers.  Those leave as one partial row a workgroup, which a second kernel
 // adds: sums in an order that the sizes fix.
 //
-// 32768 x 4096 bf16: 100 us (5.4 TB/s), the gradient 153 (5.3, a copy reaches 4.8);
-// 3001 x 1001 floats 7.2 and 15.5 us, one row 3.3 of a 7 us call.  16384 x 1024: 15 and 24.
-// Taking the first mean's error off costs 1% of the largest, 3% of 16384 x 1024.
-// Beyond 16384 columns a thread's 32 elements spill (2000 x 20000: 131 and 427 us, 2000 x 20001: 128 and 447).
+// 32768 x 4096 bf16: 100 us (5.3 TB/s), the gradient 152 (5.3, a copy reaches 4.8);
+// 3001 x 1001 floats 7.3 and 15.7 us, one row 3.4 of a 7.3 us call.  16384 x 1024: 15
+// and 24.  Taking the first mean's error off costs 1% of the largest, 3% of 16384 x
+// 1024.  Beyond 16384 columns a thread's 32 elements spill, in the gradient most
+// (2000 x 20000: 131 and 436 us, 2000 x 20001: 128 and 449).  (Back-to-back calls.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -434,8 +435,8 @@ int with_width(bool wide, F&& f) {
     return wide ? f(std::true_type{}) : f(std::false_type{});
 }
 
-// Workgroups of the gradient: one a CU, or one for every two rows of each
-// thread group where there are fewer.
+// Workgroups of the gradient: one a CU, or one for every row of each thread group
+// where there are fewer.
 constexpr int64_t kGradWgs = 256;
 int64_t grad_wgs(int64_t n, int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(kGradWgs, (n + rows - 1) / rows)); }
 

@@ -8,11 +8,13 @@
 //
 // Products, bound by the matrix cores (codes_gemm.h): forward and dx read the weight
 // and the codes as they lie, k along rows or across them; dW contracts over tokens
-// and reads both operands across.  8192 x 11008 x 4096: forward 328 us (2.25
-// PFLOP/s), dx 300 (2.46), dW in bf16 320 (2.3), in f32, by bf16 instructions, 650
-// (1.14); the library's product of two E4M3 matrices with one scale each runs at
-// 2.12 there.  Up to 64 tokens, bound by reading the weight: 4096 x 4096, 1 token 5.7
-// us (3.0 TB/s; 3.6 of it the bytes), 11008 x 4096, 64 tokens 17 us.
+// and reads both operands across.  8192 x 11008 x 4096: forward 325 us (2.27
+// PFLOP/s), dx 298 (2.48), dW in bf16 315 (2.34), in f32, by bf16 instructions, 641
+// (1.15); the library's products of two E4M3 matrices with one scale each run at 2.4
+// there (3.2 at 8192 in each direction), those of bf16 ones at 1.1 (1.6).  Up to 64
+// tokens, bound by reading the weight: 4096 x 4096, 1 token 5.1 us (3.3 TB/s; 3.6 of
+// it the bytes), 11008 x 4096, 64 tokens 17 us.  (Back-to-back calls, the first 30
+// ms of them: under longer load the card's clock falls.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
